@@ -68,6 +68,13 @@ class KvPages(ctypes.Structure):
         self._keep = (k_pool, v_pool, page_table)
 
 
+class Heads(ctypes.Structure):
+    """dflash_heads: the attention layout that the target-side calls work on."""
+    _fields_ = [("n_layers", ctypes.c_int), ("n_q_heads", ctypes.c_int), ("n_kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("rms_eps", ctypes.c_float), ("dtype", ctypes.c_int)]
+
+
+_LL = ctypes.c_longlong
 _SIGS = {
     "dflash_abi_version": (_I, []),
     "dflash_status_string": (ctypes.c_char_p, [_I]),
@@ -110,6 +117,17 @@ _SIGS = {
                                        _P, _SZ, ctypes.POINTER(Trace), _P]),
     "dflash_verify_sample": (_I, [ctypes.POINTER(Config), _P, _I, _P, _P, _I, ctypes.c_float,
                                   ctypes.c_uint64, _P, _P, _P, _P, _SZ, ctypes.POINTER(Trace), _P]),
+    "dflash_check_heads": (_I, [ctypes.POINTER(Heads)]),
+    "dflash_qk_norm_rope": (_I, [ctypes.POINTER(Heads), _I, _P, _LL, _P, _LL, _P, _P, _P, _P, _P, _I, _I, _P, _LL,
+                                 _P, _LL, _P, ctypes.POINTER(Trace), _P]),
+    "dflash_kv_append_paged": (_I, [ctypes.POINTER(Heads), _I, _P, _LL, _P, _LL, _P, _LL, _P, _P, _P, _P, _I, _P, _P,
+                                    _I, _I, _I, ctypes.POINTER(KvPages), _P, _LL, _P, ctypes.POINTER(Trace), _P]),
+    "dflash_attention_chunk_bytes": (_SZ, [ctypes.POINTER(Heads)]),
+    "dflash_attention_chunk_paged": (_I, [ctypes.POINTER(Heads), _P, _LL, _P, _P, _I, _I, _I, _I, _I,
+                                          ctypes.POINTER(KvPages), _I, ctypes.c_float, _P, _LL, _P, _P, _SZ,
+                                          ctypes.POINTER(Trace), _P]),
+    "dflash_verify_probs": (_I, [ctypes.POINTER(Config), _P, _I, _P, _P, _P, _P, _P, _I, _P, _P, _P, _P,
+                                 ctypes.POINTER(Trace), _P]),
 }
 
 _lib = None
@@ -405,6 +423,113 @@ def dflash_linear(x, w, y, ws: Workspace, stream=None):
     N = w.shape[0]
     _check("dflash_linear", load().dflash_linear(dt, _ptr(x), _ptr(w), _ptr(y), M, N, K, ws.ptr,
                                                  ws.nbytes, _stream(stream)))
+
+
+# ---------------------------------------------------------------- target side
+def make_heads(n_layers, n_q_heads, n_kv_heads, head_dim, rms_eps=1e-6, dtype=BF16) -> Heads:
+    return Heads(n_layers, n_q_heads, n_kv_heads, head_dim, rms_eps, dtype)
+
+
+def dflash_check_heads(heads: Heads) -> int:
+    return load().dflash_check_heads(ctypes.byref(heads))
+
+
+def dflash_attention_chunk_bytes(heads: Heads) -> int:
+    return load().dflash_attention_chunk_bytes(ctypes.byref(heads))
+
+
+class ChunkWorkspace:
+    """Caller-owned scratch of dflash_attention_chunk_paged (any batch of the layout)."""
+
+    def __init__(self, heads: Heads, device="cuda"):
+        n = dflash_attention_chunk_bytes(heads)
+        if n == 0:
+            raise DFlashError("dflash_attention_chunk_bytes", dflash_check_heads(heads))
+        self.buf = torch.empty(n, dtype=torch.uint8, device=device)
+        self.nbytes = n
+        self.ptr = self.buf.data_ptr()
+
+
+_DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def _rows(t, n_heads: int, head_dim: int, dtype, fn: str):
+    """(pointer, row stride) of [T, heads, Dh] rows whose heads lie side by side."""
+    if t is None:
+        return None, 0
+    if t.shape[1] != n_heads or t.shape[2] != head_dim or (n_heads > 1 and t.stride(1) != head_dim) or t.stride(2) != 1:
+        raise DFlashError(fn, ERR_SHAPE)
+    if dtype is not None and _DTYPES.get(t.dtype) != dtype:
+        raise DFlashError(fn, ERR_DTYPE)
+    # the stride of a single row says nothing
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), n_heads * head_dim)
+
+
+def dflash_qk_norm_rope(heads: Heads, q, k, positions, rope_cos, rope_sin, q_out, k_out, dev_status, g_q=None, g_k=None,
+                        trace=None, stream=None):
+    """Per-head RMSNorm (where a gain is given) and RoPE of q [T, Hq, Dh] and
+    k [T, Hkv, Dh] (either may be None) into q_out, k_out."""
+    fn = "dflash_qk_norm_rope"
+    x = q if q is not None else k
+    if x is None:
+        raise DFlashError(fn, ERR_INVALID_ARG)
+    dt, T, hq, hk, dh = _DTYPES.get(x.dtype, -1), x.shape[0], heads.n_q_heads, heads.n_kv_heads, heads.head_dim
+    if (q is not None and (q_out is None or q_out.shape[0] < T)) or (
+            k is not None and (k_out is None or k_out.shape[0] < T or k.shape[0] != T)):
+        raise DFlashError(fn, ERR_SHAPE)
+    qp, ldq = _rows(q, hq, dh, dt, fn)
+    kp, ldk = _rows(k, hk, dh, dt, fn)
+    qo, ldqo = _rows(q_out if q is not None else None, hq, dh, heads.dtype, fn)
+    ko, ldko = _rows(k_out if k is not None else None, hk, dh, heads.dtype, fn)
+    _check(fn, load().dflash_qk_norm_rope(
+        ctypes.byref(heads), dt, qp, ldq, kp, ldk, _ptr(g_q), _ptr(g_k), _ptr(positions), _ptr(rope_cos),
+        _ptr(rope_sin), rope_cos.shape[0] if rope_cos is not None else 0, T, qo, ldqo, ko, ldko, _ptr(dev_status),
+        _tr(trace), _stream(stream)))
+
+
+def dflash_kv_append_paged(heads: Heads, q, k, v, cu_rows, ctx_len, layer, pages: KvPages, rope_cos, rope_sin, q_out,
+                           dev_status, g_q=None, g_k=None, trace=None, stream=None):
+    """Appends packed rows k, v [T, Hkv, Dh] to one layer of the paged cache
+    (K normed and rotated on the way); q [T, Hq, Dh] (or None) likewise into q_out."""
+    fn = "dflash_kv_append_paged"
+    dt, T, hq, hk, dh = _DTYPES.get(k.dtype, -1), k.shape[0], heads.n_q_heads, heads.n_kv_heads, heads.head_dim
+    if v.shape[0] != T or (q is not None and (q.shape[0] != T or q_out is None or q_out.shape[0] < T)):
+        raise DFlashError(fn, ERR_SHAPE)
+    qp, ldq = _rows(q, hq, dh, dt, fn)
+    kp, ldk = _rows(k, hk, dh, dt, fn)
+    vp, ldv = _rows(v, hk, dh, dt, fn)
+    qo, ldqo = _rows(q_out if q is not None else None, hq, dh, heads.dtype, fn)
+    _check(fn, load().dflash_kv_append_paged(
+        ctypes.byref(heads), dt, qp, ldq, kp, ldk, vp, ldv, _ptr(g_q), _ptr(g_k), _ptr(rope_cos), _ptr(rope_sin),
+        rope_cos.shape[0] if rope_cos is not None else 0, _ptr(cu_rows), _ptr(ctx_len), ctx_len.shape[0], T, int(layer),
+        ctypes.byref(pages), qo, ldqo, _ptr(dev_status), _tr(trace), _stream(stream)))
+
+
+def dflash_attention_chunk_paged(heads: Heads, q, cu_rows, ctx_len, max_rows, max_ctx_hint, layer, pages: KvPages, out,
+                                 dev_status, ws: ChunkWorkspace, causal=True, scale=0.0, trace=None, stream=None):
+    """Attention of a ragged batch of chunks q [T, Hq, Dh] over the paged cache
+    that already holds the chunks' own keys and values."""
+    fn = "dflash_attention_chunk_paged"
+    T, hq, dh = q.shape[0], heads.n_q_heads, heads.head_dim
+    if out.shape[0] < T:
+        raise DFlashError(fn, ERR_SHAPE)
+    qp, ldq = _rows(q, hq, dh, heads.dtype, fn)
+    op, ldo = _rows(out, hq, dh, heads.dtype, fn)
+    _check(fn, load().dflash_attention_chunk_paged(
+        ctypes.byref(heads), qp, ldq, _ptr(cu_rows), _ptr(ctx_len), ctx_len.shape[0], T, int(max_rows),
+        int(max_ctx_hint), int(layer), ctypes.byref(pages), 1 if causal else 0, float(scale), op, ldo,
+        _ptr(dev_status), ws.ptr, ws.nbytes, _tr(trace), _stream(stream)))
+
+
+def dflash_verify_probs(cfg, target_probs, draft_probs, draft, u_accept, u_draw, tau, committed, next_anchor,
+                        dev_status, gamma_b=None, trace=None, stream=None):
+    """Verification against given probabilities from given uniforms; draft_probs
+    None for greedy drafts."""
+    dt = BF16 if target_probs.dtype == torch.bfloat16 else F32
+    _check("dflash_verify_probs", load().dflash_verify_probs(
+        ctypes.byref(cfg), _ptr(target_probs), dt, _ptr(draft_probs), _ptr(draft), _ptr(gamma_b), _ptr(u_accept),
+        _ptr(u_draw), target_probs.shape[0], _ptr(tau), _ptr(committed), _ptr(next_anchor), _ptr(dev_status),
+        _tr(trace), _stream(stream)))
 
 
 class TraceRecorder:

@@ -1,0 +1,287 @@
+// Attention of a ragged batch of chunks of new tokens over a paged KV cache:
+// row i of sequence b's chunk (position ctx_len[b] + i) attends to keys
+// 0 .. ctx_len[b] + i (causal) or to all ctx_len[b] + n_b keys.
+//
+// The rows of one KV head's G query heads are packed as r = i * G + g, so
+// that a key and value tile is read once for all of them, whether the chunk
+// has one token or thousands. This file holds the CUDA-core kernel of fp32
+// models and the merge of split results; the tcgen05 kernel of bf16 models
+// shares the packing and the partial format.
+#include "chunk.cuh"
+
+namespace dfl {
+namespace {
+
+constexpr float kLog2eC = 1.4426950408889634f;
+
+// ------------------------------------------------------------------ fp32
+// One CTA per (unit of kSimtRows packed rows, KV head, split). Keys in tiles
+// of kSimtKeys through shared memory; thread (ty, tx) of 16 x 16 holds a 4 x 4
+// piece of the score tile and rows 4 ty.. x columns tx + 16 c of the output.
+constexpr int kSimtRows = 64, kSimtKeys = 64, kSimtThreads = 256;
+
+template <typename T>
+__device__ __forceinline__ float to_f(T x);
+template <>
+__device__ __forceinline__ float to_f<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+template <int DH>
+constexpr size_t simt_smem() {
+  return sizeof(float) * (static_cast<size_t>(kSimtRows + 2 * kSimtKeys) * (DH + 4) + kSimtRows * (kSimtKeys + 4));
+}
+
+template <typename T, int DH>
+__global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkArgs p, int splits) {
+  extern __shared__ __align__(16) float sm[];
+  constexpr int LD = DH + 4, LP = kSimtKeys + 4, DC = DH / 16;
+  float* sq = sm;
+  float* sk = sq + kSimtRows * LD;
+  float* sv = sk + kSimtKeys * LD;
+  float* sp = sv + kSimtKeys * LD;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int G = p.n_q_heads / p.n_kv_heads, tok = kSimtRows / G;
+  const int kvh = blockIdx.y, sp_i = blockIdx.z;
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  ChunkUnit u;
+  const bool have = find_unit(p, tok, static_cast<int>(blockIdx.x), threadIdx.x & 31, u);   // every warp alike
+  const int unit = blockIdx.x * p.n_kv_heads + kvh;
+  if (splits > 1 && sp_i == 0 && threadIdx.x == 0) {
+    int* d = p.desc + unit * kChunkDescInts;
+    d[0] = have ? splits : 0;
+    d[1] = have ? u.row0 + u.tok0 : 0;
+    d[2] = have ? min(tok, u.n - u.tok0) : 0;
+    d[3] = kvh;
+    d[4] = unit * splits;
+    d[5] = unit * splits + 1;
+    d[6] = 1;
+  }
+  if (!have) return;
+  if (threadIdx.x == 0) check_capacity(p, u);
+  const int n_tok = min(tok, u.n - u.tok0), rows = n_tok * G;
+  const int keys = unit_keys(p, u, n_tok);
+  // this split's keys: whole tiles
+  const int tiles = (keys + kSimtKeys - 1) / kSimtKeys;
+  const int t0 = static_cast<int>(static_cast<long long>(tiles) * sp_i / splits);
+  const int t1 = static_cast<int>(static_cast<long long>(tiles) * (sp_i + 1) / splits);
+  const T* q = static_cast<const T*>(p.q);
+  for (int i = threadIdx.x; i < kSimtRows * DH; i += kSimtThreads) {
+    const int r = i / DH, d = i % DH;
+    sq[r * LD + d] = r < rows ? to_f(q[(u.row0 + u.tok0 + r / G) * p.ldq + (kvh * G + r % G) * DH + d]) : 0.f;
+  }
+  int lim[4];      // keys that row 4 ty + i sees
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 4 * ty + i;
+    lim[i] = r < rows ? row_keys(p, u, u.tok0 + r / G) : 0;
+  }
+  float m[4], l[4], o[4][DC];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int c = 0; c < DC; ++c) o[i][c] = 0.f;
+  }
+  const float scale = p.scale * kLog2eC;
+  for (int t = t0; t < t1; ++t) {
+    const int k0 = t * kSimtKeys;
+    __syncthreads();
+    // a tile lies inside one page
+    const int page = page_of(p, u.b, k0);
+    const size_t base = ((static_cast<size_t>(p.layer) * p.pages.n_pages + page) * p.n_kv_heads + kvh) *
+                            static_cast<size_t>(kPageKeys) + k0 % kPageKeys;
+    for (int i = threadIdx.x; i < kSimtKeys * DH; i += kSimtThreads) {
+      const int r = i / DH, d = i % DH;
+      const bool in = k0 + r < keys;   // rows behind the last key may hold anything
+      sk[r * LD + d] = in ? to_f(static_cast<const T*>(p.k_pool)[(base + r) * DH + d]) : 0.f;
+      sv[r * LD + d] = in ? to_f(static_cast<const T*>(p.v_pool)[(base + r) * DH + d]) : 0.f;
+    }
+    __syncthreads();
+    float s[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+    for (int d = 0; d < DH; d += 4) {
+      float4 a[4], b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(&sq[(4 * ty + i) * LD + d]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(&sk[(tx + 16 * j) * LD + d]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          s[i][j] += a[i].x * b[j].x + a[i].y * b[j].y + a[i].z * b[j].z + a[i].w * b[j].w;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = k0 + tx + 16 * j < lim[i] ? s[i][j] * scale : -INFINITY;
+        mx = fmaxf(mx, s[i][j]);
+      }
+#pragma unroll
+      for (int w = 8; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+      const float mn = fmaxf(m[i], mx);
+      const float ref = mn == -INFINITY ? 0.f : mn;   // nothing seen yet: every term is 0
+      const float al = exp2f(m[i] - ref);
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float e = exp2f(s[i][j] - ref);
+        sum += e;
+        sp[(4 * ty + i) * LP + tx + 16 * j] = e;
+      }
+#pragma unroll
+      for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+      l[i] = l[i] * al + sum;
+      m[i] = mn;
+#pragma unroll
+      for (int c = 0; c < DC; ++c) o[i][c] *= al;
+    }
+    __syncwarp();   // a warp's rows of sp are its own
+#pragma unroll 4
+    for (int j = 0; j < kSimtKeys; ++j) {
+      float pr[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pr[i] = sp[(4 * ty + i) * LP + j];
+#pragma unroll
+      for (int c = 0; c < DC; ++c) {
+        const float v = sv[j * LD + tx + 16 * c];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i][c] += pr[i] * v;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 4 * ty + i;
+    if (r >= rows) continue;
+    if (splits == 1) {
+      const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+      T* y = static_cast<T*>(p.out) + (u.row0 + u.tok0 + r / G) * p.ldo + (kvh * G + r % G) * DH;
+#pragma unroll
+      for (int c = 0; c < DC; ++c) y[tx + 16 * c] = from_f32<T>(o[i][c] * inv);
+    } else {
+      float* slot = p.partials + static_cast<size_t>(unit * splits + sp_i) * chunk_slot_floats(DH);
+#pragma unroll
+      for (int c = 0; c < DC; ++c) slot[static_cast<size_t>(r) * DH + tx + 16 * c] = o[i][c];
+      if (tx == 0)
+        reinterpret_cast<float2*>(slot + static_cast<size_t>(kChunkRows) * DH)[r] = make_float2(m[i], l[i]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ merge
+// Joins the partial rows of split units: CTA (unit, x) takes packed rows
+// 4x .. 4x+3, a warp per row. The weights 2^(m_s - M) and the sums are taken
+// in ascending split order, so a result does not depend on timing.
+template <typename T, int DH>
+__global__ void __launch_bounds__(128) chunk_merge_kernel(const ChunkArgs p) {
+  constexpr int DPT = DH / 32;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int* d = p.desc + blockIdx.x * kChunkDescInts;
+  const int S = d[0], G = p.n_q_heads / p.n_kv_heads;
+  const int lane = threadIdx.x & 31;
+  const int rows = d[2] * G;
+  for (int r = blockIdx.y * 4 + static_cast<int>(threadIdx.x >> 5); S > 0 && r < rows; r += gridDim.y * 4) {
+    const int first = d[4], rest = d[5], step = d[6];
+    auto slot = [&](int s) {
+      return p.partials + static_cast<size_t>(s == 0 ? first : rest + (s - 1) * step) * chunk_slot_floats(DH);
+    };
+    float M = -INFINITY;
+    for (int s = lane; s < S; s += 32)
+      M = fmaxf(M, reinterpret_cast<const float2*>(slot(s) + static_cast<size_t>(kChunkRows) * DH)[r].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float ref = M == -INFINITY ? 0.f : M;
+    float L = 0.f, acc[DPT];
+#pragma unroll
+    for (int i = 0; i < DPT; ++i) acc[i] = 0.f;
+#pragma unroll 8
+    for (int s = 0; s < S; ++s) {
+      const float* base = slot(s);
+      const float2 ml = reinterpret_cast<const float2*>(base + static_cast<size_t>(kChunkRows) * DH)[r];
+      const float w = exp2f(ml.x - ref);
+      L += ml.y * w;
+#pragma unroll
+      for (int i = 0; i < DPT; ++i) acc[i] += base[static_cast<size_t>(r) * DH + lane + 32 * i] * w;
+    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    T* y = static_cast<T*>(p.out) + (d[1] + r / G) * p.ldo + (d[3] * G + r % G) * DH;
+#pragma unroll
+    for (int i = 0; i < DPT; ++i) y[lane + 32 * i] = from_f32<T>(acc[i] * inv);
+  }
+}
+
+template <typename K, typename... Args>
+cudaError_t launch_plain(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s, bool pdl, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = pdl ? attr : nullptr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename T, int DH>
+cudaError_t launch_simt(const ChunkArgs& a, cudaStream_t s, bool pdl, Tracer& tr, double bytes, double flops) {
+  const int tok = kSimtRows / (a.n_q_heads / a.n_kv_heads);
+  // at most: every sequence's last unit holds one row
+  const long long units = (static_cast<long long>(a.T) + static_cast<long long>(a.B) * (tok - 1)) / tok;
+  const long long work = units * a.n_kv_heads;
+  int splits = 1;
+  if (work < num_sms_of_current_device()) {
+    const int tiles = (a.max_ctx + a.max_rows + kSimtKeys - 1) / kSimtKeys;
+    splits = static_cast<int>(2LL * num_sms_of_current_device() / (work > 0 ? work : 1));
+    if (splits > kChunkSlots / work) splits = static_cast<int>(kChunkSlots / work);
+    if (splits > tiles / 2) splits = tiles / 2;
+    if (splits < 1) splits = 1;
+  }
+  constexpr size_t smem = simt_smem<DH>();
+  static bool done[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (!done[dev & 63]) {
+    const cudaError_t e = cudaFuncSetAttribute(chunk_simt_kernel<T, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    done[dev & 63] = true;
+  }
+  tr.before(DFLASH_K_ATTN, bytes, flops);
+  cudaError_t e = launch_plain(chunk_simt_kernel<T, DH>,
+                               dim3(static_cast<unsigned>(units), a.n_kv_heads, splits), kSimtThreads, smem, s, pdl, a,
+                               splits);
+  tr.after();
+  if (e != cudaSuccess || splits == 1) return e;
+  tr.before(DFLASH_K_ATTN, 0.0, 0.0);
+  e = launch_plain(chunk_merge_kernel<T, DH>, dim3(static_cast<unsigned>(work), kSimtRows / 4), 128, 0, s, pdl, a);
+  tr.after();
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_attention_chunk(const ChunkArgs& a, int bf16, cudaStream_t s, bool pdl, Tracer& tr, double bytes,
+                                   double flops) {
+  if (a.head_dim != 64 && a.head_dim != 128) return cudaErrorInvalidValue;
+  if (bf16)
+    return a.head_dim == 128 ? launch_simt<__nv_bfloat16, 128>(a, s, pdl, tr, bytes, flops)
+                             : launch_simt<__nv_bfloat16, 64>(a, s, pdl, tr, bytes, flops);
+  return a.head_dim == 128 ? launch_simt<float, 128>(a, s, pdl, tr, bytes, flops)
+                           : launch_simt<float, 64>(a, s, pdl, tr, bytes, flops);
+}
+
+}  // namespace dfl

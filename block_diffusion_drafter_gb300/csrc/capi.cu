@@ -96,27 +96,6 @@ bool use_pdl() {
 
 namespace {
 
-// Records trace events around one launch.
-struct Tracer {
-  dflash_trace* t;
-  cudaStream_t s;
-  int idx = -1;
-  void before(int kind, double bytes, double flops) {
-    if (t == nullptr || t->count >= t->capacity) { idx = -1; return; }
-    idx = t->count;
-    t->kinds[idx] = kind;
-    t->bytes[idx] = bytes;
-    t->flops[idx] = flops;
-    cudaEventRecord(static_cast<cudaEvent_t>(t->events[2 * idx]), s);
-  }
-  void after() {
-    if (idx < 0) return;
-    cudaEventRecord(static_cast<cudaEvent_t>(t->events[2 * idx + 1]), s);
-    t->count = idx + 1;
-    idx = -1;
-  }
-};
-
 #define DFL_CUDA(call)                          \
   do {                                          \
     if ((call) != cudaSuccess) return DFLASH_ERR_CUDA; \
@@ -292,11 +271,6 @@ bool pages_ok(const dflash_config* c, const dflash_kv_pages* p) {
   return p != nullptr && p->k_pool != nullptr && p->v_pool != nullptr && p->page_table != nullptr &&
          p->n_pages >= 1 && p->pages_per_seq >= 1 &&
          static_cast<long long>(p->pages_per_seq) * DFLASH_PAGE_KEYS >= c->gamma + 2;
-}
-
-bool trace_ok(const dflash_trace* t) {
-  return t == nullptr || (t->events != nullptr && t->kinds != nullptr && t->bytes != nullptr &&
-                          t->flops != nullptr && t->capacity >= 0);
 }
 
 // RoPE tables cover every position a sequence of capacity ncap can reach.

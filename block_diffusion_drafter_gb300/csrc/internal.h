@@ -229,6 +229,108 @@ cudaError_t launch_copy_f32(float* dst, const float* src, size_t n, cudaStream_t
 // One CTA whose bounded wait on an mbarrier nothing arrives on runs out.
 cudaError_t launch_wait_selftest(int* dev_status, cudaStream_t s);
 
+// ---------------------------------------------------------------- target side
+// Page view of one KV pool pair (dflash_kv_pages) as the kernels take it.
+struct PageView {
+  const int32_t* table;      // [B, pages_per_seq]
+  int n_pages, pages_per_seq;
+};
+
+// Per-head RMSNorm and RoPE of query and key rows (target_rows.cu). A packed
+// row t holds heads of Dh elements side by side, rows ld* elements apart.
+struct RowArgs {
+  const void *q, *k, *v;     // NULL: that part is not asked for (v: append only)
+  long long ldq, ldk, ldv;
+  void *q_out, *k_out;       // k_out: dense form only
+  long long ldqo, ldko;
+  const void *g_q, *g_k;     // [Dh] gains, NULL: no norm
+  float eps;
+  const float *rope_cos, *rope_sin;   // NULL: no rotation
+  int rope_positions;
+  int T, n_q_heads, n_kv_heads, head_dim;
+  int in_bf16, out_bf16;
+  int* dev_status;
+  const int32_t* positions;  // dense form: [T]
+  // append form: row t of sequence b (cu_rows[b] <= t < cu_rows[b + 1]) is
+  // position ctx_len[b] + t - cu_rows[b]
+  const int32_t *cu_rows, *ctx_len;
+  int B, layer;
+  void *k_pool, *v_pool;     // [L, n_pages, Hkv, kPageKeys, Dh]
+  PageView pages;
+};
+cudaError_t launch_target_rows(const RowArgs& a, bool append, cudaStream_t s, bool pdl);
+
+// Causal (or full) attention of a ragged batch of chunks over paged caches
+// (attention_chunk.cu).
+struct ChunkArgs {
+  const void* q;             // [T, Hq, Dh], rows ldq elements apart
+  void* out;
+  long long ldq, ldo;
+  const int32_t *cu_rows, *ctx_len;
+  int B, T, max_rows, max_ctx, layer, n_layers, causal;
+  int n_q_heads, n_kv_heads, head_dim;
+  float scale;
+  const void *k_pool, *v_pool;
+  PageView pages;
+  int* dev_status;
+  float* partials;           // workspace: kChunkSlots slots of chunk_slot_floats
+  int32_t* desc;             // workspace: merge descriptors
+};
+// Partial results of split units: a slot holds up to kChunkRows unnormalised
+// O rows of Dh floats, then (running max, sum) of each row.
+constexpr int kChunkRows = 256;
+constexpr int kChunkMaxCtas = 160;
+constexpr int kChunkSlots = 2 * kChunkMaxCtas;
+constexpr int kChunkDescInts = 8;
+__host__ __device__ constexpr size_t chunk_slot_floats(int head_dim) {
+  return static_cast<size_t>(kChunkRows) * (head_dim + 2);
+}
+// Launches the attention (and, where units may be split, its merge); `trace`
+// records both.
+struct Tracer;
+cudaError_t launch_attention_chunk(const ChunkArgs& a, int bf16, cudaStream_t s, bool pdl, Tracer& tr, double bytes,
+                                   double flops);
+
+// Verification of drafts against given probabilities and random numbers
+// (verify_probs.cu).
+struct ProbsArgs {
+  const void* target;        // [B, gamma + 1, V]
+  int target_bf16;
+  const float* draft_probs;  // [B, gamma, V], NULL: each draft had probability one
+  const int32_t* draft;
+  const int32_t* gamma_b;    // NULL or [B]
+  const float *u_accept, *u_draw;
+  int B, gamma, V;
+  int32_t *tau, *committed, *next_anchor;
+  int* dev_status;
+};
+cudaError_t launch_verify_probs(const ProbsArgs& a, cudaStream_t s, bool pdl);
+
+// Records trace events around one launch.
+struct Tracer {
+  dflash_trace* t;
+  cudaStream_t s;
+  int idx = -1;
+  void before(int kind, double bytes, double flops) {
+    if (t == nullptr || t->count >= t->capacity) { idx = -1; return; }
+    idx = t->count;
+    t->kinds[idx] = kind;
+    t->bytes[idx] = bytes;
+    t->flops[idx] = flops;
+    cudaEventRecord(static_cast<cudaEvent_t>(t->events[2 * idx]), s);
+  }
+  void after() {
+    if (idx < 0) return;
+    cudaEventRecord(static_cast<cudaEvent_t>(t->events[2 * idx + 1]), s);
+    t->count = idx + 1;
+    idx = -1;
+  }
+};
+inline bool trace_ok(const dflash_trace* t) {
+  return t == nullptr || (t->events != nullptr && t->kinds != nullptr && t->bytes != nullptr &&
+                          t->flops != nullptr && t->capacity >= 0);
+}
+
 int num_sms_of_current_device();
 // DFLASH_ERR_ARCH unless the current device is sm_103 (cached per device).
 dflash_status check_arch();

@@ -460,6 +460,143 @@ dflash_status dflash_verify_accept_noalloc(const dflash_config* cfg,
                                            int32_t* committed, int32_t* next_anchor,
                                            dflash_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Target-side operators. Verifying a drafted block is a pass of the TARGET
+ * model over gamma + 1 new tokens a sequence behind a long cached context
+ * ([P1] "추론 구조": the target verifies the block); reading a prompt is the same
+ * pass over a chunk of hundreds or thousands of tokens, plain decoding the
+ * same over one. These calls are the steps of such a pass that are not matrix
+ * products, over the target's own paged cache (dflash_kv_pages), for ragged
+ * batches: the new rows of all sequences lie packed one after another, row t
+ * of sequence b at cu_rows[b] <= t < cu_rows[b + 1] (device int32 [B + 1],
+ * ascending from 0; sequences may have no rows), and stand at positions
+ * ctx_len[b], ctx_len[b] + 1, ... Rows t >= cu_rows[B] of any operand are
+ * neither read into a result nor written. None of the calls advances ctx_len
+ * (every layer of a pass runs over the same lengths).
+ *
+ * Row operands (q, k, v, out) hold a row's heads side by side ([T, heads, Dh])
+ * with rows ld elements apart, so that they may be parts of one projection's
+ * output; pointers and row strides must be multiples of 16 bytes (else
+ * DFLASH_ERR_ALIGN) and ld at least heads * Dh. Alignment is also asked of
+ * gains, RoPE tables, pools and workspace. */
+#define DFLASH_MAX_GROUP 64
+
+/* Attention layout of a model. */
+typedef struct {
+  int n_layers;       /* layers in the page pools                              */
+  int n_q_heads;      /* Hq, a multiple of Hkv, at most DFLASH_MAX_GROUP * Hkv */
+  int n_kv_heads;     /* Hkv                                                   */
+  int head_dim;       /* Dh: 64 or 128                                         */
+  float rms_eps;      /* epsilon of the per-head norms                         */
+  dflash_dtype dtype; /* outputs, gains, page pools                            */
+} dflash_heads;
+
+/* Checks a layout without touching the GPU: DFLASH_OK or the first violated
+ * constraint (DFLASH_ERR_INVALID_ARG / _SHAPE / _DTYPE). */
+dflash_status dflash_check_heads(const dflash_heads* heads);
+
+/* Per-head RMSNorm of queries and keys with the position rotation in the same
+ * pass, for every row t and head h:
+ *   y = R_p( g * x / sqrt(mean_Dh(x^2) + eps) ),   p = positions[t]
+ * R_p the rotate-half RoPE of this library (dflash_rope_tables).
+ * q: [T, Hq, Dh], k: [T, Hkv, Dh] of in_dtype (heads.dtype, or fp32 rows such as
+ *   dflash_linear writes); either may be NULL (that part is skipped).
+ * g_q, g_k: [Dh] gains of heads.dtype; NULL: no norm for that part.
+ * positions: device [T]; a position outside [0, rope_positions) sets
+ *   DFLASH_ERR_INVALID_ARG in dev_status and leaves the row's outputs as they
+ *   were. rope_cos, rope_sin: fp32 [rope_positions, Dh/2]; both NULL: no
+ *   rotation (positions may then be NULL).
+ * q_out, k_out: heads.dtype; may be q and k themselves (same types and
+ *   strides). Partly overlapping operands are not allowed. T == 0 launches
+ *   nothing. Statistics are fp32; an output is rounded once. */
+dflash_status dflash_qk_norm_rope(const dflash_heads* heads, dflash_dtype in_dtype, const void* q,
+                                  long long ld_q, const void* k, long long ld_k, const void* g_q,
+                                  const void* g_k, const int32_t* positions, const float* rope_cos,
+                                  const float* rope_sin, int rope_positions, int T, void* q_out,
+                                  long long ld_qo, void* k_out, long long ld_ko,
+                                  int32_t* dev_status, dflash_trace* trace,
+                                  dflash_stream_t stream);
+
+/* Appends a ragged batch's new keys and values to one layer of a paged cache,
+ * normed and rotated on the way, and norms and rotates the queries (in the
+ * one launch, as dflash_qk_norm_rope does):
+ *   p = ctx_len[b] + t - cu_rows[b];  page = page_table[b][p / 128]
+ *   K_pool[layer][page][g][p % 128] = R_p(norm(k[t][g])),  V_pool[...] = v[t][g]
+ *   q_out[t][h] = R_p(norm(q[t][h]))
+ * q (with q_out) may be NULL: keys and values alone. A position outside its
+ * sequence's table or with an entry outside [0, n_pages) sets
+ * DFLASH_ERR_CAPACITY, one beyond the RoPE tables DFLASH_ERR_INVALID_ARG; such
+ * a row is not written at all. Pages written must belong to one sequence.
+ * Other arguments as above. T == 0 or B == 0 launches nothing. */
+dflash_status dflash_kv_append_paged(const dflash_heads* heads, dflash_dtype in_dtype,
+                                     const void* q, long long ld_q, const void* k, long long ld_k,
+                                     const void* v, long long ld_v, const void* g_q,
+                                     const void* g_k, const float* rope_cos, const float* rope_sin,
+                                     int rope_positions, const int32_t* cu_rows,
+                                     const int32_t* ctx_len, int B, int T, int layer,
+                                     const dflash_kv_pages* pages, void* q_out, long long ld_qo,
+                                     int32_t* dev_status, dflash_trace* trace,
+                                     dflash_stream_t stream);
+
+/* Bytes of the workspace of dflash_attention_chunk_paged, whatever the batch
+ * (partial results of units of work that are split over SMs); 0 on a bad
+ * layout. It needs no initialisation; calls whose work may overlap on the GPU
+ * (other streams, graphs replayed at the same time) each need their own. */
+size_t dflash_attention_chunk_bytes(const dflash_heads* heads);
+
+/* Attention of a chunk of new tokens a sequence over the paged cache that
+ * already holds them (dflash_kv_append_paged):
+ *   out[t, h] = softmax_s(scale * q[t, h] . K_s) V_s,   KV head h / (Hq/Hkv)
+ * over keys s = 0 .. ctx_len[b] + (t - cu_rows[b]) (causal = 1) or all keys
+ * 0 .. ctx_len[b] + n_b - 1 (causal = 0, as in the drafter's bidirectional
+ * block), n_b = cu_rows[b + 1] - cu_rows[b]. A row that sees no key (a negative ctx_len) gives zeros.
+ * q, out: [T, Hq, Dh] of heads.dtype, rows ld_q / ld_o elements apart; out must
+ *   not overlap q. scale: 0 for 1/sqrt(Dh).
+ * Key and value rows below ctx_len[b] + n_b must be finite; later rows of a
+ *   page are never used and may hold anything.
+ * max_rows, max_ctx_hint: host bounds of n_b and ctx_len[b] that only size the
+ *   grid (any value >= 0 is correct, tight ones are faster); a trace record
+ *   counts K/V bytes and flops as if every sequence had max_ctx_hint keys.
+ * Keys beyond a sequence's table and entries outside [0, n_pages) set
+ * DFLASH_ERR_CAPACITY; that sequence's output is then unspecified.
+ * Results do not depend on timing or on the hints beyond rounding: splits are
+ * joined in a fixed order. T == 0 or B == 0 launches nothing. */
+dflash_status dflash_attention_chunk_paged(const dflash_heads* heads, const void* q, long long ld_q,
+                                           const int32_t* cu_rows, const int32_t* ctx_len, int B,
+                                           int T, int max_rows, int max_ctx_hint, int layer,
+                                           const dflash_kv_pages* pages, int causal, float scale,
+                                           void* out, long long ld_o, int32_t* dev_status, void* ws,
+                                           size_t ws_bytes, dflash_trace* trace,
+                                           dflash_stream_t stream);
+
+/* Verification of a drafted block against given probabilities from given
+ * random numbers, for callers that shape distributions themselves
+ * (temperature, top-k or top-p of their own) or own the random stream;
+ * dflash_verify_sample takes logits and a seed instead. [P2] lossless paragraph:
+ *   keep draft j while u_accept[b, j] * q_j(x_j) < p_j(x_j)
+ *   a = kept drafts, tau[b] = a + 1
+ *   w = max(p_a - q_a, 0) (w = p_a where that is all zero); a = gamma: w = p_gamma
+ *   y = the first v with w_0 + .. + w_v > u_draw[b] * (w_0 + .. + w_{V-1})
+ *   committed[b] = draft[b, 0..a-1] ++ [y] ++ (-1 padding); next_anchor[b] = y
+ * target_probs: device [B, gamma+1, V] of probs_dtype; draft_probs: device fp32
+ *   [B, gamma, V], or NULL for drafts taken without a draw (dflash_draft_block's
+ *   argmax): q_j is then one for x_j and zero elsewhere. Entries are
+ *   probabilities in [0, 1] (NaN and negative entries count as 0, larger ones
+ *   as 1); a row need not sum to one, but must sum to less than 4.
+ * u_accept: device fp32 [B, gamma], u_draw: device fp32 [B], uniforms in [0, 1).
+ * gamma_b: NULL, or device [B] as in dflash_verify_accept_dyn.
+ * A draft id outside [0, V) counts as rejected. A row a without any mass sets
+ *   DFLASH_ERR_INVALID_ARG in dev_status and gives y = 0.
+ * The draw is exact: weights are summed as multiples of 2^-62 in integers, so
+ *   that the token does not depend on an order of summation. No workspace; one
+ *   launch. */
+dflash_status dflash_verify_probs(const dflash_config* cfg, const void* target_probs,
+                                  dflash_dtype probs_dtype, const float* draft_probs,
+                                  const int32_t* draft, const int32_t* gamma_b,
+                                  const float* u_accept, const float* u_draw, int B, int32_t* tau,
+                                  int32_t* committed, int32_t* next_anchor, int32_t* dev_status,
+                                  dflash_trace* trace, dflash_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
