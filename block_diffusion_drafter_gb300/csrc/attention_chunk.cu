@@ -20,19 +20,12 @@ constexpr float kLog2eC = 1.4426950408889634f;
 // piece of the score tile and rows 4 ty.. x columns tx + 16 c of the output.
 constexpr int kSimtRows = 64, kSimtKeys = 64, kSimtThreads = 256;
 
-template <typename T>
-__device__ __forceinline__ float to_f(T x);
-template <>
-__device__ __forceinline__ float to_f<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
-
 template <int DH>
 constexpr size_t simt_smem() {
   return sizeof(float) * (static_cast<size_t>(kSimtRows + 2 * kSimtKeys) * (DH + 4) + kSimtRows * (kSimtKeys + 4));
 }
 
-template <typename T, int DH>
+template <int DH>
 __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkArgs p, int splits) {
   extern __shared__ __align__(16) float sm[];
   constexpr int LD = DH + 4, LP = kSimtKeys + 4, DC = DH / 16;
@@ -66,10 +59,10 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkArg
   const int tiles = (keys + kSimtKeys - 1) / kSimtKeys;
   const int t0 = static_cast<int>(static_cast<long long>(tiles) * sp_i / splits);
   const int t1 = static_cast<int>(static_cast<long long>(tiles) * (sp_i + 1) / splits);
-  const T* q = static_cast<const T*>(p.q);
+  const float* q = static_cast<const float*>(p.q);
   for (int i = threadIdx.x; i < kSimtRows * DH; i += kSimtThreads) {
     const int r = i / DH, d = i % DH;
-    sq[r * LD + d] = r < rows ? to_f(q[(u.row0 + u.tok0 + r / G) * p.ldq + (kvh * G + r % G) * DH + d]) : 0.f;
+    sq[r * LD + d] = r < rows ? q[(u.row0 + u.tok0 + r / G) * p.ldq + (kvh * G + r % G) * DH + d] : 0.f;
   }
   int lim[4];      // keys that row 4 ty + i sees
 #pragma unroll
@@ -96,8 +89,8 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkArg
     for (int i = threadIdx.x; i < kSimtKeys * DH; i += kSimtThreads) {
       const int r = i / DH, d = i % DH;
       const bool in = k0 + r < keys;   // rows behind the last key may hold anything
-      sk[r * LD + d] = in ? to_f(static_cast<const T*>(p.k_pool)[(base + r) * DH + d]) : 0.f;
-      sv[r * LD + d] = in ? to_f(static_cast<const T*>(p.v_pool)[(base + r) * DH + d]) : 0.f;
+      sk[r * LD + d] = in ? static_cast<const float*>(p.k_pool)[(base + r) * DH + d] : 0.f;
+      sv[r * LD + d] = in ? static_cast<const float*>(p.v_pool)[(base + r) * DH + d] : 0.f;
     }
     __syncthreads();
     float s[4][4];
@@ -165,9 +158,9 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkArg
     if (r >= rows) continue;
     if (splits == 1) {
       const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
-      T* y = static_cast<T*>(p.out) + (u.row0 + u.tok0 + r / G) * p.ldo + (kvh * G + r % G) * DH;
+      float* y = static_cast<float*>(p.out) + (u.row0 + u.tok0 + r / G) * p.ldo + (kvh * G + r % G) * DH;
 #pragma unroll
-      for (int c = 0; c < DC; ++c) y[tx + 16 * c] = from_f32<T>(o[i][c] * inv);
+      for (int c = 0; c < DC; ++c) y[tx + 16 * c] = o[i][c] * inv;
     } else {
       float* slot = p.partials + static_cast<size_t>(unit * splits + sp_i) * chunk_slot_floats(DH);
 #pragma unroll
@@ -236,7 +229,7 @@ cudaError_t launch_plain(K kernel, dim3 grid, int threads, size_t smem, cudaStre
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <typename T, int DH>
+template <int DH>
 cudaError_t launch_simt(const ChunkArgs& a, cudaStream_t s, bool pdl, Tracer& tr, double bytes, double flops) {
   const int tok = kSimtRows / (a.n_q_heads / a.n_kv_heads);
   // at most: every sequence's last unit holds one row
@@ -255,19 +248,19 @@ cudaError_t launch_simt(const ChunkArgs& a, cudaStream_t s, bool pdl, Tracer& tr
   int dev = 0;
   cudaGetDevice(&dev);
   if (!done[dev & 63]) {
-    const cudaError_t e = cudaFuncSetAttribute(chunk_simt_kernel<T, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(chunk_simt_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     done[dev & 63] = true;
   }
   tr.before(DFLASH_K_ATTN, bytes, flops);
-  cudaError_t e = launch_plain(chunk_simt_kernel<T, DH>,
+  cudaError_t e = launch_plain(chunk_simt_kernel<DH>,
                                dim3(static_cast<unsigned>(units), a.n_kv_heads, splits), kSimtThreads, smem, s, pdl, a,
                                splits);
   tr.after();
   if (e != cudaSuccess || splits == 1) return e;
   tr.before(DFLASH_K_ATTN, 0.0, 0.0);
-  e = launch_plain(chunk_merge_kernel<T, DH>, dim3(static_cast<unsigned>(work), kSimtRows / 4), 128, 0, s, pdl, a);
+  e = launch_plain(chunk_merge_kernel<float, DH>, dim3(static_cast<unsigned>(work), kSimtRows / 4), 128, 0, s, pdl, a);
   tr.after();
   return e;
 }
@@ -277,11 +270,22 @@ cudaError_t launch_simt(const ChunkArgs& a, cudaStream_t s, bool pdl, Tracer& tr
 cudaError_t launch_attention_chunk(const ChunkArgs& a, int bf16, cudaStream_t s, bool pdl, Tracer& tr, double bytes,
                                    double flops) {
   if (a.head_dim != 64 && a.head_dim != 128) return cudaErrorInvalidValue;
-  if (bf16)
-    return a.head_dim == 128 ? launch_simt<__nv_bfloat16, 128>(a, s, pdl, tr, bytes, flops)
-                             : launch_simt<__nv_bfloat16, 64>(a, s, pdl, tr, bytes, flops);
-  return a.head_dim == 128 ? launch_simt<float, 128>(a, s, pdl, tr, bytes, flops)
-                           : launch_simt<float, 64>(a, s, pdl, tr, bytes, flops);
+  if (!bf16)
+    return a.head_dim == 128 ? launch_simt<128>(a, s, pdl, tr, bytes, flops) : launch_simt<64>(a, s, pdl, tr, bytes, flops);
+  int ctas = 0;
+  tr.before(DFLASH_K_ATTN, bytes, flops);
+  cudaError_t e = launch_chunk_tc(a, &ctas, s, pdl);
+  tr.after();
+  if (e != cudaSuccess) return e;
+  // the merge's grid covers the rows of the hinted chunk; its CTAs walk on over further rows
+  const int G = a.n_q_heads / a.n_kv_heads;
+  const long long rows = static_cast<long long>(a.max_rows) * G;
+  const int y = static_cast<int>(rows < 4 ? 1 : rows >= kChunkRows ? kChunkRows / 4 : (rows + 3) / 4);
+  tr.before(DFLASH_K_ATTN, 0.0, 0.0);
+  e = a.head_dim == 128 ? launch_plain(chunk_merge_kernel<__nv_bfloat16, 128>, dim3(ctas, y), 128, 0, s, pdl, a)
+                        : launch_plain(chunk_merge_kernel<__nv_bfloat16, 64>, dim3(ctas, y), 128, 0, s, pdl, a);
+  tr.after();
+  return e;
 }
 
 }  // namespace dfl

@@ -1,0 +1,668 @@
+// Chunk attention over a paged KV cache on the 5th-generation tensor cores.
+//
+//   S = Q K^T (fp32 in TMEM);  P = 2^(scale S - m) (bf16);  O += P V (fp32)
+//
+// Units of work. The G query heads of a KV head are packed into the rows of
+// one tile (row = token * G + head), so a page's K and V are read once for all
+// of them. A unit is up to two 128-row tiles of one (sequence, KV head):
+// 2 * floor(128 / G) tokens. Its work is its number of 128-key pages, up to the
+// last key its last token sees. All units' pages, laid end to end, are cut into
+// equal ranges, one a CTA and one CTA an SM, whatever mix of long prompts
+// and single tokens the batch holds: a CTA walks through its range, and only
+// the first and the last unit of a range can be incomplete. Incomplete units
+// write unnormalised rows to the workspace; chunk_merge_kernel joins them in
+// key order.
+//
+// Two streams keep the tensor core busy: each has its own S / P and O columns in
+// TMEM and its own four softmax warps, one thread a row.
+//   pair mode  (a unit of more than one tile): stream s takes rows of tile s,
+//              both the same keys; a K or V page in shared memory serves both;
+//   split mode (one tile of rows: decoding, a drafted block, a chunk's rest):
+//              both streams take the same rows, alternate pages, and their
+//              (O, max, sum) are joined at the end of the piece.
+// So while one stream's scores are in the softmax, the other's products run.
+// P goes back to TMEM over the columns of its own S (bf16, half the columns)
+// and is the A operand of the second product. One thread issues all MMAs, in
+// an order in which S of the next page follows P V of the last one on the
+// same columns; the tensor core executes them in that order.
+//
+// K, V pages come by TMA through a ring of 32 KB stages that runs on across
+// units, Q tiles through two buffers, so the next unit's loads are in flight
+// while the current one ends.
+#include "chunk.cuh"
+
+namespace dfl {
+namespace {
+
+constexpr int kKeys = kPageKeys;             // keys of a tile: one page
+constexpr uint32_t kSubTile = 128 * 128;     // 128 rows x 128 bytes, swizzled
+constexpr int kStages = 5;                   // K / V ring
+constexpr int kTcThreads = 384;              // loads, MMAs, two idle warps; 2 x 4 softmax warps
+constexpr int kLoadRegs = 88, kSoftmaxRegs = 208;   // 128 * 88 + 256 * 208 = 384 * 168
+constexpr float kLog2eTc = 1.4426950408889634f;
+constexpr float kLag = 8.0f;                 // log2 units that the running maximum may lag behind
+
+struct ChunkSmem {
+  uint64_t kv_full[kStages], kv_empty[kStages], q_full[2], q_empty[2];
+  uint64_t s_full[2], p_full[2], o_full[2], drained;
+  uint32_t tmem_base;
+  int abort_flag;
+  int start[4];                // this CTA's first piece: sequence, unit, KV head, page
+  long long total;             // pages of all units
+  long long warp_sum[kTcThreads / 32];
+  float row_max[2][128], row_sum[2][128];   // split mode: the streams' statistics
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem], 16-bit inputs: row r of A in TMEM lane r, two
+// consecutive K elements a column.
+__device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ uint64_t l2_evict_normal() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// Bounded wait that also ends (false) once any role of the CTA gave up.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, ChunkSmem* h, int* status) {
+  const uint32_t b = smem_u32(bar);
+  if (mbar_try_wait(b, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(b, parity)) {
+    if (*reinterpret_cast<volatile int*>(&h->abort_flag)) return false;
+    if (clock64() - t0 > kWaitLimitCycles) {
+      report(status, DFLASH_ERR_TIMEOUT);
+      atomicExch(&h->abort_flag, 1);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool warp_wait_bar(uint64_t* bar, uint32_t parity, ChunkSmem* h, int* status) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, h, status)) != 0;
+}
+
+// Pages of unit j of a sequence of n rows behind ctx keys; a unit without keys
+// still takes one (masked) page, so that its rows are written.
+__device__ __forceinline__ int unit_pages(const ChunkArgs& p, int n, int ctx, int j, int unit_tok) {
+  ChunkUnit u{0, 0, n, ctx, 0};
+  const int keys = row_keys(p, u, min((j + 1) * unit_tok, n) - 1);
+  return max(1, (keys + kKeys - 1) / kKeys);
+}
+
+// A CTA's walk over its range: the current piece.
+struct Walk {
+  int b, j, kvh;        // unit
+  int row0, n, ctx;     // its sequence
+  int pages;            // the unit's pages
+  int kt0, nt;          // the piece: pages kt0 .. kt0 + nt - 1
+  int left;             // pages left in the range, this piece's included
+  long long at;         // position of the piece's first page
+  int tok0, n_tok;      // the unit's tokens
+  bool pair;
+
+  __device__ __forceinline__ void load_unit(const ChunkArgs& p, int unit_tok) {
+    tok0 = j * unit_tok;
+    n_tok = min(unit_tok, n - tok0);
+    pages = unit_pages(p, n, ctx, j, unit_tok);
+    pair = n_tok * 2 > unit_tok;
+  }
+  __device__ __forceinline__ void begin(const ChunkArgs& p, const ChunkSmem* h, long long first, int count, int unit_tok) {
+    left = count;
+    at = first;
+    if (left <= 0) return;
+    b = h->start[0]; j = h->start[1]; kvh = h->start[2]; kt0 = h->start[3];
+    chunk_rows(p, b, row0, n);
+    ctx = p.ctx_len[b];
+    load_unit(p, unit_tok);
+    nt = min(left, pages - kt0);
+  }
+  __device__ __forceinline__ void next(const ChunkArgs& p, int unit_tok) {
+    left -= nt;
+    at += nt;
+    if (left <= 0) return;
+    kt0 = 0;
+    if (++kvh == p.n_kv_heads) {
+      kvh = 0;
+      if (tok0 + n_tok >= n) {
+        j = 0;
+        do {
+          ++b;
+          chunk_rows(p, b, row0, n);
+        } while (n == 0 && b + 1 < p.B);
+        ctx = p.ctx_len[b];
+      } else {
+        ++j;
+      }
+      load_unit(p, unit_tok);
+    }
+    nt = min(left, pages);
+  }
+  __device__ __forceinline__ bool whole() const { return nt == pages; }
+  // tiles of stream s, and the page (relative to kt0) of its k-th
+  __device__ __forceinline__ int count(int s) const { return pair ? nt : (nt + 1 - s) >> 1; }
+  __device__ __forceinline__ int tile(int s, int k) const { return pair ? k : 2 * k + s; }
+};
+
+template <int DH>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    chunk_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                    const __grid_constant__ CUtensorMap v_map, const ChunkArgs p) {
+  constexpr int NSUB = DH / 64;
+  constexpr uint32_t kTileBytes = NSUB * kSubTile;
+  constexpr uint32_t kOCol = 256;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];   // tiles, then the header
+  ChunkSmem* hdr = reinterpret_cast<ChunkSmem*>(smem_raw + (2 + kStages) * kTileBytes);
+  const uint32_t q_s = smem_u32(smem_raw), kv_s = q_s + 2 * kTileBytes;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = p.n_q_heads / p.n_kv_heads;
+  const int tile_tok = 128 / G, unit_tok = 2 * tile_tok;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_u32(&hdr->kv_full[i]), 1);
+      mbar_init(smem_u32(&hdr->kv_empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&hdr->q_full[i]), 1);
+      mbar_init(smem_u32(&hdr->q_empty[i]), 1);
+      mbar_init(smem_u32(&hdr->s_full[i]), 1);
+      mbar_init(smem_u32(&hdr->p_full[i]), 128);
+      mbar_init(smem_u32(&hdr->o_full[i]), 1);
+    }
+    mbar_init(smem_u32(&hdr->drained), 1);
+    hdr->abort_flag = 0;
+    fence_mbar_init();
+    fence_proxy_async();
+    tma_prefetch_map(&q_map);
+    tma_prefetch_map(&k_map);
+    tma_prefetch_map(&v_map);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&hdr->tmem_base), 512);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  pdl_launch_dependents();   // after the wait: the merge may read what this kernel may read
+  if (threadIdx.x == 128) p.desc[blockIdx.x * kChunkDescInts] = 0;   // no incomplete unit starts here yet
+
+  // ---------------------------------------------------------------- ranges
+  // Pages of each sequence for one KV head, summed by threads over contiguous
+  // runs of sequences; a scan gives the total and finds this CTA's first page.
+  long long mine = 0;
+  const int per = (p.B + kTcThreads - 1) / kTcThreads;
+  const int b_first = threadIdx.x * per, b_last = min(p.B, b_first + per);
+  for (int b = b_first; b < b_last; ++b) {
+    int row0, n;
+    chunk_rows(p, b, row0, n);
+    const int ctx = p.ctx_len[b], units = (n + unit_tok - 1) / unit_tok;
+    for (int j = 0; j < units; ++j) mine += unit_pages(p, n, ctx, j, unit_tok);
+    if (blockIdx.x == 0 && n > 0) check_capacity(p, ChunkUnit{b, row0, n, ctx, 0});
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += t;
+  }
+  if (lane == 31) hdr->warp_sum[warp] = incl;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = hdr->tmem_base;
+  long long before = incl - mine, total = 0;
+  for (int w = 0; w < kTcThreads / 32; ++w) {
+    if (w < warp) before += hdr->warp_sum[w];
+    total += hdr->warp_sum[w];
+  }
+  total *= p.n_kv_heads;
+  before *= p.n_kv_heads;
+  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), max(total, 1LL)));
+  const int cta = blockIdx.x;
+  const long long first = cta < ctas ? total * cta / ctas : total;
+  const int count = cta < ctas ? static_cast<int>(total * (cta + 1) / ctas - first) : 0;
+  if (count > 0 && first >= before && first < before + mine * p.n_kv_heads) {
+    long long rem = first - before;
+    for (int b = b_first; b < b_last; ++b) {
+      int row0, n;
+      chunk_rows(p, b, row0, n);
+      const int ctx = p.ctx_len[b], units = (n + unit_tok - 1) / unit_tok;
+      bool found = false;
+      for (int j = 0; j < units && !found; ++j) {
+        const int pages = unit_pages(p, n, ctx, j, unit_tok);
+        if (rem < static_cast<long long>(pages) * p.n_kv_heads) {
+          hdr->start[0] = b; hdr->start[1] = j;
+          hdr->start[2] = static_cast<int>(rem / pages);
+          hdr->start[3] = static_cast<int>(rem % pages);
+          found = true;
+        } else {
+          rem -= static_cast<long long>(pages) * p.n_kv_heads;
+        }
+      }
+      if (found) break;
+    }
+  }
+  __syncthreads();
+  int* status = p.dev_status;
+  Walk w;
+  w.begin(p, hdr, first, count, unit_tok);
+
+  if (warp < 4) {
+    regs_dec<kLoadRegs>();
+    if (warp == 0) {
+      // -------------------------------------------------------------- loads
+      const uint32_t q_bytes = static_cast<uint32_t>(NSUB) * 128u * (tile_tok * G);
+      const uint64_t once = l2_evict_first(), again = l2_evict_normal();
+      int g = 0, qi = 0;                // pages' and Q tiles' loads so far
+      int issued_kv = 0, issued_q = 0;  // of which issued (a failed wait skips one)
+      bool ok = true;
+      for (; w.left > 0 && ok; w.next(p, unit_tok)) {
+        const int nq = w.pair ? 2 : 1;
+        for (int i = 0; i < nq && ok; ++i, ++qi) {
+          const int buf = qi & 1;
+          if (qi >= 2) ok = warp_wait_bar(&hdr->q_empty[buf], ((qi >> 1) - 1) & 1, hdr, status);
+          if (ok && lane == 0) {
+            const uint32_t bar = smem_u32(&hdr->q_full[buf]);
+            mbar_expect_tx(bar, q_bytes);
+#pragma unroll
+            for (int s = 0; s < NSUB; ++s)
+              tma_load_3d(q_s + buf * kTileBytes + s * kSubTile, &q_map, bar, 64 * s, w.kvh * G,
+                          w.row0 + w.tok0 + i * tile_tok, once);
+          }
+          if (ok) issued_q = qi + 1;
+        }
+        // a sequence of several units reads its pages again from L2
+        const uint64_t pol = w.n > unit_tok ? again : once;
+        const int32_t* table = p.pages.table + static_cast<size_t>(w.b) * p.pages.pages_per_seq;
+        const bool keyless = w.ctx + w.n <= 0;
+        int ids = 0;
+        for (int t = 0; t < w.nt && ok; ++t) {
+          if ((t & 31) == 0) {
+            const int at = w.kt0 + t + lane;
+            ids = 0;
+            if (t + lane < w.nt && !keyless) {
+              ids = table[at];
+              if (ids < 0 || ids >= p.pages.n_pages) {   // not a page: page 0 is read instead
+                report(status, DFLASH_ERR_CAPACITY);
+                ids = 0;
+              }
+            }
+          }
+          const int page = __shfl_sync(0xffffffffu, ids, t & 31);
+          const int z = (p.layer * p.pages.n_pages + page) * p.n_kv_heads + w.kvh;
+          for (int v = 0; v < 2 && ok; ++v, ++g) {
+            const int st = g % kStages;
+            if (g >= kStages) ok = warp_wait_bar(&hdr->kv_empty[st], (g / kStages - 1) & 1, hdr, status);
+            if (ok && lane == 0) {
+              const uint32_t bar = smem_u32(&hdr->kv_full[st]);
+              mbar_expect_tx(bar, kTileBytes);
+#pragma unroll
+              for (int s = 0; s < NSUB; ++s)
+                tma_load_3d(kv_s + st * kTileBytes + s * kSubTile, v ? &v_map : &k_map, bar, 64 * s, 0, z, pol);
+            }
+            if (ok) issued_kv = g + 1;
+          }
+        }
+      }
+      // after a timeout no load of this CTA may still be landing when it exits
+      if (lane == 0 && *reinterpret_cast<volatile int*>(&hdr->abort_flag)) {
+        for (int i = max(0, issued_kv - kStages); i < issued_kv; ++i)
+          mbar_wait(smem_u32(&hdr->kv_full[i % kStages]), (i / kStages) & 1);
+        for (int i = max(0, issued_q - 2); i < issued_q; ++i) mbar_wait(smem_u32(&hdr->q_full[i & 1]), (i >> 1) & 1);
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // -------------------------------------------------------------- MMAs
+      if (lane == 0) {
+        const uint32_t idesc_s = make_idesc(128, kKeys, kFmtBF16);
+        const uint32_t idesc_o = make_idesc(128, DH, kFmtBF16, 1);
+        int g0 = 0, qi = 0, tiles[2] = {0, 0};   // loads, Q tiles and stream tiles before this piece
+        bool ok = true;
+        for (; w.left > 0 && ok; w.next(p, unit_tok)) {
+          const bool pair = w.pair;
+          const int n0 = w.count(0), n1 = w.count(1);
+          const int nq = pair ? 2 : 1;
+          int issued = 0;
+          for (int i = 0; i < nq && ok; ++i) ok = wait_bar(&hdr->q_full[(qi + i) & 1], ((qi + i) >> 1) & 1, hdr, status);
+          auto score = [&](int s, int k) {
+            const int g = g0 + 2 * w.tile(s, k), st = g % kStages;
+            ok = ok && wait_bar(&hdr->kv_full[st], (g / kStages) & 1, hdr, status);
+            if (!ok) return;
+            tc_fence_after();
+            const uint32_t qt = q_s + ((qi + (pair ? s : 0)) & 1) * kTileBytes, kt = kv_s + st * kTileBytes;
+#pragma unroll
+            for (int ks = 0; ks < DH / 16; ++ks) {
+              const uint32_t off = (ks >> 2) * kSubTile + (ks & 3) * 32;
+              tc_mma_f16(tmem + s * 128, sw128_desc(qt + off), sw128_desc(kt + off), idesc_s, ks > 0 ? 1u : 0u);
+            }
+            tc_commit(smem_u32(&hdr->s_full[s]));
+            if (!pair || s == 1) tc_commit(smem_u32(&hdr->kv_empty[st]));
+            if (++issued == n0 + n1)
+              for (int i = 0; i < nq; ++i) tc_commit(smem_u32(&hdr->q_empty[(qi + i) & 1]));
+          };
+          auto value = [&](int s, int k, int n) {
+            const int g = g0 + 2 * w.tile(s, k) + 1, st = g % kStages;
+            ok = ok && wait_bar(&hdr->p_full[s], (tiles[s] + k) & 1, hdr, status) &&
+                 wait_bar(&hdr->kv_full[st], (g / kStages) & 1, hdr, status);
+            if (!ok) return;
+            tc_fence_after();
+            const uint32_t vt = kv_s + st * kTileBytes;
+#pragma unroll
+            for (int ks = 0; ks < kKeys / 16; ++ks)
+              tc_mma_f16_ts(tmem + kOCol + s * DH, tmem + s * 128 + ks * 8, sw128_desc_mn(vt + ks * 2048, kSubTile, 1024),
+                            idesc_o, (k > 0 || ks > 0) ? 1u : 0u);
+            if (!pair || s == 1) tc_commit(smem_u32(&hdr->kv_empty[st]));
+            if (k == n - 1) tc_commit(smem_u32(&hdr->o_full[s]));
+          };
+          if (ok) score(0, 0);
+          if (ok && n1 > 0) score(1, 0);
+          for (int k = 0; k < n0 && ok; ++k) {
+            value(0, k, n0);
+            if (ok && k + 1 < n0) score(0, k + 1);
+            if (ok && k < n1) value(1, k, n1);
+            if (ok && k + 1 < n1) score(1, k + 1);
+          }
+          g0 += 2 * w.nt;
+          qi += nq;
+          tiles[0] += n0;
+          tiles[1] += n1;
+        }
+        // every MMA issued is done before the block frees its TMEM
+        tc_commit(smem_u32(&hdr->drained));
+        mbar_wait(smem_u32(&hdr->drained), 0);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax
+    regs_inc<kSoftmaxRegs>();
+    const int s = (warp - 4) >> 2;                       // stream
+    const int r = (warp & 3) * 32 + lane;                // row of the stream's tile
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + lanes + s * 128;
+    const float scale = p.scale * kLog2eTc;
+    const int r_tok = r / G, r_head = r - r_tok * G;
+    int g0 = 0, tiles = 0, pieces[2] = {0, 0};
+    bool ok = true;
+    for (; w.left > 0; w.next(p, unit_tok)) {
+      const bool pair = w.pair;
+      const int ns = w.count(s);
+      const int tok = (pair ? s * tile_tok : 0) + r_tok;   // token of the unit
+      const bool valid = r_tok < tile_tok && tok < w.n_tok;
+      const ChunkUnit u{w.b, w.row0, w.n, w.ctx, w.tok0};
+      const int lim = valid ? row_keys(p, u, w.tok0 + tok) : 0;
+      const bool live = __any_sync(0xffffffffu, valid) != 0;   // warp-uniform
+      const int keys = max(0, min(w.ctx + w.n, p.pages.pages_per_seq * kPageKeys));   // rows of the cache that hold keys
+      float m = -INFINITY, l = 0.f;
+      for (int k = 0; k < ns && ok; ++k) {
+        const int t = w.tile(s, k);
+        const int kb = (w.kt0 + t) * kKeys;
+        ok = warp_wait_bar(&hdr->s_full[s], (tiles + k) & 1, hdr, status);
+        if (!ok) break;
+        tc_fence_after();
+        if (keys - kb < kKeys && (s == 0 || !pair)) {
+          // rows of the last page behind the last key: zero their values (0 * NaN
+          // would poison O). In pair mode stream 0 does it for both: its P is
+          // awaited before either product of the page is issued.
+          const int g = g0 + 2 * t + 1, st = g % kStages;
+          ok = warp_wait_bar(&hdr->kv_full[st], (g / kStages) & 1, hdr, status);
+          if (!ok) break;
+          if (r >= keys - kb) {
+            const uint32_t vt = kv_s + st * kTileBytes + r * 128;
+#pragma unroll
+            for (int i = 0; i < NSUB; ++i)
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vt + i * kSubTile + c * 16), "r"(0u) : "memory");
+          }
+          fence_proxy_async();
+        }
+        if (live) {
+          float x[kKeys];
+#pragma unroll
+          for (int c = 0; c < kKeys; c += 32) tmem_ld32(t_s + c, x + c);
+          tmem_ld_wait();
+          const int seen = lim - kb;      // keys of this page that the row sees
+          if (__any_sync(0xffffffffu, seen < kKeys)) {
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i) x[i] = i < seen ? x[i] : -INFINITY;
+          }
+          float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+          for (int i = 4; i < kKeys; i += 4) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], x[i + c]);
+          }
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+          // the maximum is raised only when it grew by more than 2^kLag: P and
+          // the sums stay far inside fp32 and bf16 range, and O is rarely touched
+          const bool raise = top > m + kLag;
+          if (k > 0 && __any_sync(0xffffffffu, raise)) {
+            // S of this page was issued after P V of the last one: O is at rest
+            const float f = raise ? ex2(m - top) : 1.f;
+            l *= f;
+#pragma unroll
+            for (int c = 0; c < DH; c += 32) {
+              float o[32];
+              tmem_ld32(tmem + lanes + kOCol + s * DH + c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= f;
+              tmem_st16(tmem + lanes + kOCol + s * DH + c, o);
+              tmem_st16(tmem + lanes + kOCol + s * DH + c + 16, o + 16);
+            }
+          }
+          if (raise) m = top;
+          const float ref = m == -INFINITY ? 0.f : m;   // nothing seen yet: every term is 2^-inf = 0
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < kKeys; c += 32) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float a = ex2(fmaf(x[c + i], scale, -ref)), b = ex2(fmaf(x[c + i + 1], scale, -ref));
+              sum[i & 2] += a;
+              sum[(i & 2) + 1] += b;
+              pk[i >> 1] = pack_bf16(a, b);
+            }
+            tmem_st16u(t_s + (c >> 1), pk);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        mbar_arrive(smem_u32(&hdr->p_full[s]));
+      }
+
+      // ------------------------------------------------------------ the piece's rows
+      float* slot = nullptr;
+      if (!w.whole()) slot = p.partials + static_cast<size_t>(2 * cta + (w.kt0 > 0 ? 0 : 1)) * chunk_slot_floats(DH);
+      const int row = (pair ? s * tile_tok : 0) * G + r;     // packed row of the unit
+      const size_t out_at = (static_cast<size_t>(w.row0) + w.tok0 + tok) * p.ldo + static_cast<size_t>(w.kvh * G + r_head) * DH;
+      if (pair) {
+        ok = ok && warp_wait_bar(&hdr->o_full[s], pieces[s] & 1, hdr, status);
+        tc_fence_after();
+        if (ok && live) {
+          const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+          for (int c = 0; c < DH; c += 32) {
+            float o[32];
+            tmem_ld32(tmem + lanes + kOCol + s * DH + c, o);
+            tmem_ld_wait();
+            if (!valid) continue;
+            if (slot != nullptr) {
+              float4* y = reinterpret_cast<float4*>(slot + static_cast<size_t>(row) * DH + c);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) y[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            } else {
+              uint4* y = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + out_at + c);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                y[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv), pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                  pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                                  pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+            }
+          }
+          if (slot != nullptr && valid)
+            reinterpret_cast<float2*>(slot + static_cast<size_t>(kChunkRows) * DH)[row] = make_float2(m, l);
+          tc_fence_before();
+        }
+      } else {
+        // both streams' halves of the keys: each WG joins DH / 2 columns
+        ok = ok && warp_wait_bar(&hdr->o_full[0], pieces[0] & 1, hdr, status);
+        if (w.count(1) > 0) ok = ok && warp_wait_bar(&hdr->o_full[1], pieces[1] & 1, hdr, status);
+        tc_fence_after();
+        hdr->row_max[s][r] = m;
+        hdr->row_sum[s][r] = l;
+        named_bar(1, 256);
+        const float m0 = hdr->row_max[0][r], l0 = hdr->row_sum[0][r], m1 = hdr->row_max[1][r], l1 = hdr->row_sum[1][r];
+        const float mm = fmaxf(m0, m1), ref = mm == -INFINITY ? 0.f : mm;
+        const float f0 = ex2(m0 - ref), f1 = ex2(m1 - ref);
+        const float sum = l0 * f0 + l1 * f1;
+        constexpr int HC = DH / 2;
+        float o[HC];
+        if (ok && live) {
+#pragma unroll
+          for (int c = 0; c < HC; c += 32) tmem_ld32(tmem + lanes + kOCol + s * HC + c, o + c);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < HC; ++c) o[c] *= f0;
+          if (w.count(1) > 0) {
+#pragma unroll
+            for (int c = 0; c < HC; c += 32) {
+              float e[32];
+              tmem_ld32(tmem + lanes + kOCol + DH + s * HC + c, e);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[c + i] = fmaf(e[i], f1, o[c + i]);
+            }
+          }
+        }
+        tc_fence_before();
+        named_bar(1, 256);   // both streams' O and statistics are read: the next piece may overwrite them
+        if (ok && valid) {
+          if (slot != nullptr) {
+            float4* y = reinterpret_cast<float4*>(slot + static_cast<size_t>(row) * DH + s * HC);
+#pragma unroll
+            for (int i = 0; i < HC / 4; ++i) y[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            if (s == 0) reinterpret_cast<float2*>(slot + static_cast<size_t>(kChunkRows) * DH)[row] = make_float2(mm, sum);
+          } else {
+            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            uint4* y = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + out_at + s * HC);
+#pragma unroll
+            for (int i = 0; i < HC / 8; ++i)
+              y[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv), pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+          }
+        }
+      }
+      // the unit that starts here and goes on in the next CTAs: what to join
+      if (threadIdx.x == 128 && w.kt0 == 0 && !w.whole()) {
+        const long long end = w.at + w.pages;    // its last page lies in the last CTA whose range starts before it
+        const int last = static_cast<int>((end * ctas + total - 1) / total) - 1;
+        int* d = p.desc + cta * kChunkDescInts;
+        d[0] = last - cta + 1;
+        d[1] = w.row0 + w.tok0;
+        d[2] = w.n_tok;
+        d[3] = w.kvh;
+        d[4] = 2 * cta + 1;
+        d[5] = 2 * (cta + 1);
+        d[6] = 2;
+      }
+      g0 += 2 * w.nt;
+      tiles += ns;
+      pieces[0] += w.count(0) > 0 ? 1 : 0;
+      pieces[1] += w.count(1) > 0 ? 1 : 0;
+    }
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int DH>
+cudaError_t launch_tc(const ChunkArgs& a, const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, int ctas,
+                      cudaStream_t s, bool pdl) {
+  constexpr int smem = static_cast<int>((2 + kStages) * static_cast<size_t>(DH / 64) * kSubTile + sizeof(ChunkSmem));
+  static_assert(smem <= 232448, "shared memory of a CTA");
+  static bool done[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (!done[dev & 63]) {
+    const cudaError_t e = cudaFuncSetAttribute(chunk_tc_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    done[dev & 63] = true;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(kTcThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = pdl ? attr : nullptr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, chunk_tc_kernel<DH>, qm, km, vm, a);
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_tc(const ChunkArgs& a, int* ctas, cudaStream_t s, bool pdl) {
+  const int G = a.n_q_heads / a.n_kv_heads;
+  const uint64_t slabs = static_cast<uint64_t>(a.n_layers) * a.pages.n_pages * a.n_kv_heads;
+  CUtensorMap qm, km, vm;
+  if (!make_rows_map(&qm, a.q, a.head_dim, a.n_q_heads, a.T, a.ldq, G, 128 / G) ||
+      !make_operand_map(&km, a.k_pool, 2, a.head_dim, kPageKeys, slabs, kKeys) ||
+      !make_operand_map(&vm, a.v_pool, 2, a.head_dim, kPageKeys, slabs, kKeys))
+    return cudaErrorInvalidValue;
+  const int sms = num_sms_of_current_device();
+  *ctas = sms < kChunkMaxCtas ? sms : kChunkMaxCtas;
+  return a.head_dim == 128 ? launch_tc<128>(a, qm, km, vm, *ctas, s, pdl) : launch_tc<64>(a, qm, km, vm, *ctas, s, pdl);
+}
+
+}  // namespace dfl

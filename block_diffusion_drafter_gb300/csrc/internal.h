@@ -128,6 +128,11 @@ GemmPlan plan_gemm(int m_tiles, int n_rows, int k, int elem_bytes, int num_sms, 
 bool make_operand_map(CUtensorMap* map, const void* base, int elem_bytes, uint64_t k,
                       uint64_t rows, uint64_t zdim, uint32_t box_rows);
 
+// Map over bf16 rows of heads side by side ([rows][heads][dh], rows ld elements
+// apart) with a box of 64 elements x box_heads heads x box_rows rows.
+bool make_rows_map(CUtensorMap* map, const void* base, int dh, int heads, int rows, long long ld, int box_heads,
+                   int box_rows);
+
 cudaError_t launch_gemm(const CUtensorMap& a_map, const CUtensorMap& b_map, const GemmArgs& args,
                         const GemmPlan& plan, cudaStream_t stream, bool pdl);
 
@@ -285,6 +290,9 @@ constexpr int kChunkDescInts = 8;
 __host__ __device__ constexpr size_t chunk_slot_floats(int head_dim) {
   return static_cast<size_t>(kChunkRows) * (head_dim + 2);
 }
+// bf16 path on tcgen05 (attention_chunk_tc.cu): one persistent CTA an SM;
+// *ctas is the number of merge descriptors it writes.
+cudaError_t launch_chunk_tc(const ChunkArgs& a, int* ctas, cudaStream_t s, bool pdl);
 // Launches the attention (and, where units may be split, its merge); `trace`
 // records both.
 struct Tracer;
