@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkArg
     } else {
       float* slot = p.partials + static_cast<size_t>(unit * splits + sp_i) * chunk_slot_floats(DH);
 #pragma unroll
-      for (int c = 0; c < DC; ++c) slot[static_cast<size_t>(r) * DH + tx + 16 * c] = o[i][c];
+      for (int c = 0; c < DC; ++c) slot[partial_at<DH>(r, (tx + 16 * c) >> 2) + (tx & 3)] = o[i][c];
       if (tx == 0)
         reinterpret_cast<float2*>(slot + static_cast<size_t>(kChunkRows) * DH)[r] = make_float2(m[i], l[i]);
     }
@@ -173,44 +173,75 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkArg
 
 // ------------------------------------------------------------------ merge
 // Joins the partial rows of split units: CTA (unit, x) takes packed rows
-// 4x .. 4x+3, a warp per row. The weights 2^(m_s - M) and the sums are taken
-// in ascending split order, so a result does not depend on timing.
+// 8x .. 8x+7, a warp a quarter of the columns, a lane four columns of one row.
+// The parts' rows, maxima and sums of kMergeBatch splits are requested at once;
+// they are added in ascending split order (a batch at a time, under the
+// running maximum), so a result does not depend on timing.
+constexpr int kMergeBatch = 8;
+__device__ __forceinline__ void store_out(float* y, float4 v) { *reinterpret_cast<float4*>(y) = v; }
+__device__ __forceinline__ void store_out(__nv_bfloat16* y, float4 v) {
+  __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+  *reinterpret_cast<uint2*>(y) = make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+}
 template <typename T, int DH>
 __global__ void __launch_bounds__(128) chunk_merge_kernel(const ChunkArgs p) {
-  constexpr int DPT = DH / 32;
+  constexpr int NL = DH / 64;   // loads of 16 columns a warp
   pdl_launch_dependents();
   pdl_wait();
   const int* d = p.desc + blockIdx.x * kChunkDescInts;
-  const int S = d[0], G = p.n_q_heads / p.n_kv_heads;
-  const int lane = threadIdx.x & 31;
-  const int rows = d[2] * G;
-  for (int r = blockIdx.y * 4 + static_cast<int>(threadIdx.x >> 5); S > 0 && r < rows; r += gridDim.y * 4) {
+  const int S = d[0];
+  if (S == 0) return;
+  const int G = p.n_q_heads / p.n_kv_heads, rows = d[2] * G;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int g = blockIdx.y; g * 8 < rows; g += gridDim.y) {
     const int first = d[4], rest = d[5], step = d[6];
-    auto slot = [&](int s) {
-      return p.partials + static_cast<size_t>(s == 0 ? first : rest + (s - 1) * step) * chunk_slot_floats(DH);
-    };
-    float M = -INFINITY;
-    for (int s = lane; s < S; s += 32)
-      M = fmaxf(M, reinterpret_cast<const float2*>(slot(s) + static_cast<size_t>(kChunkRows) * DH)[r].x);
+    const int r = g * 8 + (lane & 7), c0 = warp * NL * 4 + (lane >> 3);
+    float M = -INFINITY, L = 0.f;
+    float4 acc[NL];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float ref = M == -INFINITY ? 0.f : M;
-    float L = 0.f, acc[DPT];
+    for (int i = 0; i < NL; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 < S; s0 += kMergeBatch) {
+      float2 ml[kMergeBatch];
+      float4 x[kMergeBatch][NL];
 #pragma unroll
-    for (int i = 0; i < DPT; ++i) acc[i] = 0.f;
-#pragma unroll 8
-    for (int s = 0; s < S; ++s) {
-      const float* base = slot(s);
-      const float2 ml = reinterpret_cast<const float2*>(base + static_cast<size_t>(kChunkRows) * DH)[r];
-      const float w = exp2f(ml.x - ref);
-      L += ml.y * w;
+      for (int k = 0; k < kMergeBatch; ++k) {
+        ml[k] = make_float2(-INFINITY, 0.f);
+        if (s0 + k < S) {
+          const int at = s0 + k == 0 ? first : rest + (s0 + k - 1) * step;
+          const float* slot = p.partials + static_cast<size_t>(at) * chunk_slot_floats(DH);
+          ml[k] = __ldcg(reinterpret_cast<const float2*>(slot + static_cast<size_t>(kChunkRows) * DH) + r);
 #pragma unroll
-      for (int i = 0; i < DPT; ++i) acc[i] += base[static_cast<size_t>(r) * DH + lane + 32 * i] * w;
+          for (int i = 0; i < NL; ++i) x[k][i] = __ldcg(reinterpret_cast<const float4*>(slot + partial_at<DH>(r, c0 + 4 * i)));
+        }
+      }
+      float top = M;
+#pragma unroll
+      for (int k = 0; k < kMergeBatch; ++k) top = fmaxf(top, ml[k].x);
+      const float ref = top == -INFINITY ? 0.f : top;
+      const float f = exp2f(M - ref);
+      L *= f;
+#pragma unroll
+      for (int i = 0; i < NL; ++i) { acc[i].x *= f; acc[i].y *= f; acc[i].z *= f; acc[i].w *= f; }
+#pragma unroll
+      for (int k = 0; k < kMergeBatch; ++k) {
+        if (s0 + k < S) {
+          const float w = exp2f(ml[k].x - ref);
+          L += ml[k].y * w;
+#pragma unroll
+          for (int i = 0; i < NL; ++i) {
+            acc[i].x += x[k][i].x * w; acc[i].y += x[k][i].y * w; acc[i].z += x[k][i].z * w; acc[i].w += x[k][i].w * w;
+          }
+        }
+      }
+      M = top;
     }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
-    T* y = static_cast<T*>(p.out) + (d[1] + r / G) * p.ldo + (d[3] * G + r % G) * DH;
+    if (r < rows) {
+      const float inv = L > 0.f ? 1.f / L : 0.f;
+      T* y = static_cast<T*>(p.out) + (d[1] + r / G) * p.ldo + (d[3] * G + r % G) * DH;
 #pragma unroll
-    for (int i = 0; i < DPT; ++i) y[lane + 32 * i] = from_f32<T>(acc[i] * inv);
+      for (int i = 0; i < NL; ++i)
+        store_out(y + (c0 + 4 * i) * 4, make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv));
+    }
   }
 }
 
@@ -260,7 +291,7 @@ cudaError_t launch_simt(const ChunkArgs& a, cudaStream_t s, bool pdl, Tracer& tr
   tr.after();
   if (e != cudaSuccess || splits == 1) return e;
   tr.before(DFLASH_K_ATTN, 0.0, 0.0);
-  e = launch_plain(chunk_merge_kernel<float, DH>, dim3(static_cast<unsigned>(work), kSimtRows / 4), 128, 0, s, pdl, a);
+  e = launch_plain(chunk_merge_kernel<float, DH>, dim3(static_cast<unsigned>(work), kSimtRows / 8), 128, 0, s, pdl, a);
   tr.after();
   return e;
 }
@@ -280,7 +311,7 @@ cudaError_t launch_attention_chunk(const ChunkArgs& a, int bf16, cudaStream_t s,
   // the merge's grid covers the rows of the hinted chunk; its CTAs walk on over further rows
   const int G = a.n_q_heads / a.n_kv_heads;
   const long long rows = static_cast<long long>(a.max_rows) * G;
-  const int y = static_cast<int>(rows < 4 ? 1 : rows >= kChunkRows ? kChunkRows / 4 : (rows + 3) / 4);
+  const int y = static_cast<int>(rows < 8 ? 1 : rows >= kChunkRows ? kChunkRows / 8 : (rows + 7) / 8);
   tr.before(DFLASH_K_ATTN, 0.0, 0.0);
   e = a.head_dim == 128 ? launch_plain(chunk_merge_kernel<__nv_bfloat16, 128>, dim3(ctas, y), 128, 0, s, pdl, a)
                         : launch_plain(chunk_merge_kernel<__nv_bfloat16, 64>, dim3(ctas, y), 128, 0, s, pdl, a);

@@ -94,10 +94,49 @@ __device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, 
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// Two fp32 values in one 64-bit register: one instruction for both.
+__device__ __forceinline__ uint64_t pair2(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ uint64_t l2_evict_normal() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
   return p;
+}
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+// Matrix descriptors in two words (the fields of sw128_desc and sw128_desc_mn):
+// the low one holds the address / 16 and, for values, the byte offset / 16
+// between 64-column halves; the high one is the same for all.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t smem_addr) { return (smem_addr & 0x3FFFFu) >> 4; }
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+  return d;
 }
 template <int N>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -121,6 +160,52 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, ChunkSm
 }
 __device__ __forceinline__ bool warp_wait_bar(uint64_t* bar, uint32_t parity, ChunkSmem* h, int* status) {
   return __all_sync(0xffffffffu, wait_bar(bar, parity, h, status)) != 0;
+}
+
+// O row *= f, in TMEM.
+template <int DH>
+__device__ __noinline__ void rescale(uint32_t t_o, float f) {
+#pragma unroll 1
+  for (int c = 0; c < DH; c += 32) {
+    float o[32];
+    tmem_ld32(t_o + c, o);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] *= f;
+    tmem_st16(t_o + c, o);
+    tmem_st16(t_o + c + 16, o + 16);
+  }
+}
+
+// 32 columns of a warp's 32 output rows as bf16, a row a lane, to rows that lie
+// apart: four lanes exchange 16-byte pieces so that each then stores one piece
+// of each of their four rows, 64 contiguous bytes a row (stored straight from
+// the row's own lane, every 16 bytes are a line of their own; a unit of one
+// page took 7.7 us, most of it here). `at`: this lane's row, -1 for none.
+__device__ __forceinline__ void store_rows32(__nv_bfloat16* out, long long at, const float* o, float f, int lane) {
+  uint32_t c[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[i][j] = pack_bf16(o[8 * i + 2 * j] * f, o[8 * i + 2 * j + 1] * f);
+#pragma unroll
+  for (int bit = 1; bit <= 2; bit <<= 1) {
+    const bool up = (lane & bit) != 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & bit) continue;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t t = __shfl_xor_sync(0xffffffffu, up ? c[i][j] : c[i | bit][j], bit);
+        if (up) c[i][j] = t; else c[i | bit][j] = t;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const long long row = __shfl_sync(0xffffffffu, at, (lane & 28) | i);
+    if (row >= 0) *reinterpret_cast<uint4*>(out + row + (lane & 3) * 8) = make_uint4(c[i][0], c[i][1], c[i][2], c[i][3]);
+  }
 }
 
 // Pages of unit j of a sequence of n rows behind ctx keys; a unit without keys
@@ -355,61 +440,73 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       __syncwarp();
     } else if (warp == 1) {
       // -------------------------------------------------------------- MMAs
-      if (lane == 0) {
-        const uint32_t idesc_s = make_idesc(128, kKeys, kFmtBF16);
-        const uint32_t idesc_o = make_idesc(128, DH, kFmtBF16, 1);
-        int g0 = 0, qi = 0, tiles[2] = {0, 0};   // loads, Q tiles and stream tiles before this piece
-        bool ok = true;
-        for (; w.left > 0 && ok; w.next(p, unit_tok)) {
-          const bool pair = w.pair;
-          const int n0 = w.count(0), n1 = w.count(1);
-          const int nq = pair ? 2 : 1;
-          int issued = 0;
-          for (int i = 0; i < nq && ok; ++i) ok = wait_bar(&hdr->q_full[(qi + i) & 1], ((qi + i) >> 1) & 1, hdr, status);
-          auto score = [&](int s, int k) {
-            const int g = g0 + 2 * w.tile(s, k), st = g % kStages;
-            ok = ok && wait_bar(&hdr->kv_full[st], (g / kStages) & 1, hdr, status);
-            if (!ok) return;
-            tc_fence_after();
-            const uint32_t qt = q_s + ((qi + (pair ? s : 0)) & 1) * kTileBytes, kt = kv_s + st * kTileBytes;
+      // The whole warp walks and waits; one elected lane issues. Descriptors
+      // differ in their low word alone (address), kept as one base a tile: with
+      // whole descriptors built for each MMA the issue, not the tensor core, set
+      // the pace (a product of 128 x 128 x 128 takes 512 cycles, its eight MMAs
+      // took 1100 to issue).
+      const uint32_t idesc_s = make_idesc(128, kKeys, kFmtBF16);
+      const uint32_t idesc_o = make_idesc(128, DH, kFmtBF16, 1);
+      int g0 = 0, qi = 0, tiles0 = 0, tiles1 = 0;   // loads, Q tiles and stream tiles before this piece
+      bool ok = true;
+      for (; w.left > 0 && ok; w.next(p, unit_tok)) {
+        const bool pair = w.pair;
+        const int n0 = w.count(0), n1 = w.count(1);
+        const int nq = pair ? 2 : 1;
+        int issued = 0;
+        for (int i = 0; i < nq && ok; ++i) ok = warp_wait_bar(&hdr->q_full[(qi + i) & 1], ((qi + i) >> 1) & 1, hdr, status);
+        auto score = [&](int s, int k) {
+          const int g = g0 + 2 * w.tile(s, k), st = g % kStages;
+          ok = ok && warp_wait_bar(&hdr->kv_full[st], (g / kStages) & 1, hdr, status);
+          if (!ok) return;
+          tc_fence_after();
+          ++issued;
+          if (elect_one()) {
+            const uint32_t qd = desc_lo(q_s + ((qi + (pair ? s : 0)) & 1) * kTileBytes), kd = desc_lo(kv_s + st * kTileBytes);
 #pragma unroll
             for (int ks = 0; ks < DH / 16; ++ks) {
-              const uint32_t off = (ks >> 2) * kSubTile + (ks & 3) * 32;
-              tc_mma_f16(tmem + s * 128, sw128_desc(qt + off), sw128_desc(kt + off), idesc_s, ks > 0 ? 1u : 0u);
+              const uint32_t off = ((ks >> 2) * kSubTile + (ks & 3) * 32) >> 4;
+              tc_mma_f16(tmem + s * 128, desc_of(qd + off, kDescHi), desc_of(kd + off, kDescHi), idesc_s, ks > 0 ? 1u : 0u);
             }
             tc_commit(smem_u32(&hdr->s_full[s]));
             if (!pair || s == 1) tc_commit(smem_u32(&hdr->kv_empty[st]));
-            if (++issued == n0 + n1)
+            if (issued == n0 + n1)
               for (int i = 0; i < nq; ++i) tc_commit(smem_u32(&hdr->q_empty[(qi + i) & 1]));
-          };
-          auto value = [&](int s, int k, int n) {
-            const int g = g0 + 2 * w.tile(s, k) + 1, st = g % kStages;
-            ok = ok && wait_bar(&hdr->p_full[s], (tiles[s] + k) & 1, hdr, status) &&
-                 wait_bar(&hdr->kv_full[st], (g / kStages) & 1, hdr, status);
-            if (!ok) return;
-            tc_fence_after();
-            const uint32_t vt = kv_s + st * kTileBytes;
+          }
+          __syncwarp();
+        };
+        auto value = [&](int s, int k, int n) {
+          const int g = g0 + 2 * w.tile(s, k) + 1, st = g % kStages;
+          ok = ok && warp_wait_bar(&hdr->p_full[s], ((s == 0 ? tiles0 : tiles1) + k) & 1, hdr, status) &&
+               warp_wait_bar(&hdr->kv_full[st], (g / kStages) & 1, hdr, status);
+          if (!ok) return;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t vd = desc_lo(kv_s + st * kTileBytes) + ((kSubTile >> 4) << 16);   // 64-column halves kSubTile apart
 #pragma unroll
             for (int ks = 0; ks < kKeys / 16; ++ks)
-              tc_mma_f16_ts(tmem + kOCol + s * DH, tmem + s * 128 + ks * 8, sw128_desc_mn(vt + ks * 2048, kSubTile, 1024),
-                            idesc_o, (k > 0 || ks > 0) ? 1u : 0u);
+              tc_mma_f16_ts(tmem + kOCol + s * DH, tmem + s * 128 + ks * 8, desc_of(vd + ks * (2048 >> 4), kDescHi), idesc_o,
+                            (k > 0 || ks > 0) ? 1u : 0u);
             if (!pair || s == 1) tc_commit(smem_u32(&hdr->kv_empty[st]));
             if (k == n - 1) tc_commit(smem_u32(&hdr->o_full[s]));
-          };
-          if (ok) score(0, 0);
-          if (ok && n1 > 0) score(1, 0);
-          for (int k = 0; k < n0 && ok; ++k) {
-            value(0, k, n0);
-            if (ok && k + 1 < n0) score(0, k + 1);
-            if (ok && k < n1) value(1, k, n1);
-            if (ok && k + 1 < n1) score(1, k + 1);
           }
-          g0 += 2 * w.nt;
-          qi += nq;
-          tiles[0] += n0;
-          tiles[1] += n1;
+          __syncwarp();
+        };
+        if (ok) score(0, 0);
+        if (ok && n1 > 0) score(1, 0);
+        for (int k = 0; k < n0 && ok; ++k) {
+          value(0, k, n0);
+          if (ok && k + 1 < n0) score(0, k + 1);
+          if (ok && k < n1) value(1, k, n1);
+          if (ok && k + 1 < n1) score(1, k + 1);
         }
-        // every MMA issued is done before the block frees its TMEM
+        g0 += 2 * w.nt;
+        qi += nq;
+        tiles0 += n0;
+        tiles1 += n1;
+      }
+      // every MMA issued is done before the block frees its TMEM
+      if (elect_one()) {
         tc_commit(smem_u32(&hdr->drained));
         mbar_wait(smem_u32(&hdr->drained), 0);
       }
@@ -460,22 +557,43 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           fence_proxy_async();
         }
         if (live) {
-          float x[kKeys];
-#pragma unroll
-          for (int c = 0; c < kKeys; c += 32) tmem_ld32(t_s + c, x + c);
-          tmem_ld_wait();
+          // The row's scores are read in halves: the second once for the maximum
+          // and again for its exponentials, so that at most 96 of them are live
+          // (all 128 spilled registers). P of keys 2c, 2c + 1 goes to column c:
+          // columns that hold scores not yet turned into weights are never hit.
           const int seen = lim - kb;      // keys of this page that the row sees
-          if (__any_sync(0xffffffffu, seen < kKeys)) {
+          const bool cut = __any_sync(0xffffffffu, seen < kKeys) != 0;
+          float x[64], y[32];
+          float top;
+          {
+            float z[64];
+            tmem_ld32(t_s + 64, z);
+            tmem_ld32(t_s + 96, z + 32);
+            tmem_ld32(t_s, x);
+            tmem_ld32(t_s + 32, x + 32);
+            tmem_ld_wait();
+            if (cut) {
 #pragma unroll
-            for (int i = 0; i < kKeys; ++i) x[i] = i < seen ? x[i] : -INFINITY;
+              for (int i = 0; i < 64; ++i) {
+                x[i] = i < seen ? x[i] : -INFINITY;
+                z[i] = i + 64 < seen ? z[i] : -INFINITY;
+              }
+            }
+            float m0 = max3(x[0], x[1], z[0]), m1 = max3(x[2], x[3], z[1]), m2 = max3(x[4], x[5], z[2]),
+                  m3 = max3(x[6], x[7], z[3]);
+#pragma unroll
+            for (int i = 8; i < 64; i += 8) {
+              m0 = max3(m0, x[i], x[i + 1]); m1 = max3(m1, x[i + 2], x[i + 3]);
+              m2 = max3(m2, x[i + 4], x[i + 5]); m3 = max3(m3, x[i + 6], x[i + 7]);
+            }
+#pragma unroll
+            for (int i = 4; i < 60; i += 8) {
+              m0 = max3(m0, z[i], z[i + 1]); m1 = max3(m1, z[i + 2], z[i + 3]);
+              m2 = max3(m2, z[i + 4], z[i + 5]); m3 = max3(m3, z[i + 6], z[i + 7]);
+            }
+            m0 = max3(m0, z[60], z[61]); m1 = max3(m1, z[62], z[63]);
+            top = fmaxf(max3(m0, m1, m2), m3) * scale;
           }
-          float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-          for (int i = 4; i < kKeys; i += 4) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], x[i + c]);
-          }
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
           // the maximum is raised only when it grew by more than 2^kLag: P and
           // the sums stay far inside fp32 and bf16 range, and O is rarely touched
           const bool raise = top > m + kLag;
@@ -483,33 +601,40 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // S of this page was issued after P V of the last one: O is at rest
             const float f = raise ? ex2(m - top) : 1.f;
             l *= f;
-#pragma unroll
-            for (int c = 0; c < DH; c += 32) {
-              float o[32];
-              tmem_ld32(tmem + lanes + kOCol + s * DH + c, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] *= f;
-              tmem_st16(tmem + lanes + kOCol + s * DH + c, o);
-              tmem_st16(tmem + lanes + kOCol + s * DH + c + 16, o + 16);
-            }
+            rescale<DH>(tmem + lanes + kOCol + s * DH, f);
           }
           if (raise) m = top;
           const float ref = m == -INFINITY ? 0.f : m;   // nothing seen yet: every term is 2^-inf = 0
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int c = 0; c < kKeys; c += 32) {
+          const uint64_t scale2 = pair2(scale, scale), ref2 = pair2(-ref, -ref);
+          uint64_t sum2[2] = {0ull, 0ull};
+          auto weights = [&](const float* v, int col) {   // 32 scores to P's 16 columns from col on
             uint32_t pk[16];
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
-              const float a = ex2(fmaf(x[c + i], scale, -ref)), b = ex2(fmaf(x[c + i + 1], scale, -ref));
-              sum[i & 2] += a;
-              sum[(i & 2) + 1] += b;
+              const uint64_t e = fma2(pair2(v[i], v[i + 1]), scale2, ref2);
+              const float a = ex2(lo_of(e)), b = ex2(hi_of(e));
+              sum2[(i >> 1) & 1] = add2(sum2[(i >> 1) & 1], pair2(a, b));
               pk[i >> 1] = pack_bf16(a, b);
             }
-            tmem_st16u(t_s + (c >> 1), pk);
+            tmem_st16u(t_s + col, pk);
+          };
+          tmem_ld32(t_s + 64, y);
+          weights(x, 0);
+          weights(x + 32, 16);
+          tmem_ld_wait();
+          if (cut) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[i] = i + 64 < seen ? y[i] : -INFINITY;
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_ld32(t_s + 96, x);
+          weights(y, 32);
+          tmem_ld_wait();
+          if (cut) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = i + 96 < seen ? x[i] : -INFINITY;
+          }
+          weights(x, 48);
+          l += (lo_of(sum2[0]) + hi_of(sum2[0])) + (lo_of(sum2[1]) + hi_of(sum2[1]));
           tmem_st_wait();
         }
         tc_fence_before();
@@ -520,7 +645,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       float* slot = nullptr;
       if (!w.whole()) slot = p.partials + static_cast<size_t>(2 * cta + (w.kt0 > 0 ? 0 : 1)) * chunk_slot_floats(DH);
       const int row = (pair ? s * tile_tok : 0) * G + r;     // packed row of the unit
-      const size_t out_at = (static_cast<size_t>(w.row0) + w.tok0 + tok) * p.ldo + static_cast<size_t>(w.kvh * G + r_head) * DH;
+      const long long out_at = valid ? (static_cast<long long>(w.row0) + w.tok0 + tok) * p.ldo + (w.kvh * G + r_head) * DH : -1;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
       if (pair) {
         ok = ok && warp_wait_bar(&hdr->o_full[s], pieces[s] & 1, hdr, status);
         tc_fence_after();
@@ -531,18 +657,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             float o[32];
             tmem_ld32(tmem + lanes + kOCol + s * DH + c, o);
             tmem_ld_wait();
-            if (!valid) continue;
-            if (slot != nullptr) {
-              float4* y = reinterpret_cast<float4*>(slot + static_cast<size_t>(row) * DH + c);
+            if (slot == nullptr) {
+              store_rows32(out + c, out_at, o, inv, lane);
+            } else if (valid) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) y[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-            } else {
-              uint4* y = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + out_at + c);
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                y[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv), pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                  pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                                  pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+              for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<float4*>(slot + partial_at<DH>(row, c / 4 + i)) =
+                    make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
             }
           }
           if (slot != nullptr && valid)
@@ -582,19 +703,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         tc_fence_before();
         named_bar(1, 256);   // both streams' O and statistics are read: the next piece may overwrite them
-        if (ok && valid) {
-          if (slot != nullptr) {
-            float4* y = reinterpret_cast<float4*>(slot + static_cast<size_t>(row) * DH + s * HC);
-#pragma unroll
-            for (int i = 0; i < HC / 4; ++i) y[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-            if (s == 0) reinterpret_cast<float2*>(slot + static_cast<size_t>(kChunkRows) * DH)[row] = make_float2(mm, sum);
-          } else {
+        if (ok && live) {
+          if (slot == nullptr) {
             const float inv = sum > 0.f ? 1.f / sum : 0.f;
-            uint4* y = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + out_at + s * HC);
 #pragma unroll
-            for (int i = 0; i < HC / 8; ++i)
-              y[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv), pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+            for (int c = 0; c < HC; c += 32) store_rows32(out + s * HC + c, out_at, o + c, inv, lane);
+          } else if (valid) {
+#pragma unroll
+            for (int i = 0; i < HC / 4; ++i)
+              *reinterpret_cast<float4*>(slot + partial_at<DH>(row, s * HC / 4 + i)) =
+                  make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            if (s == 0) reinterpret_cast<float2*>(slot + static_cast<size_t>(kChunkRows) * DH)[row] = make_float2(mm, sum);
           }
         }
       }

@@ -17,6 +17,14 @@ struct ChunkUnit {
   int tok0;    // the unit's first token of the chunk
 };
 
+// Partial rows in a slot: 8 rows x 4 columns are 128 contiguous bytes, so that
+// the kernel that holds a row a thread stores, and the merge that takes 8 rows
+// of 16 columns a load reads, whole lines. Index of columns 4c .. 4c+3 of row r.
+template <int DH>
+__device__ __forceinline__ size_t partial_at(int r, int c) {
+  return static_cast<size_t>(((r >> 3) * (DH / 4) + c) * 8 + (r & 7)) * 4;
+}
+
 // Rows [first, last) of sequence b, kept inside the T rows of q whatever
 // cu_rows holds.
 __device__ __forceinline__ void chunk_rows(const ChunkArgs& p, int b, int& first, int& n) {
