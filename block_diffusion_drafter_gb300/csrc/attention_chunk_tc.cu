@@ -22,9 +22,9 @@
 //              (O, max, sum) are joined at the end of the piece.
 // So while one stream's scores are in the softmax, the other's products run.
 // P goes back to TMEM over the columns of its own S (bf16, half the columns)
-// and is the A operand of the second product. One thread issues all MMAs, in
-// an order in which S of the next page follows P V of the last one on the
-// same columns; the tensor core executes them in that order.
+// and is the A operand of the second product. A thread of its own issues each
+// stream's MMAs, S of the next page after P V of the last one on the same
+// columns; the tensor core executes them in that order.
 //
 // K, V pages come by TMA through a ring of 32 KB stages that runs on across
 // units, Q tiles through two buffers, so the next unit's loads are in flight
@@ -37,14 +37,14 @@ namespace {
 constexpr int kKeys = kPageKeys;             // keys of a tile: one page
 constexpr uint32_t kSubTile = 128 * 128;     // 128 rows x 128 bytes, swizzled
 constexpr int kStages = 5;                   // K / V ring
-constexpr int kTcThreads = 384;              // loads, MMAs, two idle warps; 2 x 4 softmax warps
+constexpr int kTcThreads = 384;              // K and V, 2 x MMAs, Q; 2 x 4 softmax warps
 constexpr int kLoadRegs = 88, kSoftmaxRegs = 208;   // 128 * 88 + 256 * 208 = 384 * 168
 constexpr float kLog2eTc = 1.4426950408889634f;
 constexpr float kLag = 8.0f;                 // log2 units that the running maximum may lag behind
 
 struct ChunkSmem {
   uint64_t kv_full[kStages], kv_empty[kStages], q_full[2], q_empty[2];
-  uint64_t s_full[2], p_full[2], o_full[2], drained;
+  uint64_t s_full[2], p_half[2], p_full[2], o_full[2], turn[2], drained[2];
   uint32_t tmem_base;
   int abort_flag;
   int start[4];                // this CTA's first piece: sequence, unit, KV head, page
@@ -84,14 +84,62 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t* v) {
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
-// D[tmem] (+)= A[tmem] * B[smem], 16-bit inputs: row r of A in TMEM lane r, two
-// consecutive K elements a column.
-__device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                              uint32_t accumulate) {
+// Tensor-core instructions of a converged warp: one elected lane (the same one
+// every time) issues a product's MMAs. The election and the MMAs are one block:
+// issued so, eight MMAs cost 170 cycles; with an election each 340; one by one
+// from a branch that one lane takes 570 to 830, more than the 512 that the
+// tensor core needs for them.
+#define DFL_ELECT "elect.sync _|e, 0xffffffff;\n\t"
+#define DFL_MMA_SS(off, acc)                                 \
+  "add.s64 a, %1, " #off ";\n\tadd.s64 b, %2, " #off ";\n\t" \
+  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, " #acc ";\n\t"
+// D[tmem] = A[smem] * B[smem]^T over a depth of DH: 16 columns are 32 bytes (2 in
+// a descriptor's address), a 64-column half is kSubTile on (1024).
+template <int DH>
+__device__ __forceinline__ void mma_scores(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc) {
+  static_assert(kSubTile == 1024 * 16, "offset of the second half");
+  if (DH == 128) {
+    asm volatile(
+        "{\n\t.reg .pred n, y, e;\n\t.reg .b64 a, b;\n\t" DFL_ELECT "setp.ne.b32 n, 0, 0;\n\tsetp.eq.b32 y, 0, 0;\n\t"
+        DFL_MMA_SS(0, n) DFL_MMA_SS(2, y) DFL_MMA_SS(4, y) DFL_MMA_SS(6, y)
+        DFL_MMA_SS(1024, y) DFL_MMA_SS(1026, y) DFL_MMA_SS(1028, y) DFL_MMA_SS(1030, y) "}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred n, y, e;\n\t.reg .b64 a, b;\n\t" DFL_ELECT "setp.ne.b32 n, 0, 0;\n\tsetp.eq.b32 y, 0, 0;\n\t"
+        DFL_MMA_SS(0, n) DFL_MMA_SS(2, y) DFL_MMA_SS(4, y) DFL_MMA_SS(6, y) "}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc)
+        : "memory");
+  }
+}
+#define DFL_MMA_TS(col, off, acc)                            \
+  "add.s32 a, %1, " #col ";\n\tadd.s64 b, %2, " #off ";\n\t" \
+  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, " #acc ";\n\t"
+// D[tmem] (+)= A[tmem] * B[smem] over 64 keys from 16 KS0 on: row r of A in TMEM lane
+// r, two consecutive keys a column; 16 keys of B are 2048 bytes (128).
+template <int KS0>
+__device__ __forceinline__ void mma_values(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  if (KS0 == 0) {
+    asm volatile(
+        "{\n\t.reg .pred p, y, e;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\t" DFL_ELECT
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 y, 0, 0;\n\t"
+        DFL_MMA_TS(0, 0, p) DFL_MMA_TS(8, 128, y) DFL_MMA_TS(16, 256, y) DFL_MMA_TS(24, 384, y) "}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred y, e;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\t" DFL_ELECT "setp.eq.b32 y, 0, 0;\n\t"
+        DFL_MMA_TS(32, 512, y) DFL_MMA_TS(40, 640, y) DFL_MMA_TS(48, 768, y) DFL_MMA_TS(56, 896, y) "}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc)
+        : "memory");
+  }
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred e;\n\t" DFL_ELECT
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
       : "memory");
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -122,17 +170,13 @@ __device__ __forceinline__ uint64_t l2_evict_normal() {
   asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
   return p;
 }
-// One lane of a converged warp, the same one every time.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
-}
 // Matrix descriptors in two words (the fields of sw128_desc and sw128_desc_mn):
 // the low one holds the address / 16 and, for values, the byte offset / 16
 // between 64-column halves; the high one is the same for all.
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_lo(uint32_t smem_addr) { return (smem_addr & 0x3FFFFu) >> 4; }
+// A value that all lanes hold alike, told to the compiler.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 __device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) {
   uint64_t d;
   asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
@@ -162,9 +206,16 @@ __device__ __forceinline__ bool warp_wait_bar(uint64_t* bar, uint32_t parity, Ch
   return __all_sync(0xffffffffu, wait_bar(bar, parity, h, status)) != 0;
 }
 
+// A warp's arrival, behind its lanes' TMEM accesses.
+__device__ __forceinline__ void arrive_warp(uint64_t* bar, int lane) {
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(smem_u32(bar));
+}
+
 // O row *= f, in TMEM.
 template <int DH>
-__device__ __noinline__ void rescale(uint32_t t_o, float f) {
+__device__ __forceinline__ void rescale(uint32_t t_o, float f) {
 #pragma unroll 1
   for (int c = 0; c < DH; c += 32) {
     float o[32];
@@ -215,6 +266,19 @@ __device__ __forceinline__ int unit_pages(const ChunkArgs& p, int n, int ctx, in
   const int keys = row_keys(p, u, min((j + 1) * unit_tok, n) - 1);
   return max(1, (keys + kKeys - 1) / kKeys);
 }
+
+// Stage and phase of the i-th load of the ring.
+struct RingPos {
+  int st;
+  uint32_t phase;
+  __device__ __forceinline__ explicit RingPos(int i) : st(i % kStages), phase((i / kStages) & 1) {}
+  __device__ __forceinline__ RingPos plus(int n) const {   // n <= kStages
+    RingPos r = *this;
+    r.st += n;
+    if (r.st >= kStages) { r.st -= kStages; r.phase ^= 1u; }
+    return r;
+  }
+};
 
 // A CTA's walk over its range: the current piece.
 struct Walk {
@@ -288,16 +352,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&hdr->kv_full[i]), 1);
-      mbar_init(smem_u32(&hdr->kv_empty[i]), 1);
+      mbar_init(smem_u32(&hdr->kv_empty[i]), 2);   // a stream each
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&hdr->q_full[i]), 1);
-      mbar_init(smem_u32(&hdr->q_empty[i]), 1);
+      mbar_init(smem_u32(&hdr->q_empty[i]), 2);
       mbar_init(smem_u32(&hdr->s_full[i]), 1);
-      mbar_init(smem_u32(&hdr->p_full[i]), 128);
+      mbar_init(smem_u32(&hdr->p_half[i]), 4);   // a softmax warp each
+      mbar_init(smem_u32(&hdr->p_full[i]), 4);
       mbar_init(smem_u32(&hdr->o_full[i]), 1);
+      mbar_init(smem_u32(&hdr->turn[i]), 1);
+      mbar_init(smem_u32(&hdr->drained[i]), 1);
     }
-    mbar_init(smem_u32(&hdr->drained), 1);
     hdr->abort_flag = 0;
     fence_mbar_init();
     fence_proxy_async();
@@ -377,27 +443,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp < 4) {
     regs_dec<kLoadRegs>();
     if (warp == 0) {
-      // -------------------------------------------------------------- loads
-      const uint32_t q_bytes = static_cast<uint32_t>(NSUB) * 128u * (tile_tok * G);
+      // -------------------------------------------------------------- K and V
       const uint64_t once = l2_evict_first(), again = l2_evict_normal();
-      int g = 0, qi = 0;                // pages' and Q tiles' loads so far
-      int issued_kv = 0, issued_q = 0;  // of which issued (a failed wait skips one)
+      int g = 0, issued = 0;   // loads so far, of which issued (a failed wait skips one)
       bool ok = true;
       for (; w.left > 0 && ok; w.next(p, unit_tok)) {
-        const int nq = w.pair ? 2 : 1;
-        for (int i = 0; i < nq && ok; ++i, ++qi) {
-          const int buf = qi & 1;
-          if (qi >= 2) ok = warp_wait_bar(&hdr->q_empty[buf], ((qi >> 1) - 1) & 1, hdr, status);
-          if (ok && lane == 0) {
-            const uint32_t bar = smem_u32(&hdr->q_full[buf]);
-            mbar_expect_tx(bar, q_bytes);
-#pragma unroll
-            for (int s = 0; s < NSUB; ++s)
-              tma_load_3d(q_s + buf * kTileBytes + s * kSubTile, &q_map, bar, 64 * s, w.kvh * G,
-                          w.row0 + w.tok0 + i * tile_tok, once);
-          }
-          if (ok) issued_q = qi + 1;
-        }
         // a sequence of several units reads its pages again from L2
         const uint64_t pol = w.n > unit_tok ? again : once;
         const int32_t* table = p.pages.table + static_cast<size_t>(w.b) * p.pages.pages_per_seq;
@@ -427,89 +477,131 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               for (int s = 0; s < NSUB; ++s)
                 tma_load_3d(kv_s + st * kTileBytes + s * kSubTile, v ? &v_map : &k_map, bar, 64 * s, 0, z, pol);
             }
-            if (ok) issued_kv = g + 1;
+            if (ok) issued = g + 1;
           }
         }
       }
       // after a timeout no load of this CTA may still be landing when it exits
       if (lane == 0 && *reinterpret_cast<volatile int*>(&hdr->abort_flag)) {
-        for (int i = max(0, issued_kv - kStages); i < issued_kv; ++i)
-          mbar_wait(smem_u32(&hdr->kv_full[i % kStages]), (i / kStages) & 1);
-        for (int i = max(0, issued_q - 2); i < issued_q; ++i) mbar_wait(smem_u32(&hdr->q_full[i & 1]), (i >> 1) & 1);
+        for (int i = max(0, issued - kStages); i < issued; ++i) mbar_wait(smem_u32(&hdr->kv_full[i % kStages]), (i / kStages) & 1);
       }
       __syncwarp();
-    } else if (warp == 1) {
-      // -------------------------------------------------------------- MMAs
-      // The whole warp walks and waits; one elected lane issues. Descriptors
-      // differ in their low word alone (address), kept as one base a tile: with
-      // whole descriptors built for each MMA the issue, not the tensor core, set
-      // the pace (a product of 128 x 128 x 128 takes 512 cycles, its eight MMAs
-      // took 1100 to issue).
-      const uint32_t idesc_s = make_idesc(128, kKeys, kFmtBF16);
-      const uint32_t idesc_o = make_idesc(128, DH, kFmtBF16, 1);
-      int g0 = 0, qi = 0, tiles0 = 0, tiles1 = 0;   // loads, Q tiles and stream tiles before this piece
+    } else if (warp == 3) {
+      // -------------------------------------------------------------- Q
+      // A warp of its own: waiting for a Q buffer holds up no K or V.
+      const uint32_t q_bytes = static_cast<uint32_t>(NSUB) * 128u * (tile_tok * G);
+      const uint64_t once = l2_evict_first();
+      int qi = 0, issued = 0;
       bool ok = true;
       for (; w.left > 0 && ok; w.next(p, unit_tok)) {
-        const bool pair = w.pair;
-        const int n0 = w.count(0), n1 = w.count(1);
-        const int nq = pair ? 2 : 1;
-        int issued = 0;
-        for (int i = 0; i < nq && ok; ++i) ok = warp_wait_bar(&hdr->q_full[(qi + i) & 1], ((qi + i) >> 1) & 1, hdr, status);
-        auto score = [&](int s, int k) {
-          const int g = g0 + 2 * w.tile(s, k), st = g % kStages;
-          ok = ok && warp_wait_bar(&hdr->kv_full[st], (g / kStages) & 1, hdr, status);
-          if (!ok) return;
-          tc_fence_after();
-          ++issued;
-          if (elect_one()) {
-            const uint32_t qd = desc_lo(q_s + ((qi + (pair ? s : 0)) & 1) * kTileBytes), kd = desc_lo(kv_s + st * kTileBytes);
+        const int nq = w.pair ? 2 : 1;
+        for (int i = 0; i < nq && ok; ++i, ++qi) {
+          const int buf = qi & 1;
+          if (qi >= 2) ok = warp_wait_bar(&hdr->q_empty[buf], ((qi >> 1) - 1) & 1, hdr, status);
+          if (ok && lane == 0) {
+            const uint32_t bar = smem_u32(&hdr->q_full[buf]);
+            mbar_expect_tx(bar, q_bytes);
 #pragma unroll
-            for (int ks = 0; ks < DH / 16; ++ks) {
-              const uint32_t off = ((ks >> 2) * kSubTile + (ks & 3) * 32) >> 4;
-              tc_mma_f16(tmem + s * 128, desc_of(qd + off, kDescHi), desc_of(kd + off, kDescHi), idesc_s, ks > 0 ? 1u : 0u);
-            }
-            tc_commit(smem_u32(&hdr->s_full[s]));
-            if (!pair || s == 1) tc_commit(smem_u32(&hdr->kv_empty[st]));
-            if (issued == n0 + n1)
-              for (int i = 0; i < nq; ++i) tc_commit(smem_u32(&hdr->q_empty[(qi + i) & 1]));
+            for (int s = 0; s < NSUB; ++s)
+              tma_load_3d(q_s + buf * kTileBytes + s * kSubTile, &q_map, bar, 64 * s, w.kvh * G,
+                          w.row0 + w.tok0 + i * tile_tok, once);
           }
-          __syncwarp();
-        };
-        auto value = [&](int s, int k, int n) {
-          const int g = g0 + 2 * w.tile(s, k) + 1, st = g % kStages;
-          ok = ok && warp_wait_bar(&hdr->p_full[s], ((s == 0 ? tiles0 : tiles1) + k) & 1, hdr, status) &&
-               warp_wait_bar(&hdr->kv_full[st], (g / kStages) & 1, hdr, status);
-          if (!ok) return;
-          tc_fence_after();
-          if (elect_one()) {
-            const uint32_t vd = desc_lo(kv_s + st * kTileBytes) + ((kSubTile >> 4) << 16);   // 64-column halves kSubTile apart
-#pragma unroll
-            for (int ks = 0; ks < kKeys / 16; ++ks)
-              tc_mma_f16_ts(tmem + kOCol + s * DH, tmem + s * 128 + ks * 8, desc_of(vd + ks * (2048 >> 4), kDescHi), idesc_o,
-                            (k > 0 || ks > 0) ? 1u : 0u);
-            if (!pair || s == 1) tc_commit(smem_u32(&hdr->kv_empty[st]));
-            if (k == n - 1) tc_commit(smem_u32(&hdr->o_full[s]));
-          }
-          __syncwarp();
-        };
-        if (ok) score(0, 0);
-        if (ok && n1 > 0) score(1, 0);
-        for (int k = 0; k < n0 && ok; ++k) {
-          value(0, k, n0);
-          if (ok && k + 1 < n0) score(0, k + 1);
-          if (ok && k < n1) value(1, k, n1);
-          if (ok && k + 1 < n1) score(1, k + 1);
+          if (ok) issued = qi + 1;
         }
+      }
+      if (lane == 0 && *reinterpret_cast<volatile int*>(&hdr->abort_flag)) {
+        for (int i = max(0, issued - 2); i < issued; ++i) mbar_wait(smem_u32(&hdr->q_full[i & 1]), (i >> 1) & 1);
+      }
+      __syncwarp();
+    } else if (warp < 3) {
+      // -------------------------------------------------------------- MMAs
+      // A warp a stream. Waits (100 cycles each even where nothing is to be
+      // waited for) and issuing are kept off the path from a page's weights to
+      // the next page's scores: everything else is awaited before the weights,
+      // and both products then issue in one go.
+      const int s = warp - 1;
+      const uint32_t idesc_s = make_idesc(128, kKeys, kFmtBF16);
+      const uint32_t idesc_o = make_idesc(128, DH, kFmtBF16, 1);
+      const uint32_t t_s = uniform(tmem + s * 128), t_o = uniform(tmem + kOCol + s * DH);
+      int g0 = 0, qi = 0, tiles = 0, turns = 0;   // loads, Q tiles, stream tiles and turns before this piece
+      bool ok = true;
+      for (; w.left > 0 && ok; w.next(p, unit_tok)) {
+        // Both streams take every load in order, also those that only the other
+        // one reads: a barrier's phases are seen one by one, and none passes
+        // before both saw it.
+        const bool pair = w.pair;
+        const int n = w.count(s), qt = qi + (pair ? s : 0);   // this stream's Q tile
+        RingPos at(g0);
+        auto wait_load = [&](const RingPos& r) { ok = ok && warp_wait_bar(&hdr->kv_full[r.st], r.phase, hdr, status); };
+        auto skip = [&]() {   // a page of the other stream: its K and V
+          for (int i = 0; i < 2 && ok; ++i) {
+            wait_load(at);
+            if (ok && lane == 0) mbar_arrive(smem_u32(&hdr->kv_empty[at.st]));
+            at = at.plus(1);
+          }
+        };
+        auto skip_q = [&](int i) {
+          ok = ok && warp_wait_bar(&hdr->q_full[i & 1], (i >> 1) & 1, hdr, status);
+          if (ok && lane == 0) mbar_arrive(smem_u32(&hdr->q_empty[i & 1]));
+        };
+        if (n > 0) ok = warp_wait_bar(&hdr->q_full[qt & 1], (qt >> 1) & 1, hdr, status);
+        const uint64_t qd = desc_of(uniform(desc_lo(q_s + (qt & 1) * kTileBytes)), kDescHi);
+        auto score = [&](const RingPos& r) {
+          mma_scores<DH>(t_s, qd, desc_of(uniform(desc_lo(kv_s + r.st * kTileBytes)), kDescHi), idesc_s);
+          mma_commit(&hdr->s_full[s]);
+          mma_commit(&hdr->kv_empty[r.st]);
+        };
+        if (!pair && s == 1 && ok) skip();
+        if (n > 0) {
+          wait_load(at);
+          tc_fence_after();
+          if (ok) score(at);
+        }
+        if (pair) skip_q(qi + 1 - s);   // early: the other stream's Q tile is free when that stream is done with it
+        for (int k = 0; k < n && ok; ++k) {
+          const RingPos v = at.plus(1), next = at.plus(2);
+          const uint32_t phase = (tiles + k) & 1;
+          wait_load(v);
+          if (pair && k + 1 < n) wait_load(next);
+          // 64-column halves of V lie kSubTile apart
+          const uint64_t vd = desc_of(uniform(desc_lo(kv_s + v.st * kTileBytes) + ((kSubTile >> 4) << 16)), kDescHi);
+          // the weights come in two halves of 64 keys, the first while the softmax still works on the second
+          ok = ok && warp_wait_bar(&hdr->p_half[s], phase, hdr, status);
+          // pair mode: in turn, so that one stream's softmax runs beside the other's products
+          if (pair && turns + k + s > 0) ok = ok && warp_wait_bar(&hdr->turn[s], (turns + k - 1 + s) & 1, hdr, status);
+          if (!ok) break;
+          tc_fence_after();
+          mma_values<0>(t_o, t_s, vd, idesc_o, k > 0 ? 1u : 0u);
+          ok = warp_wait_bar(&hdr->p_full[s], phase, hdr, status);
+          if (!ok) break;
+          tc_fence_after();
+          mma_values<4>(t_o, t_s, vd, idesc_o, 1u);
+          at = next;
+          if (k == n - 1) mma_commit(&hdr->o_full[s]);
+          if (pair) {
+            if (k + 1 < n) score(at);
+            if (lane == 0) mbar_arrive(smem_u32(&hdr->turn[1 - s]));
+            mma_commit(&hdr->kv_empty[v.st]);
+          } else {
+            mma_commit(&hdr->kv_empty[v.st]);
+            if (2 * k + s + 1 < w.nt) skip();
+            if (k + 1 < n) {
+              wait_load(at);
+              tc_fence_after();
+              if (ok) score(at);
+            }
+          }
+        }
+        if (ok && n > 0) mma_commit(&hdr->q_empty[qt & 1]);
+        if (n == 0) skip_q(qt);
         g0 += 2 * w.nt;
-        qi += nq;
-        tiles0 += n0;
-        tiles1 += n1;
+        qi += pair ? 2 : 1;
+        tiles += n;
+        if (pair) turns += n;
       }
       // every MMA issued is done before the block frees its TMEM
-      if (elect_one()) {
-        tc_commit(smem_u32(&hdr->drained));
-        mbar_wait(smem_u32(&hdr->drained), 0);
-      }
+      mma_commit(&hdr->drained[s]);
+      mbar_wait(smem_u32(&hdr->drained[s]), 0);
       __syncwarp();
     }
   } else {
@@ -539,10 +631,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         ok = warp_wait_bar(&hdr->s_full[s], (tiles + k) & 1, hdr, status);
         if (!ok) break;
         tc_fence_after();
-        if (keys - kb < kKeys && (s == 0 || !pair)) {
+        if (keys - kb < kKeys) {
           // rows of the last page behind the last key: zero their values (0 * NaN
-          // would poison O). In pair mode stream 0 does it for both: its P is
-          // awaited before either product of the page is issued.
+          // would poison O). In pair mode both streams do, each before its own product.
           const int g = g0 + 2 * t + 1, st = g % kStages;
           ok = warp_wait_bar(&hdr->kv_full[st], (g / kStages) & 1, hdr, status);
           if (!ok) break;
@@ -622,6 +713,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           weights(x, 0);
           weights(x + 32, 16);
           tmem_ld_wait();
+          tmem_st_wait();
+          arrive_warp(&hdr->p_half[s], lane);
           if (cut) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) y[i] = i + 64 < seen ? y[i] : -INFINITY;
@@ -636,9 +729,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           weights(x, 48);
           l += (lo_of(sum2[0]) + hi_of(sum2[0])) + (lo_of(sum2[1]) + hi_of(sum2[1]));
           tmem_st_wait();
+        } else {
+          arrive_warp(&hdr->p_half[s], lane);
         }
-        tc_fence_before();
-        mbar_arrive(smem_u32(&hdr->p_full[s]));
+        arrive_warp(&hdr->p_full[s], lane);
       }
 
       // ------------------------------------------------------------ the piece's rows
@@ -671,13 +765,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tc_fence_before();
         }
       } else {
-        // both streams' halves of the keys: each WG joins DH / 2 columns
-        ok = ok && warp_wait_bar(&hdr->o_full[0], pieces[0] & 1, hdr, status);
-        if (w.count(1) > 0) ok = ok && warp_wait_bar(&hdr->o_full[1], pieces[1] & 1, hdr, status);
-        tc_fence_after();
+        // both streams' halves of the keys: each WG joins DH / 2 columns. The
+        // first barrier also tells that the other stream is in this piece, so
+        // that its o_full is waited for in the right phase.
         hdr->row_max[s][r] = m;
         hdr->row_sum[s][r] = l;
         named_bar(1, 256);
+        ok = ok && warp_wait_bar(&hdr->o_full[0], pieces[0] & 1, hdr, status);
+        if (w.count(1) > 0) ok = ok && warp_wait_bar(&hdr->o_full[1], pieces[1] & 1, hdr, status);
+        tc_fence_after();
         const float m0 = hdr->row_max[0][r], l0 = hdr->row_sum[0][r], m1 = hdr->row_max[1][r], l1 = hdr->row_sum[1][r];
         const float mm = fmaxf(m0, m1), ref = mm == -INFINITY ? 0.f : mm;
         const float f0 = ex2(m0 - ref), f1 = ex2(m1 - ref);
