@@ -187,25 +187,39 @@ __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.a
 template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 
-// Bounded wait that also ends (false) once any role of the CTA gave up.
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, ChunkSmem* h, int* status) {
-  const uint32_t b = smem_u32(bar);
-  if (mbar_try_wait(b, parity)) return true;
+// Bounded wait that also ends (false) once any role of the CTA gave up. The
+// polling loop is a call, as is all code that is run rarely: inlined wherever
+// it is used, it made a kernel of 110 KB, whose roles drove each other's code
+// out of the instruction cache (thousands of cycles at every unit's end).
+__device__ __forceinline__ bool poll_bar(uint32_t bar, uint32_t parity, int* abort_flag, int* status) {
   const long long t0 = clock64();
-  while (!mbar_try_wait(b, parity)) {
-    if (*reinterpret_cast<volatile int*>(&h->abort_flag)) return false;
+  while (!mbar_try_wait(bar, parity)) {
+    if (*reinterpret_cast<volatile int*>(abort_flag)) return false;
     if (clock64() - t0 > kWaitLimitCycles) {
       report(status, DFLASH_ERR_TIMEOUT);
-      atomicExch(&h->abort_flag, 1);
+      atomicExch(abort_flag, 1);
       return false;
     }
   }
   return true;
 }
-__device__ __forceinline__ bool warp_wait_bar(uint64_t* bar, uint32_t parity, ChunkSmem* h, int* status) {
-  return __all_sync(0xffffffffu, wait_bar(bar, parity, h, status)) != 0;
+__device__ __noinline__ bool poll_bar_call(uint32_t bar, uint32_t parity, int* abort_flag, int* status) {
+  return poll_bar(bar, parity, abort_flag, status);
 }
-
+// Waits of a converged warp: a call in the warps that load and issue, inline in the
+// softmax, whose registers are full.
+__device__ __forceinline__ bool warp_wait_bar(uint64_t* bar, uint32_t parity, ChunkSmem* h, int* status) {
+  const uint32_t b = smem_u32(bar);
+  const bool ok = mbar_try_wait(b, parity) || poll_bar_call(b, parity, &h->abort_flag, status);
+  return __all_sync(0xffffffffu, ok) != 0;
+}
+__device__ __forceinline__ bool softmax_wait_bar(uint64_t* bar, uint32_t parity, ChunkSmem* h, int* status) {
+  const uint32_t b = smem_u32(bar);
+  const bool ok = mbar_try_wait(b, parity) || poll_bar(b, parity, &h->abort_flag, status);
+  return __all_sync(0xffffffffu, ok) != 0;
+}
+// a * b / c
+__device__ __noinline__ long long mul_div(long long a, long long b, long long c) { return a * b / c; }
 // A warp's arrival, behind its lanes' TMEM accesses.
 __device__ __forceinline__ void arrive_warp(uint64_t* bar, int lane) {
   tc_fence_before();
@@ -217,14 +231,13 @@ __device__ __forceinline__ void arrive_warp(uint64_t* bar, int lane) {
 template <int DH>
 __device__ __forceinline__ void rescale(uint32_t t_o, float f) {
 #pragma unroll 1
-  for (int c = 0; c < DH; c += 32) {
-    float o[32];
-    tmem_ld32(t_o + c, o);
+  for (int c = 0; c < DH; c += 16) {
+    float o[16];
+    tmem_ld16(t_o + c, o);
     tmem_ld_wait();
 #pragma unroll
-    for (int i = 0; i < 32; ++i) o[i] *= f;
+    for (int i = 0; i < 16; ++i) o[i] *= f;
     tmem_st16(t_o + c, o);
-    tmem_st16(t_o + c + 16, o + 16);
   }
 }
 
@@ -232,8 +245,8 @@ __device__ __forceinline__ void rescale(uint32_t t_o, float f) {
 // apart: four lanes exchange 16-byte pieces so that each then stores one piece
 // of each of their four rows, 64 contiguous bytes a row (stored straight from
 // the row's own lane, every 16 bytes are a line of their own; a unit of one
-// page took 7.7 us, most of it here). `at`: this lane's row, -1 for none.
-__device__ __forceinline__ void store_rows32(__nv_bfloat16* out, long long at, const float* o, float f, int lane) {
+// page took 7.7 us, most of it here). rows: the four lanes' rows, -1 for none.
+__device__ __forceinline__ void store_rows32(__nv_bfloat16* out, const long long* rows, const float* o, float f, int lane) {
   uint32_t c[4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -254,8 +267,7 @@ __device__ __forceinline__ void store_rows32(__nv_bfloat16* out, long long at, c
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const long long row = __shfl_sync(0xffffffffu, at, (lane & 28) | i);
-    if (row >= 0) *reinterpret_cast<uint4*>(out + row + (lane & 3) * 8) = make_uint4(c[i][0], c[i][1], c[i][2], c[i][3]);
+    if (rows[i] >= 0) *reinterpret_cast<uint4*>(out + rows[i] + (lane & 3) * 8) = make_uint4(c[i][0], c[i][1], c[i][2], c[i][3]);
   }
 }
 
@@ -377,7 +389,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
   pdl_wait();
   pdl_launch_dependents();   // after the wait: the merge may read what this kernel may read
-  if (threadIdx.x == 128) p.desc[blockIdx.x * kChunkDescInts] = 0;   // no incomplete unit starts here yet
+  if (threadIdx.x == 96) p.desc[blockIdx.x * kChunkDescInts] = 0;   // no incomplete unit starts here yet
 
   // ---------------------------------------------------------------- ranges
   // Pages of each sequence for one KV head, summed by threads over contiguous
@@ -385,10 +397,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   long long mine = 0;
   const int per = (p.B + kTcThreads - 1) / kTcThreads;
   const int b_first = threadIdx.x * per, b_last = min(p.B, b_first + per);
+#pragma unroll 1
   for (int b = b_first; b < b_last; ++b) {
     int row0, n;
     chunk_rows(p, b, row0, n);
     const int ctx = p.ctx_len[b], units = (n + unit_tok - 1) / unit_tok;
+#pragma unroll 1
     for (int j = 0; j < units; ++j) mine += unit_pages(p, n, ctx, j, unit_tok);
     if (blockIdx.x == 0 && n > 0) check_capacity(p, ChunkUnit{b, row0, n, ctx, 0});
   }
@@ -412,15 +426,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   before *= p.n_kv_heads;
   const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), max(total, 1LL)));
   const int cta = blockIdx.x;
-  const long long first = cta < ctas ? total * cta / ctas : total;
-  const int count = cta < ctas ? static_cast<int>(total * (cta + 1) / ctas - first) : 0;
+  const long long first = cta < ctas ? mul_div(total, cta, ctas) : total;
+  const int count = cta < ctas ? static_cast<int>(mul_div(total, cta + 1, ctas) - first) : 0;
   if (count > 0 && first >= before && first < before + mine * p.n_kv_heads) {
     long long rem = first - before;
+#pragma unroll 1
     for (int b = b_first; b < b_last; ++b) {
       int row0, n;
       chunk_rows(p, b, row0, n);
       const int ctx = p.ctx_len[b], units = (n + unit_tok - 1) / unit_tok;
       bool found = false;
+#pragma unroll 1
       for (int j = 0; j < units && !found; ++j) {
         const int pages = unit_pages(p, n, ctx, j, unit_tok);
         if (rem < static_cast<long long>(pages) * p.n_kv_heads) {
@@ -494,6 +510,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       int qi = 0, issued = 0;
       bool ok = true;
       for (; w.left > 0 && ok; w.next(p, unit_tok)) {
+        // the unit that starts here and goes on in the next CTAs: what to join
+        if (lane == 0 && w.kt0 == 0 && !w.whole()) {
+          const long long end = w.at + w.pages;    // its last page lies in the last CTA whose range starts before it
+          const int last = static_cast<int>(mul_div(end * ctas + total - 1, 1, total)) - 1;
+          int* d = p.desc + cta * kChunkDescInts;
+          d[0] = last - cta + 1;
+          d[1] = w.row0 + w.tok0;
+          d[2] = w.n_tok;
+          d[3] = w.kvh;
+          d[4] = 2 * cta + 1;
+          d[5] = 2 * (cta + 1);
+          d[6] = 2;
+        }
         const int nq = w.pair ? 2 : 1;
         for (int i = 0; i < nq && ok; ++i, ++qi) {
           const int buf = qi & 1;
@@ -531,69 +560,62 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // before both saw it.
         const bool pair = w.pair;
         const int n = w.count(s), qt = qi + (pair ? s : 0);   // this stream's Q tile
-        RingPos at(g0);
+        const int qo = pair ? qi + 1 - s : n == 0 ? qt : -1;  // a Q tile it only passes
+        RingPos at(g0), v = at;
         auto wait_load = [&](const RingPos& r) { ok = ok && warp_wait_bar(&hdr->kv_full[r.st], r.phase, hdr, status); };
-        auto skip = [&]() {   // a page of the other stream: its K and V
-          for (int i = 0; i < 2 && ok; ++i) {
-            wait_load(at);
-            if (ok && lane == 0) mbar_arrive(smem_u32(&hdr->kv_empty[at.st]));
-            at = at.plus(1);
-          }
-        };
-        auto skip_q = [&](int i) {
-          ok = ok && warp_wait_bar(&hdr->q_full[i & 1], (i >> 1) & 1, hdr, status);
-          if (ok && lane == 0) mbar_arrive(smem_u32(&hdr->q_empty[i & 1]));
-        };
         if (n > 0) ok = warp_wait_bar(&hdr->q_full[qt & 1], (qt >> 1) & 1, hdr, status);
         const uint64_t qd = desc_of(uniform(desc_lo(q_s + (qt & 1) * kTileBytes)), kDescHi);
-        auto score = [&](const RingPos& r) {
-          mma_scores<DH>(t_s, qd, desc_of(uniform(desc_lo(kv_s + r.st * kTileBytes)), kDescHi), idesc_s);
-          mma_commit(&hdr->s_full[s]);
-          mma_commit(&hdr->kv_empty[r.st]);
-        };
-        if (!pair && s == 1 && ok) skip();
-        if (n > 0) {
-          wait_load(at);
-          tc_fence_after();
-          if (ok) score(at);
-        }
-        if (pair) skip_q(qi + 1 - s);   // early: the other stream's Q tile is free when that stream is done with it
-        for (int k = 0; k < n && ok; ++k) {
-          const RingPos v = at.plus(1), next = at.plus(2);
-          const uint32_t phase = (tiles + k) & 1;
-          wait_load(v);
-          if (pair && k + 1 < n) wait_load(next);
-          // 64-column halves of V lie kSubTile apart
-          const uint64_t vd = desc_of(uniform(desc_lo(kv_s + v.st * kTileBytes) + ((kSubTile >> 4) << 16)), kDescHi);
-          // the weights come in two halves of 64 keys, the first while the softmax still works on the second
-          ok = ok && warp_wait_bar(&hdr->p_half[s], phase, hdr, status);
-          // pair mode: in turn, so that one stream's softmax runs beside the other's products
-          if (pair && turns + k + s > 0) ok = ok && warp_wait_bar(&hdr->turn[s], (turns + k - 1 + s) & 1, hdr, status);
-          if (!ok) break;
-          tc_fence_after();
-          mma_values<0>(t_o, t_s, vd, idesc_o, k > 0 ? 1u : 0u);
-          ok = warp_wait_bar(&hdr->p_full[s], phase, hdr, status);
-          if (!ok) break;
-          tc_fence_after();
-          mma_values<4>(t_o, t_s, vd, idesc_o, 1u);
-          at = next;
-          if (k == n - 1) mma_commit(&hdr->o_full[s]);
-          if (pair) {
-            if (k + 1 < n) score(at);
-            if (lane == 0) mbar_arrive(smem_u32(&hdr->turn[1 - s]));
-            mma_commit(&hdr->kv_empty[v.st]);
-          } else {
-            mma_commit(&hdr->kv_empty[v.st]);
-            if (2 * k + s + 1 < w.nt) skip();
-            if (k + 1 < n) {
+#pragma unroll 1
+        for (int k = 0; k <= n && ok; ++k) {
+          if (k > 0) {   // P V of page k - 1
+            const uint32_t phase = (tiles + k - 1) & 1;
+            v = at.plus(1);
+            at = at.plus(2);
+            wait_load(v);
+            if (pair && k < n) wait_load(at);
+            // 64-column halves of V lie kSubTile apart
+            const uint64_t vd = desc_of(uniform(desc_lo(kv_s + v.st * kTileBytes) + ((kSubTile >> 4) << 16)), kDescHi);
+            // the weights come in two halves of 64 keys, the first while the softmax still works on the second
+            ok = ok && warp_wait_bar(&hdr->p_half[s], phase, hdr, status);
+            // pair mode: in turn, so that one stream's softmax runs beside the other's products
+            if (pair && turns + k - 1 + s > 0) ok = ok && warp_wait_bar(&hdr->turn[s], (turns + k - 2 + s) & 1, hdr, status);
+            if (!ok) break;
+            tc_fence_after();
+            mma_values<0>(t_o, t_s, vd, idesc_o, k > 1 ? 1u : 0u);
+            ok = warp_wait_bar(&hdr->p_full[s], phase, hdr, status);
+            if (!ok) break;
+            tc_fence_after();
+            mma_values<4>(t_o, t_s, vd, idesc_o, 1u);
+            if (k == n) mma_commit(&hdr->o_full[s]);
+            if (!pair) mma_commit(&hdr->kv_empty[v.st]);
+          }
+          // split mode: the other stream's page before this stream's k-th
+          if (!pair && 2 * k + s >= 1 && 2 * k + s - 1 < w.nt) {
+#pragma unroll 1
+            for (int i = 0; i < 2 && ok; ++i) {
               wait_load(at);
-              tc_fence_after();
-              if (ok) score(at);
+              if (ok && lane == 0) mbar_arrive(smem_u32(&hdr->kv_empty[at.st]));
+              at = at.plus(1);
             }
           }
+          if (k < n) {   // S of page k
+            if (!pair || k == 0) wait_load(at);
+            if (!ok) break;
+            tc_fence_after();
+            mma_scores<DH>(t_s, qd, desc_of(uniform(desc_lo(kv_s + at.st * kTileBytes)), kDescHi), idesc_s);
+            mma_commit(&hdr->s_full[s]);
+            mma_commit(&hdr->kv_empty[at.st]);
+            if (k == n - 1) mma_commit(&hdr->q_empty[qt & 1]);
+          }
+          if (pair && k > 0) {
+            if (lane == 0) mbar_arrive(smem_u32(&hdr->turn[1 - s]));
+            mma_commit(&hdr->kv_empty[v.st]);
+          }
+          if (k == 0 && qo >= 0) {   // early: the tile is free once the other stream is done with it
+            ok = warp_wait_bar(&hdr->q_full[qo & 1], (qo >> 1) & 1, hdr, status);
+            if (ok && lane == 0) mbar_arrive(smem_u32(&hdr->q_empty[qo & 1]));
+          }
         }
-        if (ok && n > 0) mma_commit(&hdr->q_empty[qt & 1]);
-        if (n == 0) skip_q(qt);
         g0 += 2 * w.nt;
         qi += pair ? 2 : 1;
         tiles += n;
@@ -628,14 +650,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int k = 0; k < ns && ok; ++k) {
         const int t = w.tile(s, k);
         const int kb = (w.kt0 + t) * kKeys;
-        ok = warp_wait_bar(&hdr->s_full[s], (tiles + k) & 1, hdr, status);
+        ok = softmax_wait_bar(&hdr->s_full[s], (tiles + k) & 1, hdr, status);
         if (!ok) break;
         tc_fence_after();
         if (keys - kb < kKeys) {
           // rows of the last page behind the last key: zero their values (0 * NaN
           // would poison O). In pair mode both streams do, each before its own product.
           const int g = g0 + 2 * t + 1, st = g % kStages;
-          ok = warp_wait_bar(&hdr->kv_full[st], (g / kStages) & 1, hdr, status);
+          ok = softmax_wait_bar(&hdr->kv_full[st], (g / kStages) & 1, hdr, status);
           if (!ok) break;
           if (r >= keys - kb) {
             const uint32_t vt = kv_s + st * kTileBytes + r * 128;
@@ -648,12 +670,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           fence_proxy_async();
         }
         if (live) {
+          // Scores that the row does not see are overwritten where they lie. (A
+          // page that is cut anywhere is a unit's last one or two.)
+          const int seen = lim - kb;      // keys of this page that the row sees
+          if (__any_sync(0xffffffffu, seen < kKeys)) {
+#pragma unroll 1
+            for (int c = 0; c < kKeys; c += 16) {
+              float v[16];
+              tmem_ld16(t_s + c, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = c + i < seen ? v[i] : -INFINITY;
+              tmem_st16(t_s + c, v);
+            }
+            tmem_st_wait();
+          }
           // The row's scores are read in halves: the second once for the maximum
           // and again for its exponentials, so that at most 96 of them are live
           // (all 128 spilled registers). P of keys 2c, 2c + 1 goes to column c:
           // columns that hold scores not yet turned into weights are never hit.
-          const int seen = lim - kb;      // keys of this page that the row sees
-          const bool cut = __any_sync(0xffffffffu, seen < kKeys) != 0;
           float x[64], y[32];
           float top;
           {
@@ -663,13 +698,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tmem_ld32(t_s, x);
             tmem_ld32(t_s + 32, x + 32);
             tmem_ld_wait();
-            if (cut) {
-#pragma unroll
-              for (int i = 0; i < 64; ++i) {
-                x[i] = i < seen ? x[i] : -INFINITY;
-                z[i] = i + 64 < seen ? z[i] : -INFINITY;
-              }
-            }
             float m0 = max3(x[0], x[1], z[0]), m1 = max3(x[2], x[3], z[1]), m2 = max3(x[4], x[5], z[2]),
                   m3 = max3(x[6], x[7], z[3]);
 #pragma unroll
@@ -715,17 +743,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tmem_ld_wait();
           tmem_st_wait();
           arrive_warp(&hdr->p_half[s], lane);
-          if (cut) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) y[i] = i + 64 < seen ? y[i] : -INFINITY;
-          }
           tmem_ld32(t_s + 96, x);
           weights(y, 32);
           tmem_ld_wait();
-          if (cut) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = i + 96 < seen ? x[i] : -INFINITY;
-          }
           weights(x, 48);
           l += (lo_of(sum2[0]) + hi_of(sum2[0])) + (lo_of(sum2[1]) + hi_of(sum2[1]));
           tmem_st_wait();
@@ -741,91 +761,61 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int row = (pair ? s * tile_tok : 0) * G + r;     // packed row of the unit
       const long long out_at = valid ? (static_cast<long long>(w.row0) + w.tok0 + tok) * p.ldo + (w.kvh * G + r_head) * DH : -1;
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
-      if (pair) {
-        ok = ok && warp_wait_bar(&hdr->o_full[s], pieces[s] & 1, hdr, status);
-        tc_fence_after();
-        if (ok && live) {
-          const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-          for (int c = 0; c < DH; c += 32) {
-            float o[32];
-            tmem_ld32(tmem + lanes + kOCol + s * DH + c, o);
-            tmem_ld_wait();
-            if (slot == nullptr) {
-              store_rows32(out + c, out_at, o, inv, lane);
-            } else if (valid) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<float4*>(slot + partial_at<DH>(row, c / 4 + i)) =
-                    make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-            }
-          }
-          if (slot != nullptr && valid)
-            reinterpret_cast<float2*>(slot + static_cast<size_t>(kChunkRows) * DH)[row] = make_float2(m, l);
-          tc_fence_before();
-        }
-      } else {
-        // both streams' halves of the keys: each WG joins DH / 2 columns. The
-        // first barrier also tells that the other stream is in this piece, so
-        // that its o_full is waited for in the right phase.
+      // pair mode: all columns of the stream's own rows. Split mode: the streams hold
+      // the same rows over alternate pages; each joins half of the columns.
+      const bool both = !pair && w.count(1) > 0;
+      float f0 = 1.f, f1 = 0.f;
+      if (!pair) {
+        // The first barrier also tells that the other stream is in this piece,
+        // so that its o_full is waited for in the right phase.
         hdr->row_max[s][r] = m;
         hdr->row_sum[s][r] = l;
         named_bar(1, 256);
-        ok = ok && warp_wait_bar(&hdr->o_full[0], pieces[0] & 1, hdr, status);
-        if (w.count(1) > 0) ok = ok && warp_wait_bar(&hdr->o_full[1], pieces[1] & 1, hdr, status);
-        tc_fence_after();
-        const float m0 = hdr->row_max[0][r], l0 = hdr->row_sum[0][r], m1 = hdr->row_max[1][r], l1 = hdr->row_sum[1][r];
-        const float mm = fmaxf(m0, m1), ref = mm == -INFINITY ? 0.f : mm;
-        const float f0 = ex2(m0 - ref), f1 = ex2(m1 - ref);
-        const float sum = l0 * f0 + l1 * f1;
-        constexpr int HC = DH / 2;
-        float o[HC];
-        if (ok && live) {
+        const float m0 = hdr->row_max[0][r], m1 = hdr->row_max[1][r];
+        m = fmaxf(m0, m1);
+        const float ref = m == -INFINITY ? 0.f : m;
+        f0 = ex2(m0 - ref);
+        f1 = ex2(m1 - ref);
+        l = hdr->row_sum[0][r] * f0 + hdr->row_sum[1][r] * f1;
+        ok = ok && softmax_wait_bar(&hdr->o_full[0], pieces[0] & 1, hdr, status);
+      }
+      if (pair ? ns > 0 : both) ok = ok && softmax_wait_bar(&hdr->o_full[pair ? s : 1], pieces[pair ? s : 1] & 1, hdr, status);
+      tc_fence_after();
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const int c0 = pair ? 0 : s * (DH / 2), c1 = pair ? DH : c0 + DH / 2;
+      const uint32_t t_o = tmem + lanes + kOCol + (pair ? s * DH : 0);
+      if (slot != nullptr && valid && c0 == 0)
+        reinterpret_cast<float2*>(slot + static_cast<size_t>(kChunkRows) * DH)[row] = make_float2(m, l);
+      long long rows[4];
 #pragma unroll
-          for (int c = 0; c < HC; c += 32) tmem_ld32(tmem + lanes + kOCol + s * HC + c, o + c);
+      for (int i = 0; i < 4; ++i) rows[i] = __shfl_sync(0xffffffffu, out_at, (lane & 28) | i);
+#pragma unroll 1
+      for (int c = c0; c < c1 && ok && live; c += 32) {
+        float o[32];
+        tmem_ld32(t_o + c, o);
+        tmem_ld_wait();
+        if (!pair) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] *= f0;
+        }
+        if (both) {
+          float e[32];
+          tmem_ld32(t_o + DH + c, e);
           tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < HC; ++c) o[c] *= f0;
-          if (w.count(1) > 0) {
-#pragma unroll
-            for (int c = 0; c < HC; c += 32) {
-              float e[32];
-              tmem_ld32(tmem + lanes + kOCol + DH + s * HC + c, e);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[c + i] = fmaf(e[i], f1, o[c + i]);
-            }
-          }
+          for (int i = 0; i < 32; ++i) o[i] = fmaf(e[i], f1, o[i]);
         }
-        tc_fence_before();
-        named_bar(1, 256);   // both streams' O and statistics are read: the next piece may overwrite them
-        if (ok && live) {
-          if (slot == nullptr) {
-            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        if (slot == nullptr) {
+          store_rows32(out + c, rows, o, inv, lane);
+        } else if (valid) {
 #pragma unroll
-            for (int c = 0; c < HC; c += 32) store_rows32(out + s * HC + c, out_at, o + c, inv, lane);
-          } else if (valid) {
-#pragma unroll
-            for (int i = 0; i < HC / 4; ++i)
-              *reinterpret_cast<float4*>(slot + partial_at<DH>(row, s * HC / 4 + i)) =
-                  make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-            if (s == 0) reinterpret_cast<float2*>(slot + static_cast<size_t>(kChunkRows) * DH)[row] = make_float2(mm, sum);
-          }
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4*>(slot + partial_at<DH>(row, c / 4 + i)) =
+                make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
       }
-      // the unit that starts here and goes on in the next CTAs: what to join
-      if (threadIdx.x == 128 && w.kt0 == 0 && !w.whole()) {
-        const long long end = w.at + w.pages;    // its last page lies in the last CTA whose range starts before it
-        const int last = static_cast<int>((end * ctas + total - 1) / total) - 1;
-        int* d = p.desc + cta * kChunkDescInts;
-        d[0] = last - cta + 1;
-        d[1] = w.row0 + w.tok0;
-        d[2] = w.n_tok;
-        d[3] = w.kvh;
-        d[4] = 2 * cta + 1;
-        d[5] = 2 * (cta + 1);
-        d[6] = 2;
-      }
+      tc_fence_before();
+      if (!pair) named_bar(1, 256);   // both streams' O and statistics are read: the next piece may overwrite them
       g0 += 2 * w.nt;
       tiles += ns;
       pieces[0] += w.count(0) > 0 ? 1 : 0;
