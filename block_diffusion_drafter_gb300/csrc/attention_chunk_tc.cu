@@ -5,9 +5,9 @@
 // Units of work. The G query heads of a KV head are packed into the rows of
 // one tile (row = token * G + head), so a page's K and V are read once for all
 // of them. A unit is up to two 128-row tiles of one (sequence, KV head):
-// 2 * floor(128 / G) tokens. Its work is its number of 128-key pages, up to the
-// last key its last token sees. All units' pages, laid end to end, are cut into
-// equal ranges, one a CTA and one CTA an SM, whatever mix of long prompts
+// 2 * floor(128 / G) tokens. Its work is its 128-key pages, up to the last key its last
+// token sees, and a share of its own. All units, laid end to end, are cut into
+// ranges of equal cost, one a CTA and one CTA an SM, whatever mix of long prompts
 // and single tokens the batch holds: a CTA walks through its range, and only
 // the first and the last unit of a range can be incomplete. Incomplete units
 // write unnormalised rows to the workspace; chunk_merge_kernel joins them in
@@ -47,8 +47,7 @@ struct ChunkSmem {
   uint64_t s_full[2], p_half[2], p_full[2], o_full[2], turn[2], drained[2];
   uint32_t tmem_base;
   int abort_flag;
-  int start[4];                // this CTA's first piece: sequence, unit, KV head, page
-  long long total;             // pages of all units
+  int start[4];                // where this CTA begins: sequence, unit, KV head, position in the unit
   long long warp_sum[kTcThreads / 32];
   float row_max[2][128], row_sum[2][128];   // split mode: the streams' statistics
 };
@@ -292,16 +291,29 @@ struct RingPos {
   }
 };
 
+// Cost of a unit in thirds of a microsecond: its own share (Q, the first page's
+// latency, the rows' way out), then its pages. Measured over 1520 units of one
+// and of eight pages: two tiles of rows 5 us and 1.7 us a page, one tile 2 us and
+// 1.4 us a page. Cut by pages alone, the first CTA of an 8192-token prompt got 60
+// short units and ran 1.6 times as long as the others.
+__device__ __forceinline__ int unit_share(bool pair) { return pair ? 15 : 6; }
+__device__ __forceinline__ int page_share(bool pair) { return pair ? 5 : 4; }
+constexpr int kMinRange = 8;   // a CTA's least range: at least one page of any kind
+
+__device__ __forceinline__ int unit_cost(const ChunkArgs& p, int n, int ctx, int j, int unit_tok) {
+  const bool pair = min(unit_tok, n - j * unit_tok) * 2 > unit_tok;
+  return unit_share(pair) + unit_pages(p, n, ctx, j, unit_tok) * page_share(pair);
+}
+
 // A CTA's walk over its range: the current piece.
 struct Walk {
   int b, j, kvh;        // unit
   int row0, n, ctx;     // its sequence
   int pages;            // the unit's pages
   int kt0, nt;          // the piece: pages kt0 .. kt0 + nt - 1
-  int left;             // pages left in the range, this piece's included
-  long long at;         // position of the piece's first page
+  int begin, end;       // the range's ends, relative to the unit's first position
   int tok0, n_tok;      // the unit's tokens
-  bool pair;
+  bool pair, more;
 
   __device__ __forceinline__ void load_unit(const ChunkArgs& p, int unit_tok) {
     tok0 = j * unit_tok;
@@ -309,21 +321,35 @@ struct Walk {
     pages = unit_pages(p, n, ctx, j, unit_tok);
     pair = n_tok * 2 > unit_tok;
   }
-  __device__ __forceinline__ void begin(const ChunkArgs& p, const ChunkSmem* h, long long first, int count, int unit_tok) {
-    left = count;
-    at = first;
-    if (left <= 0) return;
-    b = h->start[0]; j = h->start[1]; kvh = h->start[2]; kt0 = h->start[3];
+  __device__ __forceinline__ int span() const { return unit_share(pair) + pages * page_share(pair); }
+  // Pages whose position (the unit's share, then page by page) lies before x.
+  __device__ __forceinline__ int pages_before(int x) const {
+    const int d = x - unit_share(pair);
+    const unsigned up = static_cast<unsigned>(max(d, 0) + page_share(pair) - 1);
+    return min(pages, static_cast<int>(pair ? up / 5u : up / 4u));
+  }
+  __device__ __forceinline__ void place() {
+    kt0 = pages_before(begin);
+    nt = pages_before(end) - kt0;
+  }
+  __device__ __forceinline__ void start(const ChunkArgs& p, const ChunkSmem* h, int count, int unit_tok) {
+    more = count > 0;
+    if (!more) return;
+    b = h->start[0]; j = h->start[1]; kvh = h->start[2];
+    begin = h->start[3];
+    end = begin + count;
     chunk_rows(p, b, row0, n);
     ctx = p.ctx_len[b];
     load_unit(p, unit_tok);
-    nt = min(left, pages - kt0);
+    place();
+    if (nt == 0) next(p, unit_tok);   // behind the last page's position, or before the first one's
   }
   __device__ __forceinline__ void next(const ChunkArgs& p, int unit_tok) {
-    left -= nt;
-    at += nt;
-    if (left <= 0) return;
-    kt0 = 0;
+    const int used = span();
+    begin -= used;
+    end -= used;
+    more = end > 0;
+    if (!more) return;
     if (++kvh == p.n_kv_heads) {
       kvh = 0;
       if (tok0 + n_tok >= n) {
@@ -338,7 +364,8 @@ struct Walk {
       }
       load_unit(p, unit_tok);
     }
-    nt = min(left, pages);
+    place();
+    more = nt > 0;   // a range that ends in a unit's own share has none of its pages
   }
   __device__ __forceinline__ bool whole() const { return nt == pages; }
   // tiles of stream s, and the page (relative to kt0) of its k-th
@@ -392,8 +419,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (threadIdx.x == 96) p.desc[blockIdx.x * kChunkDescInts] = 0;   // no incomplete unit starts here yet
 
   // ---------------------------------------------------------------- ranges
-  // Pages of each sequence for one KV head, summed by threads over contiguous
-  // runs of sequences; a scan gives the total and finds this CTA's first page.
+  // The cost of each sequence for one KV head, summed by threads over contiguous
+  // runs of sequences; a scan gives the total and finds where this CTA begins.
   long long mine = 0;
   const int per = (p.B + kTcThreads - 1) / kTcThreads;
   const int b_first = threadIdx.x * per, b_last = min(p.B, b_first + per);
@@ -403,7 +430,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     chunk_rows(p, b, row0, n);
     const int ctx = p.ctx_len[b], units = (n + unit_tok - 1) / unit_tok;
 #pragma unroll 1
-    for (int j = 0; j < units; ++j) mine += unit_pages(p, n, ctx, j, unit_tok);
+    for (int j = 0; j < units; ++j) mine += unit_cost(p, n, ctx, j, unit_tok);
     if (blockIdx.x == 0 && n > 0) check_capacity(p, ChunkUnit{b, row0, n, ctx, 0});
   }
   long long incl = mine;
@@ -424,7 +451,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
   total *= p.n_kv_heads;
   before *= p.n_kv_heads;
-  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), max(total, 1LL)));
+  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), max(total / kMinRange, 1LL)));
   const int cta = blockIdx.x;
   const long long first = cta < ctas ? mul_div(total, cta, ctas) : total;
   const int count = cta < ctas ? static_cast<int>(mul_div(total, cta + 1, ctas) - first) : 0;
@@ -438,14 +465,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       bool found = false;
 #pragma unroll 1
       for (int j = 0; j < units && !found; ++j) {
-        const int pages = unit_pages(p, n, ctx, j, unit_tok);
-        if (rem < static_cast<long long>(pages) * p.n_kv_heads) {
+        const int cost = unit_cost(p, n, ctx, j, unit_tok);
+        if (rem < static_cast<long long>(cost) * p.n_kv_heads) {
           hdr->start[0] = b; hdr->start[1] = j;
-          hdr->start[2] = static_cast<int>(rem / pages);
-          hdr->start[3] = static_cast<int>(rem % pages);
+          hdr->start[2] = static_cast<int>(rem / cost);
+          hdr->start[3] = static_cast<int>(rem % cost);
           found = true;
         } else {
-          rem -= static_cast<long long>(pages) * p.n_kv_heads;
+          rem -= static_cast<long long>(cost) * p.n_kv_heads;
         }
       }
       if (found) break;
@@ -454,7 +481,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncthreads();
   int* status = p.dev_status;
   Walk w;
-  w.begin(p, hdr, first, count, unit_tok);
+  w.start(p, hdr, count, unit_tok);
 
   if (warp < 4) {
     regs_dec<kLoadRegs>();
@@ -463,7 +490,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const uint64_t once = l2_evict_first(), again = l2_evict_normal();
       int g = 0, issued = 0;   // loads so far, of which issued (a failed wait skips one)
       bool ok = true;
-      for (; w.left > 0 && ok; w.next(p, unit_tok)) {
+      for (; w.more && ok; w.next(p, unit_tok)) {
         // a sequence of several units reads its pages again from L2
         const uint64_t pol = w.n > unit_tok ? again : once;
         const int32_t* table = p.pages.table + static_cast<size_t>(w.b) * p.pages.pages_per_seq;
@@ -509,11 +536,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const uint64_t once = l2_evict_first();
       int qi = 0, issued = 0;
       bool ok = true;
-      for (; w.left > 0 && ok; w.next(p, unit_tok)) {
+      for (; w.more && ok; w.next(p, unit_tok)) {
         // the unit that starts here and goes on in the next CTAs: what to join
         if (lane == 0 && w.kt0 == 0 && !w.whole()) {
-          const long long end = w.at + w.pages;    // its last page lies in the last CTA whose range starts before it
-          const int last = static_cast<int>(mul_div(end * ctas + total - 1, 1, total)) - 1;
+          // its last page lies in the last CTA whose range starts at or before that page
+          const long long x = first - w.begin + unit_share(w.pair) + (w.pages - 1) * page_share(w.pair);
+          const int last = static_cast<int>(mul_div((x + 1) * ctas + total - 1, 1, total)) - 1;
           int* d = p.desc + cta * kChunkDescInts;
           d[0] = last - cta + 1;
           d[1] = w.row0 + w.tok0;
@@ -554,7 +582,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const uint32_t t_s = uniform(tmem + s * 128), t_o = uniform(tmem + kOCol + s * DH);
       int g0 = 0, qi = 0, tiles = 0, turns = 0;   // loads, Q tiles, stream tiles and turns before this piece
       bool ok = true;
-      for (; w.left > 0 && ok; w.next(p, unit_tok)) {
+      for (; w.more && ok; w.next(p, unit_tok)) {
         // Both streams take every load in order, also those that only the other
         // one reads: a barrier's phases are seen one by one, and none passes
         // before both saw it.
@@ -637,7 +665,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int r_tok = r / G, r_head = r - r_tok * G;
     int g0 = 0, tiles = 0, pieces[2] = {0, 0};
     bool ok = true;
-    for (; w.left > 0; w.next(p, unit_tok)) {
+    for (; w.more; w.next(p, unit_tok)) {
       const bool pair = w.pair;
       const int ns = w.count(s);
       const int tok = (pair ? s * tile_tok : 0) + r_tok;   // token of the unit
