@@ -4,13 +4,15 @@
 //   y = R_p( g (.) x / sqrt(mean(x^2) + eps) )     x one head's Dh values
 //   R_p: (x_j, x_{j+Dh/2}) turned by the angle p * theta^(-2j/Dh)
 //
-// A group of Dh/8 lanes takes one (row, head): each lane holds elements
-// 4l..4l+3 of the first half and the same of the second, so a rotation's two
-// values sit in one thread and only the sum of squares crosses lanes (a fixed
-// shuffle tree). A block of 256 threads takes the heads of one row (of two to
-// four rows where there are few heads): the row's position, its page and its
-// cos / sin values are fetched once for all its heads. Statistics and the
-// rotation are fp32; each output is rounded once, to its storage type.
+// A group of Dh/16 lanes takes one (row, head): each lane holds elements
+// 8l .. 8l+7 of the first half and the same of the second in 16-byte accesses,
+// so a rotation's two values sit in one thread and only the sum of squares
+// crosses lanes (a fixed shuffle tree). A block of 256 threads takes the heads
+// of a few rows: a row's position, its page and its cos / sin values are
+// fetched once for all its heads, while the first heads are already on
+// their way. Statistics and the rotation are fp32; each output is rounded once,
+// to its storage type. Bound by the rows' bytes for many rows, by three
+// dependent loads (sequence, lengths or page, tables) for few.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -20,22 +22,47 @@ namespace dfl {
 namespace {
 
 constexpr int kRowThreads = 256;
-constexpr int kHeadsInFlight = 4;   // heads whose loads a group has in flight
+constexpr int kHeadsInFlight = 3;   // heads whose loads a group has in flight
 
-__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
-  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
-  return make_float4(a.x, a.y, b.x, b.y);
+// Eight elements as they lie in memory.
+template <typename T>
+struct Eight;
+template <>
+struct Eight<__nv_bfloat16> {
+  uint4 r;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { r = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(float* v) const {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {   // bf16 is the upper half of an fp32
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+};
+template <>
+struct Eight<float> {
+  float4 r[2];
+  __device__ __forceinline__ void load(const float* p) {
+    r[0] = *reinterpret_cast<const float4*>(p);
+    r[1] = *reinterpret_cast<const float4*>(p + 4);
+  }
+  __device__ __forceinline__ void get(float* v) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) { v[4 * i] = r[i].x; v[4 * i + 1] = r[i].y; v[4 * i + 2] = r[i].z; v[4 * i + 3] = r[i].w; }
+  }
+};
+__device__ __forceinline__ uint32_t two_bf16(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
 }
-__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
-  __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-  uint2 u;
-  u.x = *reinterpret_cast<uint32_t*>(&a);
-  u.y = *reinterpret_cast<uint32_t*>(&b);
-  *reinterpret_cast<uint2*>(p) = u;
+__device__ __forceinline__ void store8(float* p, const float* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v) {
+  *reinterpret_cast<uint4*>(p) =
+      make_uint4(two_bf16(v[0], v[1]), two_bf16(v[2], v[3]), two_bf16(v[4], v[5]), two_bf16(v[6], v[7]));
 }
 
 // The number of entries of cu[1..B] that are <= t, i.e. the sequence of packed
@@ -55,18 +82,36 @@ __device__ __forceinline__ int find_sequence(const int32_t* cu, int B, int t, in
 
 template <typename TI, typename TO, int DH, bool APPEND>
 __global__ void __launch_bounds__(kRowThreads) target_rows_kernel(const RowArgs p, int groups_per_row) {
-  constexpr int GL = DH / 8;                    // lanes per (row, head)
+  constexpr int GL = DH / 16;                   // lanes per (row, head)
   constexpr int NG = kRowThreads / GL;          // groups per block
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int group = threadIdx.x / GL, gl = threadIdx.x % GL;
   const int rows_per_block = NG / groups_per_row;
-  // groups_per_row is a power of two and a warp's groups may span two rows:
-  // the search below runs once per distinct row of the warp
+  // groups_per_row is a power of two; a warp's groups may span several rows
   const int t = blockIdx.x * rows_per_block + group / groups_per_row;
   const int sub = group % groups_per_row;
+  const int hq = p.q != nullptr ? p.n_q_heads : 0, hk = p.k != nullptr ? p.n_kv_heads : 0;
+  const int heads = hq + hk + (APPEND ? p.n_kv_heads : 0);
+  const TI* xq = static_cast<const TI*>(p.q) + t * p.ldq;
+  const TI* xk = static_cast<const TI*>(p.k) + t * p.ldk;
+  const TI* xv = static_cast<const TI*>(p.v) + t * p.ldv;
+  Eight<TI> lo[kHeadsInFlight], hi[kHeadsInFlight];
+  auto fetch = [&](int h0) {
+#pragma unroll
+    for (int i = 0; i < kHeadsInFlight; ++i) {
+      const int h = h0 + i * groups_per_row;
+      if (h < heads) {
+        const TI* x = h < hq ? xq + h * DH : h < hq + hk ? xk + (h - hq) * DH : xv + (h - hq - hk) * DH;
+        lo[i].load(x + 8 * gl);
+        hi[i].load(x + DH / 2 + 8 * gl);
+      }
+    }
+  };
   bool live = t < p.T;
+  if (live) fetch(sub);   // on its way while the row's place is looked up
+
   int pos = 0, page_row = 0;
   size_t page_base = 0;
   if (APPEND) {
@@ -105,50 +150,56 @@ __global__ void __launch_bounds__(kRowThreads) target_rows_kernel(const RowArgs 
       live = false;
     }
   }
-  const unsigned group_mask = GL == 32 ? 0xffffffffu : ((1u << GL) - 1u) << (lane / GL * GL);
+  const unsigned group_mask = ((1u << GL) - 1u) << (lane / GL * GL);
   if (!live) return;   // whole groups leave together
 
-  float4 cs = make_float4(1.f, 1.f, 1.f, 1.f), sn = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (p.rope_cos != nullptr) {
-    cs = load4(p.rope_cos + static_cast<size_t>(pos) * (DH / 2) + 4 * gl);
-    sn = load4(p.rope_sin + static_cast<size_t>(pos) * (DH / 2) + 4 * gl);
+  float cs[8], sn[8];
+  const bool turn = p.rope_cos != nullptr;
+  if (turn) {
+    Eight<float> c, s;
+    c.load(p.rope_cos + static_cast<size_t>(pos) * (DH / 2) + 8 * gl);
+    s.load(p.rope_sin + static_cast<size_t>(pos) * (DH / 2) + 8 * gl);
+    c.get(cs);
+    s.get(sn);
   }
-  const int hq = p.q != nullptr ? p.n_q_heads : 0, hk = p.k != nullptr ? p.n_kv_heads : 0;
-  const int hv = APPEND ? p.n_kv_heads : 0;
-  const TI* xq = static_cast<const TI*>(p.q) + t * p.ldq;
-  const TI* xk = static_cast<const TI*>(p.k) + t * p.ldk;
-  const TI* xv = static_cast<const TI*>(p.v) + t * p.ldv;
-  for (int h0 = sub; h0 < hq + hk + hv; h0 += kHeadsInFlight * groups_per_row) {
-    float4 lo[kHeadsInFlight], hi[kHeadsInFlight];
+  for (int h0 = sub; h0 < heads; h0 += kHeadsInFlight * groups_per_row) {
+    if (h0 != sub) fetch(h0);
 #pragma unroll
     for (int i = 0; i < kHeadsInFlight; ++i) {
       const int h = h0 + i * groups_per_row;
-      if (h < hq + hk + hv) {
-        const TI* x = h < hq ? xq + h * DH : h < hq + hk ? xk + (h - hq) * DH : xv + (h - hq - hk) * DH;
-        lo[i] = load4(x + 4 * gl);
-        hi[i] = load4(x + DH / 2 + 4 * gl);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kHeadsInFlight; ++i) {
-      const int h = h0 + i * groups_per_row;
-      if (h >= hq + hk + hv) break;   // uniform in the group
-      float4 a = lo[i], b = hi[i];
-      const bool is_v = h >= hq + hk;
-      const TO* gain = static_cast<const TO*>(h < hq ? p.g_q : p.g_k);
+      if (h >= heads) break;   // uniform in the group
+      float a[8], b[8];
+      lo[i].get(a);
+      hi[i].get(b);
+      const bool is_v = APPEND && h >= hq + hk;
       if (!is_v) {
+        const TO* gain = static_cast<const TO*>(h < hq ? p.g_q : p.g_k);
         if (gain != nullptr) {
-          float ss = a.x * a.x + a.y * a.y + a.z * a.z + a.w * a.w + b.x * b.x + b.y * b.y + b.z * b.z + b.w * b.w;
+          Eight<TO> ga, gb;
+          ga.load(gain + 8 * gl);
+          gb.load(gain + DH / 2 + 8 * gl);
+          float ss = 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) ss = fmaf(a[j], a[j], fmaf(b[j], b[j], ss));
 #pragma unroll
           for (int o = GL / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(group_mask, ss, o);
-          const float r = 1.0f / sqrtf(ss * (1.0f / DH) + p.eps);
-          const float4 ga = load4(gain + 4 * gl), gb = load4(gain + DH / 2 + 4 * gl);
-          a.x *= r * ga.x; a.y *= r * ga.y; a.z *= r * ga.z; a.w *= r * ga.w;
-          b.x *= r * gb.x; b.y *= r * gb.y; b.z *= r * gb.z; b.w *= r * gb.w;
+          const float r = rsqrtf(ss * (1.0f / DH) + p.eps);
+          float g[8];
+          ga.get(g);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) a[j] *= r * g[j];
+          gb.get(g);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) b[j] *= r * g[j];
         }
-        const float4 u = a, w = b;
-        a = make_float4(u.x * cs.x - w.x * sn.x, u.y * cs.y - w.y * sn.y, u.z * cs.z - w.z * sn.z, u.w * cs.w - w.w * sn.w);
-        b = make_float4(w.x * cs.x + u.x * sn.x, w.y * cs.y + u.y * sn.y, w.z * cs.z + u.z * sn.z, w.w * cs.w + u.w * sn.w);
+        if (turn) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float u = a[j], w = b[j];
+            a[j] = u * cs[j] - w * sn[j];
+            b[j] = w * cs[j] + u * sn[j];
+          }
+        }
       }
       TO* y;
       if (h < hq) {
@@ -159,20 +210,28 @@ __global__ void __launch_bounds__(kRowThreads) target_rows_kernel(const RowArgs 
       } else {
         y = static_cast<TO*>(p.k_out) + t * p.ldko + (h - hq) * DH;
       }
-      store4(y + 4 * gl, a);
-      store4(y + DH / 2 + 4 * gl, b);
+      store8(y + 8 * gl, a);
+      store8(y + DH / 2 + 8 * gl, b);
     }
   }
 }
 
 template <typename TI, typename TO, int DH, bool APPEND>
 cudaError_t launch_rows(const RowArgs& a, cudaStream_t s, bool pdl) {
-  constexpr int NG = kRowThreads / (DH / 8);
+  constexpr int NG = kRowThreads / (DH / 16);
   const int heads = (a.q != nullptr ? a.n_q_heads : 0) + (a.k != nullptr ? a.n_kv_heads : 0) +
                     (APPEND ? a.n_kv_heads : 0);
-  // groups of a row: as many as it has heads, up to the block's
+  // Groups of a row. Few rows: as many as the row has heads, for the most loads
+  // at once. Many rows: the split that leaves the fewest groups idle in a row's
+  // last round (40 heads: 8 groups in 5 rounds, not 32 in 2).
   int gpr = 1;
   while (gpr < NG && gpr < heads) gpr *= 2;
+  if (static_cast<long long>(a.T) * gpr > 2LL * NG * 8 * num_sms_of_current_device()) {
+    int best = gpr;
+    for (int g = gpr; g >= 4; g /= 2)
+      if ((heads + g - 1) / g * g < (heads + best - 1) / best * best) best = g;
+    gpr = best;
+  }
   const int rpb = NG / gpr;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((a.T + rpb - 1) / rpb));

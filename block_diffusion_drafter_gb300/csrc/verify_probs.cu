@@ -15,11 +15,14 @@
 // depend on their order, and the threshold floor(u * total) is an exact
 // 128-bit product. The acceptance products u * q are exact in 64-bit floats.
 //
-// One launch: a cluster of kParts CTAs takes a sequence, each a contiguous
-// part of its vocabulary, each warp a contiguous part of that. Every CTA runs
-// the acceptance test for itself (gamma independent lookups); the parts'
-// sums meet through distributed shared memory; the warp whose range holds the
-// threshold walks it once more (from L2) to the token.
+// One launch: a cluster of CTAs takes a sequence, each a contiguous part of its
+// vocabulary, each warp a contiguous part of that, in rows of 32 entries of
+// which eight are in flight (and the next eight requested). Every CTA runs the
+// acceptance test for itself (gamma independent lookups); the parts' sums meet
+// through distributed shared memory; the warp whose range holds the threshold
+// knows its groups' sums and reads one group once more (from L2) to find the
+// token. Bound by latency for few sequences (16 CTAs each), by the rows' bytes
+// and the conversions (26 integer instructions an entry) for many.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -28,18 +31,25 @@
 namespace dfl {
 namespace {
 
-constexpr int kParts = 8;            // CTAs of a cluster: the portable maximum
 constexpr int kProbThreads = 512;
 constexpr int kProbWarps = kProbThreads / 32;
-constexpr int kVec = 4;              // entries of a lane's step
+constexpr int kRows = 8;             // rows of 32 entries that a warp loads at once
+constexpr int kGroups = 8;           // groups of rows whose sums a warp keeps
 
 // floor(x * 2^62) for 0 <= x <= 1; NaN and negative values count as 0, values
-// above 1 as 1.
+// above 1 as 1. The mantissa, 1.0 = 2^62, shifted right by 127 - exponent (PTX
+// shifts by 32 and more give 0).
 __device__ __forceinline__ unsigned long long fixed62(float x) {
   const uint32_t u = __float_as_uint(fminf(fmaxf(x, 0.f), 1.f));
-  const int e = static_cast<int>(u >> 23);   // 0 .. 127
-  const unsigned long long m = static_cast<unsigned long long>((u & 0x7FFFFFu) | 0x800000u) << 39;   // 1.0 = 2^62
-  return e == 0 ? 0ull : m >> min(127 - e, 63);
+  const uint32_t n = 127u - (u >> 23);
+  const uint32_t m = ((u << 8) | 0x80000000u) >> 1;
+  uint32_t lo, hi;
+  asm("{\n\t.reg .u32 t, k;\n\t"
+      "max.u32 k, %3, 32;\n\tsub.u32 k, k, 32;\n\tshr.u32 t, %2, k;\n\t"
+      "shf.r.clamp.b32 %0, 0, t, %3;\n\tshr.u32 %1, %2, %3;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(m), "r"(n));
+  return static_cast<unsigned long long>(hi) << 32 | lo;
 }
 // floor(u * total), u clamped to [0, 1 - 2^-24].
 __device__ __forceinline__ unsigned long long threshold(float u, unsigned long long total) {
@@ -53,8 +63,8 @@ __device__ __forceinline__ unsigned long long threshold(float u, unsigned long l
   if (sh >= 64) return hi >> (sh - 64);
   return (hi << (64 - sh)) | (lo >> sh);     // hi < 2^24: the quotient fits
 }
-__device__ __forceinline__ float prob_at(const float* p) { return *p; }
-__device__ __forceinline__ float prob_at(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ float prob_at(const float* p) { return __ldg(p); }
+__device__ __forceinline__ float prob_at(const __nv_bfloat16* p) { return __bfloat162float(__ldg(p)); }
 
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
 #pragma unroll
@@ -67,30 +77,53 @@ __device__ __forceinline__ unsigned long long ld_dsmem_u64(uint32_t addr) {
   return v;
 }
 
+// The kRows rows of 32 entries from entry v0 on, this lane's of each: p_a and q_a.
 template <typename TT>
-__global__ void __cluster_dims__(kParts, 1, 1) __launch_bounds__(kProbThreads)
-    verify_probs_kernel(const ProbsArgs p) {
+struct Chunk {
+  float p[kRows], q[kRows];
+  __device__ __forceinline__ void load(const TT* row, const float* qrow, int v0, int end, int lane) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int v = v0 + 32 * i + lane;
+      p[i] = v < end ? prob_at(row + v) : 0.f;
+      q[i] = qrow != nullptr && v < end ? __ldg(qrow + v) : 0.f;
+    }
+  }
+  // weight of entry i: w, or p_a itself (whole)
+  __device__ __forceinline__ unsigned long long weight(int i, int v0, int lane, int out_token, bool whole) const {
+    const unsigned long long a = fixed62(p[i]);
+    if (whole) return a;
+    if (v0 + 32 * i + lane == out_token) return 0ull;
+    const unsigned long long b = fixed62(q[i]);
+    return a > b ? a - b : 0ull;
+  }
+};
+
+template <typename TT, int PARTS>
+__global__ void __launch_bounds__(kProbThreads) verify_probs_kernel(const ProbsArgs p) {
   __shared__ int s_a;
-  __shared__ unsigned long long s_left[kProbWarps], s_all[kProbWarps];   // sums of w and of p_a
+  __shared__ unsigned long long s_warp[2][kProbWarps];   // sums of w and, where w has no mass, of p_a
+  __shared__ unsigned long long s_group[kProbWarps][kGroups];
   __shared__ unsigned long long s_part[2];
   pdl_launch_dependents();
   pdl_wait();
-  const int part = blockIdx.x % kParts, b = blockIdx.x / kParts;
+  const int part = blockIdx.x % PARTS, b = blockIdx.x / PARTS;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int V = p.V, R = p.gamma + 1;
   const int g = p.gamma_b == nullptr ? p.gamma : min(max(p.gamma_b[b], 1), p.gamma);
   const TT* target = static_cast<const TT*>(p.target) + static_cast<size_t>(b) * R * V;
   const float* drafter = p.draft_probs == nullptr ? nullptr : p.draft_probs + static_cast<size_t>(b) * p.gamma * V;
   const int32_t* draft = p.draft + static_cast<size_t>(b) * p.gamma;
+  const float u_draw = p.u_draw[b];
 
   if (warp == 0) {
     bool keep = false;
     if (lane < g) {
       const int x = draft[lane];
+      const float u = p.u_accept[static_cast<size_t>(b) * p.gamma + lane];
       if (x >= 0 && x < V) {   // not a token: rejected
         const float pj = prob_at(target + static_cast<size_t>(lane) * V + x);
-        const float qj = drafter == nullptr ? 1.f : drafter[static_cast<size_t>(lane) * V + x];
-        const float u = p.u_accept[static_cast<size_t>(b) * p.gamma + lane];
+        const float qj = drafter == nullptr ? 1.f : __ldg(drafter + static_cast<size_t>(lane) * V + x);
         keep = static_cast<double>(u) * static_cast<double>(qj) < static_cast<double>(pj);
       }
     }
@@ -103,87 +136,85 @@ __global__ void __cluster_dims__(kParts, 1, 1) __launch_bounds__(kProbThreads)
   const float* qrow = a < g && drafter != nullptr ? drafter + static_cast<size_t>(a) * V : nullptr;
   const int out_token = a < g && drafter == nullptr ? draft[a] : -1;   // greedy drafter's rejected token
 
-  // entries [begin, end) of this warp: whole steps of 32 * kVec
-  constexpr int kStep = 32 * kVec;
-  const int steps = (V + kStep - 1) / kStep, shares = kParts * kProbWarps;
-  const int id = part * kProbWarps + warp;
-  const int begin = static_cast<int>(static_cast<long long>(steps) * id / shares) * kStep;
-  const int end = min(V, static_cast<int>(static_cast<long long>(steps) * (id + 1) / shares) * kStep);
-  // weights of the kVec entries from v on: w (left) and p_a (all)
-  auto weights = [&](int v, unsigned long long* left, unsigned long long* all) {
+  // this warp's entries [begin, end), in groups of whole chunks
+  constexpr int kChunk = 32 * kRows;
+  const int rows = (V + 31) / 32, shares = PARTS * kProbWarps, id = part * kProbWarps + warp;
+  const int r0 = static_cast<int>(static_cast<long long>(rows) * id / shares);
+  const int r1 = static_cast<int>(static_cast<long long>(rows) * (id + 1) / shares);
+  const int begin = r0 * 32, end = min(V, r1 * 32);
+  const int group = ((r1 - r0 + kGroups - 1) / kGroups + kRows - 1) / kRows * kChunk;   // entries of a group
+  auto sum_up = [&](bool whole) {
+    unsigned long long all = 0ull, sum = 0ull;
+    int left = group, at = 0;
+    Chunk<TT> now, then;
+    if (begin < end) now.load(row, qrow, begin, end, lane);
+    for (int v0 = begin; v0 < end; v0 += kChunk) {
+      if (v0 + kChunk < end) then.load(row, qrow, v0 + kChunk, end, lane);
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      left[i] = all[i] = 0ull;
-      if (v + i < end) {
-        all[i] = fixed62(prob_at(row + v + i));
-        const unsigned long long q = qrow != nullptr ? fixed62(qrow[v + i]) : (v + i == out_token ? all[i] : 0ull);
-        left[i] = all[i] > q ? all[i] - q : 0ull;
+      for (int i = 0; i < kRows; ++i) sum += now.weight(i, v0, lane, out_token, whole);
+      now = then;
+      left -= kChunk;
+      if (left == 0 || v0 + kChunk >= end) {
+        sum = warp_sum(sum);
+        if (lane == 0) s_group[warp][at] = sum;
+        all += sum;
+        sum = 0ull;
+        left = group;
+        ++at;
       }
     }
-  };
-  unsigned long long sum_left = 0ull, sum_all = 0ull;
-  for (int v0 = begin; v0 < end; v0 += kStep) {
-    unsigned long long l[kVec], w[kVec];
-    weights(v0 + lane * kVec, l, w);
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) { sum_left += l[i]; sum_all += w[i]; }
-  }
-  sum_left = warp_sum(sum_left);
-  sum_all = warp_sum(sum_all);
-  if (lane == 0) { s_left[warp] = sum_left; s_all[warp] = sum_all; }
-  __syncthreads();
-  if (threadIdx.x < 2) {
-    const unsigned long long* s = threadIdx.x == 0 ? s_left : s_all;
-    unsigned long long t = 0ull;
-    for (int w = 0; w < kProbWarps; ++w) t += s[w];
-    s_part[threadIdx.x] = t;
-  }
-  cluster_sync();
-  // the parts' sums in vocabulary order
-  unsigned long long before[2] = {0ull, 0ull}, total[2] = {0ull, 0ull};
-#pragma unroll
-  for (int r = 0; r < kParts; ++r) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const unsigned long long t = ld_dsmem_u64(mapa_shared(smem_u32(&s_part[k]), r));
-      if (r < part) before[k] += t;
-      total[k] += t;
+    if (lane == 0) s_warp[whole ? 1 : 0][warp] = all;
+    __syncthreads();
+    if (warp == 0) {
+      const unsigned long long t = warp_sum(lane < kProbWarps ? s_warp[whole ? 1 : 0][lane] : 0ull);
+      if (lane == 0) s_part[whole ? 1 : 0] = t;
     }
+    return all;
+  };
+  // the sum before this part and over all parts, in vocabulary order
+  unsigned long long before = 0ull, total = 0ull;
+  auto join = [&](int k) {
+    before = total = 0ull;
+    unsigned long long t = lane < PARTS ? ld_dsmem_u64(mapa_shared(smem_u32(&s_part[k]), lane)) : 0ull;
+    total = warp_sum(t);
+    before = warp_sum(lane < part ? t : 0ull);
+  };
+  unsigned long long mine = sum_up(false);
+  cluster_sync();
+  join(0);
+  bool whole = false;
+  if (total == 0ull) {   // no residual mass anywhere: p_a itself (the whole cluster goes this way)
+    cluster_sync();      // s_group and s_warp are read no more
+    whole = true;
+    mine = sum_up(true);
+    cluster_sync();
+    join(1);
   }
-  cluster_arrive();   // this CTA's reads of its peers are done
-  const int k = total[0] > 0ull ? 0 : 1;   // no residual mass: p_a itself
-  const unsigned long long thr = threshold(p.u_draw[b], total[k]);
-  unsigned long long cum = before[k];
-  for (int w = 0; w < warp; ++w) cum += k == 0 ? s_left[w] : s_all[w];
-  const unsigned long long mine = k == 0 ? sum_left : sum_all;
+  cluster_arrive();      // this CTA's reads of its peers are done
+  const unsigned long long thr = threshold(u_draw, total);
+  unsigned long long cum = before + warp_sum(lane < warp ? s_warp[whole ? 1 : 0][lane] : 0ull);
   int y = -1;
-  if (total[k] == 0ull) {   // nothing to draw from
+  if (total == 0ull) {   // nothing to draw from
     if (id == 0 && lane == 0) report(p.dev_status, DFLASH_ERR_INVALID_ARG);
     if (id == 0) y = 0;
   } else if (cum <= thr && thr - cum < mine) {
-    for (int v0 = begin; v0 < end; v0 += kStep) {
-      unsigned long long l[kVec], w[kVec], c[kVec];
-      weights(v0 + lane * kVec, l, w);
-      unsigned long long s = 0ull;
+    int v0 = begin;
+    for (int at = 0; thr - cum >= s_group[warp][at]; ++at, v0 += group) cum += s_group[warp][at];
+    for (; y < 0 && v0 < end; v0 += kChunk) {
+      Chunk<TT> c;
+      c.load(row, qrow, v0, end, lane);
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) { s += k == 0 ? l[i] : w[i]; c[i] = s; }
-      unsigned long long incl = s;   // inclusive prefix over the lanes
+      for (int i = 0; i < kRows; ++i) {
+        unsigned long long incl = c.weight(i, v0, lane, out_token, whole);   // inclusive prefix over the lanes
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long t = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += t;
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned long long t = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += t;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, cum + incl > thr);
+        if (hit != 0u && y < 0) y = v0 + 32 * i + __ffs(static_cast<int>(hit)) - 1;
+        cum += __shfl_sync(0xffffffffu, incl, 31);
       }
-      const unsigned hit = __ballot_sync(0xffffffffu, cum + incl > thr);
-      if (hit != 0u) {
-        const int src = __ffs(static_cast<int>(hit)) - 1;
-        int at = 0;
-#pragma unroll
-        for (int i = kVec - 1; i >= 0; --i)
-          if (cum + (incl - s) + c[i] > thr) at = i;
-        y = __shfl_sync(0xffffffffu, v0 + lane * kVec + at, src);
-        break;
-      }
-      cum += __shfl_sync(0xffffffffu, incl, 31);
     }
   }
   if (y >= 0) {   // one warp of the cluster
@@ -194,28 +225,49 @@ __global__ void __cluster_dims__(kParts, 1, 1) __launch_bounds__(kProbThreads)
       p.next_anchor[b] = y;
     }
   }
-  cluster_wait();     // no peer reads this CTA's sums any more
+  cluster_wait();        // no peer reads this CTA's sums any more
+}
+
+template <typename TT, int PARTS>
+cudaError_t launch_probs(const ProbsArgs& a, cudaStream_t s, bool pdl) {
+  if (PARTS > 8) {
+    static bool done[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (!done[dev & 63]) {
+      const cudaError_t e =
+          cudaFuncSetAttribute(verify_probs_kernel<TT, PARTS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return e;
+      done[dev & 63] = true;
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.B) * PARTS);
+  cfg.blockDim = dim3(kProbThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = PARTS;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, verify_probs_kernel<TT, PARTS>, a);
 }
 
 template <typename TT>
-cudaError_t launch_probs(const ProbsArgs& a, cudaStream_t s, bool pdl) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.B) * kParts);
-  cfg.blockDim = dim3(kProbThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = pdl ? attr : nullptr;
-  cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, verify_probs_kernel<TT>, a);
+cudaError_t launch_typed(const ProbsArgs& a, cudaStream_t s, bool pdl) {
+  // 16 CTAs a sequence while every one of them can have an SM of its own
+  return 16 * a.B <= num_sms_of_current_device() ? launch_probs<TT, 16>(a, s, pdl) : launch_probs<TT, 8>(a, s, pdl);
 }
 
 }  // namespace
 
 cudaError_t launch_verify_probs(const ProbsArgs& a, cudaStream_t s, bool pdl) {
   if (a.gamma > DFLASH_MAX_GAMMA) return cudaErrorInvalidValue;
-  return a.target_bf16 ? launch_probs<__nv_bfloat16>(a, s, pdl) : launch_probs<float>(a, s, pdl);
+  return a.target_bf16 ? launch_typed<__nv_bfloat16>(a, s, pdl) : launch_typed<float>(a, s, pdl);
 }
 
 }  // namespace dfl
