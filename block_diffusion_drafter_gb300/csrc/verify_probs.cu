@@ -22,7 +22,7 @@
 // through distributed shared memory; the warp whose range holds the threshold
 // knows its groups' sums and reads one group once more (from L2) to find the
 // token. Bound by latency for few sequences (16 CTAs each), by the rows' bytes
-// and the conversions (26 integer instructions an entry) for many.
+// and the conversions (30 integer instructions an entry) for many.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -37,19 +37,32 @@ constexpr int kRows = 8;             // rows of 32 entries that a warp loads at 
 constexpr int kGroups = 8;           // groups of rows whose sums a warp keeps
 
 // floor(x * 2^62) for 0 <= x <= 1; NaN and negative values count as 0, values
-// above 1 as 1. The mantissa, 1.0 = 2^62, shifted right by 127 - exponent (PTX
-// shifts by 32 and more give 0).
-__device__ __forceinline__ unsigned long long fixed62(float x) {
-  const uint32_t u = __float_as_uint(fminf(fmaxf(x, 0.f), 1.f));
-  const uint32_t n = 127u - (u >> 23);
-  const uint32_t m = ((u << 8) | 0x80000000u) >> 1;
+// above 1 as 1 (a saturating move). The mantissa, 1.0 = 2^62, shifted right by
+// 127 - exponent (PTX shifts by 32 and more give 0).
+struct Fixed {
   uint32_t lo, hi;
+  __device__ __forceinline__ unsigned long long value() const { return static_cast<unsigned long long>(hi) << 32 | lo; }
+};
+__device__ __forceinline__ Fixed fixed62(float x) {
+  const uint32_t u = __float_as_uint(__saturatef(x));
+  const uint32_t n = 127u - (u >> 23);
+  const uint32_t m = ((u & 0x7FFFFFu) | 0x800000u) << 7;
+  Fixed f;
   asm("{\n\t.reg .u32 t, k;\n\t"
       "max.u32 k, %3, 32;\n\tsub.u32 k, k, 32;\n\tshr.u32 t, %2, k;\n\t"
       "shf.r.clamp.b32 %0, 0, t, %3;\n\tshr.u32 %1, %2, %3;\n\t}"
-      : "=r"(lo), "=r"(hi)
+      : "=r"(f.lo), "=r"(f.hi)
       : "r"(m), "r"(n));
-  return static_cast<unsigned long long>(hi) << 32 | lo;
+  return f;
+}
+// max(a - b, 0)
+__device__ __forceinline__ Fixed minus(Fixed a, Fixed b) {
+  Fixed d;
+  asm("{\n\t.reg .u32 m;\n\tsub.cc.u32 %0, %2, %4;\n\tsubc.cc.u32 %1, %3, %5;\n\tsubc.u32 m, 0, 0;\n\t"
+      "not.b32 m, m;\n\tand.b32 %0, %0, m;\n\tand.b32 %1, %1, m;\n\t}"
+      : "=&r"(d.lo), "=&r"(d.hi)
+      : "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi));
+  return d;
 }
 // floor(u * total), u clamped to [0, 1 - 2^-24].
 __device__ __forceinline__ unsigned long long threshold(float u, unsigned long long total) {
@@ -77,27 +90,93 @@ __device__ __forceinline__ unsigned long long ld_dsmem_u64(uint32_t addr) {
   return v;
 }
 
-// The kRows rows of 32 entries from entry v0 on, this lane's of each: p_a and q_a.
-template <typename TT>
+// The kRows rows of 32 entries from entry v0 on, this lane's of each: p_a and,
+// where the drafter drew (DREW), q_a.
+template <typename TT, bool DREW>
 struct Chunk {
-  float p[kRows], q[kRows];
+  float p[kRows], q[DREW ? kRows : 1];
   __device__ __forceinline__ void load(const TT* row, const float* qrow, int v0, int end, int lane) {
+    const TT* a = row + v0 + lane;
+    const float* b = qrow + v0 + lane;
+    if (v0 + 32 * kRows <= end) {   // offsets known at compile time, nothing to test
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const int v = v0 + 32 * i + lane;
-      p[i] = v < end ? prob_at(row + v) : 0.f;
-      q[i] = qrow != nullptr && v < end ? __ldg(qrow + v) : 0.f;
+      for (int i = 0; i < kRows; ++i) {
+        p[i] = prob_at(a + 32 * i);
+        if (DREW) q[i] = __ldg(b + 32 * i);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const bool in = v0 + 32 * i + lane < end;
+        p[i] = in ? prob_at(a + 32 * i) : 0.f;
+        if (DREW) q[i] = in ? __ldg(b + 32 * i) : 0.f;
+      }
     }
   }
-  // weight of entry i: w, or p_a itself (whole)
-  __device__ __forceinline__ unsigned long long weight(int i, int v0, int lane, int out_token, bool whole) const {
-    const unsigned long long a = fixed62(p[i]);
-    if (whole) return a;
-    if (v0 + 32 * i + lane == out_token) return 0ull;
-    const unsigned long long b = fixed62(q[i]);
-    return a > b ? a - b : 0ull;
+  // weight of entry i: w, or p_a itself where the draft is a greedy drafter's and is not `out`
+  __device__ __forceinline__ unsigned long long weight(int i, int v0, int lane, int out) const {
+    const Fixed a = fixed62(p[i]);
+    if (DREW) return minus(a, fixed62(q[i])).value();
+    return v0 + 32 * i + lane == out ? 0ull : a.value();
   }
 };
+
+// This warp's entries [begin, end) in groups of whole chunks: the sum of the
+// weights of the range, and of each group into sums[].
+template <typename TT, bool DREW>
+__device__ __forceinline__ unsigned long long sum_range(const TT* row, const float* qrow, int begin, int end, int group,
+                                                        int out, int lane, unsigned long long* sums) {
+  constexpr int kChunk = 32 * kRows;
+  unsigned long long all = 0ull, sum = 0ull;
+  int left = group, at = 0;
+  Chunk<TT, DREW> even, odd;
+  auto take = [&](const Chunk<TT, DREW>& c, int v0) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) sum += c.weight(i, v0, lane, out);
+    left -= kChunk;
+    if (left == 0 || v0 + kChunk >= end) {
+      sum = warp_sum(sum);
+      if (lane == 0) sums[at] = sum;
+      all += sum;
+      sum = 0ull;
+      left = group;
+      ++at;
+    }
+  };
+  if (begin < end) even.load(row, qrow, begin, end, lane);
+  for (int v0 = begin; v0 < end; v0 += 2 * kChunk) {   // the next chunk is on its way while one is taken
+    const bool two = v0 + kChunk < end;
+    if (two) odd.load(row, qrow, v0 + kChunk, end, lane);
+    take(even, v0);
+    if (v0 + 2 * kChunk < end) even.load(row, qrow, v0 + 2 * kChunk, end, lane);
+    if (two) take(odd, v0 + kChunk);
+  }
+  return all;
+}
+
+// The first entry of [v0, end) at which the running sum, cum before it, exceeds thr.
+template <typename TT, bool DREW>
+__device__ __forceinline__ int find_entry(const TT* row, const float* qrow, int v0, int end, int out, int lane,
+                                          unsigned long long cum, unsigned long long thr) {
+  int y = -1;
+  for (; y < 0 && v0 < end; v0 += 32 * kRows) {
+    Chunk<TT, DREW> c;
+    c.load(row, qrow, v0, end, lane);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      unsigned long long incl = c.weight(i, v0, lane, out);   // inclusive prefix over the lanes
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, cum + incl > thr);
+      if (hit != 0u && y < 0) y = v0 + 32 * i + __ffs(static_cast<int>(hit)) - 1;
+      cum += __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
+  return y;
+}
 
 template <typename TT, int PARTS>
 __global__ void __launch_bounds__(kProbThreads) verify_probs_kernel(const ProbsArgs p) {
@@ -137,62 +216,39 @@ __global__ void __launch_bounds__(kProbThreads) verify_probs_kernel(const ProbsA
   const int out_token = a < g && drafter == nullptr ? draft[a] : -1;   // greedy drafter's rejected token
 
   // this warp's entries [begin, end), in groups of whole chunks
-  constexpr int kChunk = 32 * kRows;
   const int rows = (V + 31) / 32, shares = PARTS * kProbWarps, id = part * kProbWarps + warp;
-  const int r0 = static_cast<int>(static_cast<long long>(rows) * id / shares);
-  const int r1 = static_cast<int>(static_cast<long long>(rows) * (id + 1) / shares);
-  const int begin = r0 * 32, end = min(V, r1 * 32);
-  const int group = ((r1 - r0 + kGroups - 1) / kGroups + kRows - 1) / kRows * kChunk;   // entries of a group
-  auto sum_up = [&](bool whole) {
-    unsigned long long all = 0ull, sum = 0ull;
-    int left = group, at = 0;
-    Chunk<TT> now, then;
-    if (begin < end) now.load(row, qrow, begin, end, lane);
-    for (int v0 = begin; v0 < end; v0 += kChunk) {
-      if (v0 + kChunk < end) then.load(row, qrow, v0 + kChunk, end, lane);
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) sum += now.weight(i, v0, lane, out_token, whole);
-      now = then;
-      left -= kChunk;
-      if (left == 0 || v0 + kChunk >= end) {
-        sum = warp_sum(sum);
-        if (lane == 0) s_group[warp][at] = sum;
-        all += sum;
-        sum = 0ull;
-        left = group;
-        ++at;
-      }
-    }
-    if (lane == 0) s_warp[whole ? 1 : 0][warp] = all;
-    __syncthreads();
-    if (warp == 0) {
-      const unsigned long long t = warp_sum(lane < kProbWarps ? s_warp[whole ? 1 : 0][lane] : 0ull);
-      if (lane == 0) s_part[whole ? 1 : 0] = t;
-    }
-    return all;
-  };
-  // the sum before this part and over all parts, in vocabulary order
-  unsigned long long before = 0ull, total = 0ull;
+  const int begin = static_cast<int>(static_cast<long long>(rows) * id / shares) * 32;
+  const int end = min(V, static_cast<int>(static_cast<long long>(rows) * (id + 1) / shares) * 32);
+  const int group = (((end - begin + 31) / 32 + kGroups - 1) / kGroups + kRows - 1) / kRows * kRows * 32;   // entries of a group
+  // the sums of this warp, of the warps before it in the part, of the parts before and of all
+  unsigned long long mine, before, total;
   auto join = [&](int k) {
-    before = total = 0ull;
-    unsigned long long t = lane < PARTS ? ld_dsmem_u64(mapa_shared(smem_u32(&s_part[k]), lane)) : 0ull;
-    total = warp_sum(t);
-    before = warp_sum(lane < part ? t : 0ull);
-  };
-  unsigned long long mine = sum_up(false);
-  cluster_sync();
-  join(0);
-  bool whole = false;
-  if (total == 0ull) {   // no residual mass anywhere: p_a itself (the whole cluster goes this way)
-    cluster_sync();      // s_group and s_warp are read no more
-    whole = true;
-    mine = sum_up(true);
+    if (lane == 0) s_warp[k][warp] = mine;
+    __syncthreads();
+    const unsigned long long w = lane < kProbWarps ? s_warp[k][lane] : 0ull;
+    if (warp == 0) {
+      const unsigned long long t = warp_sum(w);
+      if (lane == 0) s_part[k] = t;
+    }
     cluster_sync();
+    const unsigned long long t = lane < PARTS ? ld_dsmem_u64(mapa_shared(smem_u32(&s_part[k]), lane)) : 0ull;
+    total = warp_sum(t);
+    before = warp_sum((lane < part ? t : 0ull) + (lane < warp ? w : 0ull));
+  };
+  mine = qrow != nullptr ? sum_range<TT, true>(row, qrow, begin, end, group, -1, lane, s_group[warp])
+                         : sum_range<TT, false>(row, nullptr, begin, end, group, out_token, lane, s_group[warp]);
+  join(0);
+  bool whole = qrow == nullptr;
+  int out = out_token;
+  if (total == 0ull) {   // no residual mass anywhere: p_a itself (the whole cluster goes this way)
+    whole = true;
+    out = -1;
+    mine = sum_range<TT, false>(row, nullptr, begin, end, group, -1, lane, s_group[warp]);
     join(1);
   }
   cluster_arrive();      // this CTA's reads of its peers are done
   const unsigned long long thr = threshold(u_draw, total);
-  unsigned long long cum = before + warp_sum(lane < warp ? s_warp[whole ? 1 : 0][lane] : 0ull);
+  unsigned long long cum = before;
   int y = -1;
   if (total == 0ull) {   // nothing to draw from
     if (id == 0 && lane == 0) report(p.dev_status, DFLASH_ERR_INVALID_ARG);
@@ -200,22 +256,8 @@ __global__ void __launch_bounds__(kProbThreads) verify_probs_kernel(const ProbsA
   } else if (cum <= thr && thr - cum < mine) {
     int v0 = begin;
     for (int at = 0; thr - cum >= s_group[warp][at]; ++at, v0 += group) cum += s_group[warp][at];
-    for (; y < 0 && v0 < end; v0 += kChunk) {
-      Chunk<TT> c;
-      c.load(row, qrow, v0, end, lane);
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        unsigned long long incl = c.weight(i, v0, lane, out_token, whole);   // inclusive prefix over the lanes
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const unsigned long long t = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += t;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, cum + incl > thr);
-        if (hit != 0u && y < 0) y = v0 + 32 * i + __ffs(static_cast<int>(hit)) - 1;
-        cum += __shfl_sync(0xffffffffu, incl, 31);
-      }
-    }
+    y = whole ? find_entry<TT, false>(row, nullptr, v0, end, out, lane, cum, thr)
+              : find_entry<TT, true>(row, qrow, v0, end, -1, lane, cum, thr);
   }
   if (y >= 0) {   // one warp of the cluster
     if (lane <= p.gamma)
@@ -259,8 +301,13 @@ cudaError_t launch_probs(const ProbsArgs& a, cudaStream_t s, bool pdl) {
 
 template <typename TT>
 cudaError_t launch_typed(const ProbsArgs& a, cudaStream_t s, bool pdl) {
-  // 16 CTAs a sequence while every one of them can have an SM of its own
-  return 16 * a.B <= num_sms_of_current_device() ? launch_probs<TT, 16>(a, s, pdl) : launch_probs<TT, 8>(a, s, pdl);
+  // as many CTAs a sequence as are all resident at once (two an SM): at 64
+  // sequences 8 CTAs each ran in two waves of the same latency
+  const long long slots = 2LL * num_sms_of_current_device();
+  if (16LL * a.B <= slots) return launch_probs<TT, 16>(a, s, pdl);
+  if (8LL * a.B <= slots) return launch_probs<TT, 8>(a, s, pdl);
+  if (4LL * a.B <= slots) return launch_probs<TT, 4>(a, s, pdl);
+  return launch_probs<TT, 2>(a, s, pdl);
 }
 
 }  // namespace
