@@ -15,20 +15,23 @@ namespace {
 constexpr float kLog2eC = 1.4426950408889634f;
 
 // ------------------------------------------------------------------ fp32
-// One CTA per (unit of kSimtRows packed rows, KV head, split). Keys in tiles
-// of kSimtKeys through shared memory; thread (ty, tx) of 16 x 16 holds a 4 x 4
-// piece of the score tile and rows 4 ty.. x columns tx + 16 c of the output.
-constexpr int kSimtRows = 64, kSimtKeys = 64, kSimtThreads = 256;
+// One CTA per (unit of 16 RT packed rows, KV head, split). Keys in tiles of
+// kSimtKeys through shared memory; thread (ty, tx) of 16 x 16 holds an RT x 4 piece
+// of the score tile and rows RT ty.. x columns tx + 16 c of the output. RT is 4,
+// or less where the chunks are hinted to have fewer rows (a drafted block of 17
+// rows of one head each: 32 rows a unit instead of 64).
+constexpr int kSimtKeys = 64, kSimtThreads = 256;
 
-template <int DH>
+template <int DH, int RT>
 constexpr size_t simt_smem() {
-  return sizeof(float) * (static_cast<size_t>(kSimtRows + 2 * kSimtKeys) * (DH + 4) + kSimtRows * (kSimtKeys + 4));
+  return sizeof(float) * (static_cast<size_t>(16 * RT + 2 * kSimtKeys) * (DH + 4) + 16 * RT * (kSimtKeys + 4));
 }
 
-template <int DH>
+template <int DH, int RT>
 __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkArgs p, int splits) {
   extern __shared__ __align__(16) float sm[];
-  constexpr int LD = DH + 4, LP = kSimtKeys + 4, DC = DH / 16;
+  constexpr int kSimtRows = 16 * RT;
+  constexpr int LD = DH + 4, LP = kSimtKeys + 4, DC = DH / 16, D4 = DH / 4;
   float* sq = sm;
   float* sk = sq + kSimtRows * LD;
   float* sv = sk + kSimtKeys * LD;
@@ -60,19 +63,22 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkArg
   const int t0 = static_cast<int>(static_cast<long long>(tiles) * sp_i / splits);
   const int t1 = static_cast<int>(static_cast<long long>(tiles) * (sp_i + 1) / splits);
   const float* q = static_cast<const float*>(p.q);
-  for (int i = threadIdx.x; i < kSimtRows * DH; i += kSimtThreads) {
-    const int r = i / DH, d = i % DH;
-    sq[r * LD + d] = r < rows ? q[(u.row0 + u.tok0 + r / G) * p.ldq + (kvh * G + r % G) * DH + d] : 0.f;
-  }
-  int lim[4];      // keys that row 4 ty + i sees
+  const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 4 * ty + i;
+  for (int i = threadIdx.x; i < kSimtRows * D4; i += kSimtThreads) {
+    const int r = i / D4, d = i % D4 * 4;
+    *reinterpret_cast<float4*>(&sq[r * LD + d]) =
+        r < rows ? *reinterpret_cast<const float4*>(&q[(u.row0 + u.tok0 + r / G) * p.ldq + (kvh * G + r % G) * DH + d]) : none;
+  }
+  int lim[RT];     // keys that row RT ty + i sees
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const int r = RT * ty + i;
     lim[i] = r < rows ? row_keys(p, u, u.tok0 + r / G) : 0;
   }
-  float m[4], l[4], o[4][DC];
+  float m[RT], l[RT], o[RT][DC];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < RT; ++i) {
     m[i] = -INFINITY;
     l[i] = 0.f;
 #pragma unroll
@@ -86,33 +92,36 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkArg
     const int page = page_of(p, u.b, k0);
     const size_t base = ((static_cast<size_t>(p.layer) * p.pages.n_pages + page) * p.n_kv_heads + kvh) *
                             static_cast<size_t>(kPageKeys) + k0 % kPageKeys;
-    for (int i = threadIdx.x; i < kSimtKeys * DH; i += kSimtThreads) {
-      const int r = i / DH, d = i % DH;
+    const float* kg = static_cast<const float*>(p.k_pool) + base * DH;
+    const float* vg = static_cast<const float*>(p.v_pool) + base * DH;
+#pragma unroll
+    for (int i = threadIdx.x; i < kSimtKeys * D4; i += kSimtThreads) {
+      const int r = i / D4, d = i % D4 * 4;
       const bool in = k0 + r < keys;   // rows behind the last key may hold anything
-      sk[r * LD + d] = in ? static_cast<const float*>(p.k_pool)[(base + r) * DH + d] : 0.f;
-      sv[r * LD + d] = in ? static_cast<const float*>(p.v_pool)[(base + r) * DH + d] : 0.f;
+      *reinterpret_cast<float4*>(&sk[r * LD + d]) = in ? *reinterpret_cast<const float4*>(&kg[r * DH + d]) : none;
+      *reinterpret_cast<float4*>(&sv[r * LD + d]) = in ? *reinterpret_cast<const float4*>(&vg[r * DH + d]) : none;
     }
     __syncthreads();
-    float s[4][4];
+    float s[RT][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < RT; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
 #pragma unroll 4
     for (int d = 0; d < DH; d += 4) {
-      float4 a[4], b[4];
+      float4 a[RT], b[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(&sq[(4 * ty + i) * LD + d]);
+      for (int i = 0; i < RT; ++i) a[i] = *reinterpret_cast<const float4*>(&sq[(RT * ty + i) * LD + d]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(&sk[(tx + 16 * j) * LD + d]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           s[i][j] += a[i].x * b[j].x + a[i].y * b[j].y + a[i].z * b[j].z + a[i].w * b[j].w;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RT; ++i) {
       float mx = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -129,7 +138,7 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkArg
       for (int j = 0; j < 4; ++j) {
         const float e = exp2f(s[i][j] - ref);
         sum += e;
-        sp[(4 * ty + i) * LP + tx + 16 * j] = e;
+        sp[(RT * ty + i) * LP + tx + 16 * j] = e;
       }
 #pragma unroll
       for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
@@ -141,20 +150,20 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkArg
     __syncwarp();   // a warp's rows of sp are its own
 #pragma unroll 4
     for (int j = 0; j < kSimtKeys; ++j) {
-      float pr[4];
+      float pr[RT];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) pr[i] = sp[(4 * ty + i) * LP + j];
+      for (int i = 0; i < RT; ++i) pr[i] = sp[(RT * ty + i) * LP + j];
 #pragma unroll
       for (int c = 0; c < DC; ++c) {
         const float v = sv[j * LD + tx + 16 * c];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i][c] += pr[i] * v;
+        for (int i = 0; i < RT; ++i) o[i][c] += pr[i] * v;
       }
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 4 * ty + i;
+  for (int i = 0; i < RT; ++i) {
+    const int r = RT * ty + i;
     if (r >= rows) continue;
     if (splits == 1) {
       const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
@@ -260,40 +269,50 @@ cudaError_t launch_plain(K kernel, dim3 grid, int threads, size_t smem, cudaStre
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int DH>
+template <int DH, int RT>
 cudaError_t launch_simt(const ChunkArgs& a, cudaStream_t s, bool pdl, Tracer& tr, double bytes, double flops) {
-  const int tok = kSimtRows / (a.n_q_heads / a.n_kv_heads);
+  constexpr int rows = 16 * RT;
+  const int tok = rows / (a.n_q_heads / a.n_kv_heads);
   // at most: every sequence's last unit holds one row
   const long long units = (static_cast<long long>(a.T) + static_cast<long long>(a.B) * (tok - 1)) / tok;
   const long long work = units * a.n_kv_heads;
   int splits = 1;
-  if (work < num_sms_of_current_device()) {
+  if (work > 0 && work < num_sms_of_current_device()) {
     const int tiles = (a.max_ctx + a.max_rows + kSimtKeys - 1) / kSimtKeys;
-    splits = static_cast<int>(2LL * num_sms_of_current_device() / (work > 0 ? work : 1));
+    splits = static_cast<int>(2LL * num_sms_of_current_device() / work);
     if (splits > kChunkSlots / work) splits = static_cast<int>(kChunkSlots / work);
-    if (splits > tiles / 2) splits = tiles / 2;
+    if (splits > tiles) splits = tiles;
     if (splits < 1) splits = 1;
   }
-  constexpr size_t smem = simt_smem<DH>();
+  constexpr size_t smem = simt_smem<DH, RT>();
   static bool done[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
   if (!done[dev & 63]) {
-    const cudaError_t e = cudaFuncSetAttribute(chunk_simt_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(chunk_simt_kernel<DH, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     done[dev & 63] = true;
   }
   tr.before(DFLASH_K_ATTN, bytes, flops);
-  cudaError_t e = launch_plain(chunk_simt_kernel<DH>,
+  cudaError_t e = launch_plain(chunk_simt_kernel<DH, RT>,
                                dim3(static_cast<unsigned>(units), a.n_kv_heads, splits), kSimtThreads, smem, s, pdl, a,
                                splits);
   tr.after();
   if (e != cudaSuccess || splits == 1) return e;
   tr.before(DFLASH_K_ATTN, 0.0, 0.0);
-  e = launch_plain(chunk_merge_kernel<float, DH>, dim3(static_cast<unsigned>(work), kSimtRows / 8), 128, 0, s, pdl, a);
+  e = launch_plain(chunk_merge_kernel<float, DH>, dim3(static_cast<unsigned>(work), rows / 8), 128, 0, s, pdl, a);
   tr.after();
   return e;
+}
+
+template <int DH>
+cudaError_t launch_f32(const ChunkArgs& a, cudaStream_t s, bool pdl, Tracer& tr, double bytes, double flops) {
+  const int G = a.n_q_heads / a.n_kv_heads;
+  const long long rows = static_cast<long long>(a.max_rows) * G;
+  if (rows <= 16 && G <= 16) return launch_simt<DH, 1>(a, s, pdl, tr, bytes, flops);
+  if (rows <= 32 && G <= 32) return launch_simt<DH, 2>(a, s, pdl, tr, bytes, flops);
+  return launch_simt<DH, 4>(a, s, pdl, tr, bytes, flops);
 }
 
 }  // namespace
@@ -302,7 +321,7 @@ cudaError_t launch_attention_chunk(const ChunkArgs& a, int bf16, cudaStream_t s,
                                    double flops) {
   if (a.head_dim != 64 && a.head_dim != 128) return cudaErrorInvalidValue;
   if (!bf16)
-    return a.head_dim == 128 ? launch_simt<128>(a, s, pdl, tr, bytes, flops) : launch_simt<64>(a, s, pdl, tr, bytes, flops);
+    return a.head_dim == 128 ? launch_f32<128>(a, s, pdl, tr, bytes, flops) : launch_f32<64>(a, s, pdl, tr, bytes, flops);
   int ctas = 0;
   tr.before(DFLASH_K_ATTN, bytes, flops);
   cudaError_t e = launch_chunk_tc(a, &ctas, s, pdl);
