@@ -47,7 +47,7 @@ struct ChunkSmem {
   uint64_t s_full[2], p_half[2], p_full[2], o_full[2], turn[2], drained[2];
   uint32_t tmem_base;
   int abort_flag;
-  int start[4];                // where this CTA begins: sequence, unit, KV head, position in the unit
+  int start[7];                // where this CTA begins: sequence, unit, KV head, position in the unit; the sequence's rows and lengths
   long long warp_sum[kTcThreads / 32];
   float row_max[2][128], row_sum[2][128];   // split mode: the streams' statistics
 };
@@ -217,8 +217,12 @@ __device__ __forceinline__ bool softmax_wait_bar(uint64_t* bar, uint32_t parity,
   const bool ok = mbar_try_wait(b, parity) || poll_bar(b, parity, &h->abort_flag, status);
   return __all_sync(0xffffffffu, ok) != 0;
 }
-// a * b / c
-__device__ __noinline__ long long mul_div(long long a, long long b, long long c) { return a * b / c; }
+// a * b / c; a 64-bit division takes some 300 cycles, at the start of every CTA
+__device__ __noinline__ long long mul_div64(long long a, long long b, long long c) { return a * b / c; }
+__device__ __forceinline__ long long mul_div(long long a, int b, long long c) {
+  if (a < (1 << 22) && c < (1 << 22)) return static_cast<uint32_t>(a) * static_cast<uint32_t>(b) / static_cast<uint32_t>(c);   // b <= 1024
+  return mul_div64(a, b, c);
+}
 // A warp's arrival, behind its lanes' TMEM accesses.
 __device__ __forceinline__ void arrive_warp(uint64_t* bar, int lane) {
   tc_fence_before();
@@ -338,8 +342,7 @@ struct Walk {
     b = h->start[0]; j = h->start[1]; kvh = h->start[2];
     begin = h->start[3];
     end = begin + count;
-    chunk_rows(p, b, row0, n);
-    ctx = p.ctx_len[b];
+    row0 = h->start[4]; n = h->start[5]; ctx = h->start[6];
     load_unit(p, unit_tok);
     place();
     if (nt == 0) next(p, unit_tok);   // behind the last page's position, or before the first one's
@@ -468,8 +471,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int cost = unit_cost(p, n, ctx, j, unit_tok);
         if (rem < static_cast<long long>(cost) * p.n_kv_heads) {
           hdr->start[0] = b; hdr->start[1] = j;
-          hdr->start[2] = static_cast<int>(rem / cost);
-          hdr->start[3] = static_cast<int>(rem % cost);
+          hdr->start[2] = static_cast<int>(static_cast<uint32_t>(rem) / static_cast<uint32_t>(cost));   // rem < cost * Hkv
+          hdr->start[3] = static_cast<int>(static_cast<uint32_t>(rem) % static_cast<uint32_t>(cost));
+          hdr->start[4] = row0; hdr->start[5] = n; hdr->start[6] = ctx;
           found = true;
         } else {
           rem -= static_cast<long long>(cost) * p.n_kv_heads;
@@ -541,7 +545,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (lane == 0 && w.kt0 == 0 && !w.whole()) {
           // its last page lies in the last CTA whose range starts at or before that page
           const long long x = first - w.begin + unit_share(w.pair) + (w.pages - 1) * page_share(w.pair);
-          const int last = static_cast<int>(mul_div((x + 1) * ctas + total - 1, 1, total)) - 1;
+          const int last = static_cast<int>(mul_div64((x + 1) * ctas + total - 1, 1, total)) - 1;
           int* d = p.desc + cta * kChunkDescInts;
           d[0] = last - cta + 1;
           d[1] = w.row0 + w.tok0;
