@@ -183,16 +183,15 @@ __global__ void __launch_bounds__(kSimtThreads) chunk_simt_kernel(const ChunkArg
 // ------------------------------------------------------------------ merge
 // Joins the partial rows of split units: CTA (unit, x) takes packed rows
 // 8x .. 8x+7, a warp a quarter of the columns, a lane four columns of one row.
-// The parts' rows, maxima and sums of kMergeBatch splits are requested at once;
+// The parts' rows, maxima and sums of BATCH splits are requested at once;
 // they are added in ascending split order (a batch at a time, under the
 // running maximum), so a result does not depend on timing.
-constexpr int kMergeBatch = 8;
 __device__ __forceinline__ void store_out(float* y, float4 v) { *reinterpret_cast<float4*>(y) = v; }
 __device__ __forceinline__ void store_out(__nv_bfloat16* y, float4 v) {
   __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
   *reinterpret_cast<uint2*>(y) = make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
 }
-template <typename T, int DH>
+template <typename T, int DH, int BATCH>
 __global__ void __launch_bounds__(128) chunk_merge_kernel(const ChunkArgs p) {
   constexpr int NL = DH / 64;   // loads of 16 columns a warp
   pdl_launch_dependents();
@@ -209,11 +208,11 @@ __global__ void __launch_bounds__(128) chunk_merge_kernel(const ChunkArgs p) {
     float4 acc[NL];
 #pragma unroll
     for (int i = 0; i < NL; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < S; s0 += kMergeBatch) {
-      float2 ml[kMergeBatch];
-      float4 x[kMergeBatch][NL];
+    for (int s0 = 0; s0 < S; s0 += BATCH) {
+      float2 ml[BATCH];
+      float4 x[BATCH][NL];
 #pragma unroll
-      for (int k = 0; k < kMergeBatch; ++k) {
+      for (int k = 0; k < BATCH; ++k) {
         ml[k] = make_float2(-INFINITY, 0.f);
         if (s0 + k < S) {
           const int at = s0 + k == 0 ? first : rest + (s0 + k - 1) * step;
@@ -225,14 +224,14 @@ __global__ void __launch_bounds__(128) chunk_merge_kernel(const ChunkArgs p) {
       }
       float top = M;
 #pragma unroll
-      for (int k = 0; k < kMergeBatch; ++k) top = fmaxf(top, ml[k].x);
+      for (int k = 0; k < BATCH; ++k) top = fmaxf(top, ml[k].x);
       const float ref = top == -INFINITY ? 0.f : top;
       const float f = exp2f(M - ref);
       L *= f;
 #pragma unroll
       for (int i = 0; i < NL; ++i) { acc[i].x *= f; acc[i].y *= f; acc[i].z *= f; acc[i].w *= f; }
 #pragma unroll
-      for (int k = 0; k < kMergeBatch; ++k) {
+      for (int k = 0; k < BATCH; ++k) {
         if (s0 + k < S) {
           const float w = exp2f(ml[k].x - ref);
           L += ml[k].y * w;
@@ -301,7 +300,7 @@ cudaError_t launch_simt(const ChunkArgs& a, cudaStream_t s, bool pdl, Tracer& tr
   tr.after();
   if (e != cudaSuccess || splits == 1) return e;
   tr.before(DFLASH_K_ATTN, 0.0, 0.0);
-  e = launch_plain(chunk_merge_kernel<float, DH>, dim3(static_cast<unsigned>(work), rows / 8), 128, 0, s, pdl, a);
+  e = launch_plain(chunk_merge_kernel<float, DH, 8>, dim3(static_cast<unsigned>(work), rows / 8), 128, 0, s, pdl, a);
   tr.after();
   return e;
 }
@@ -313,6 +312,15 @@ cudaError_t launch_f32(const ChunkArgs& a, cudaStream_t s, bool pdl, Tracer& tr,
   if (rows <= 16 && G <= 16) return launch_simt<DH, 1>(a, s, pdl, tr, bytes, flops);
   if (rows <= 32 && G <= 32) return launch_simt<DH, 2>(a, s, pdl, tr, bytes, flops);
   return launch_simt<DH, 4>(a, s, pdl, tr, bytes, flops);
+}
+
+template <int DH>
+cudaError_t launch_merge(const ChunkArgs& a, int ctas, int y, cudaStream_t s, bool pdl) {
+  // Long chunks have many units, each in two or three parts: two requested at
+  // once leave room for more warps than eight (with eight, a 2048-token chunk's
+  // merge took 12 us). Few rows behind a long context have one unit in many parts.
+  return y == kChunkRows / 8 ? launch_plain(chunk_merge_kernel<__nv_bfloat16, DH, 2>, dim3(ctas, y), 128, 0, s, pdl, a)
+                             : launch_plain(chunk_merge_kernel<__nv_bfloat16, DH, 8>, dim3(ctas, y), 128, 0, s, pdl, a);
 }
 
 }  // namespace
@@ -332,8 +340,7 @@ cudaError_t launch_attention_chunk(const ChunkArgs& a, int bf16, cudaStream_t s,
   const long long rows = static_cast<long long>(a.max_rows) * G;
   const int y = static_cast<int>(rows < 8 ? 1 : rows >= kChunkRows ? kChunkRows / 8 : (rows + 7) / 8);
   tr.before(DFLASH_K_ATTN, 0.0, 0.0);
-  e = a.head_dim == 128 ? launch_plain(chunk_merge_kernel<__nv_bfloat16, 128>, dim3(ctas, y), 128, 0, s, pdl, a)
-                        : launch_plain(chunk_merge_kernel<__nv_bfloat16, 64>, dim3(ctas, y), 128, 0, s, pdl, a);
+  e = a.head_dim == 128 ? launch_merge<128>(a, ctas, y, s, pdl) : launch_merge<64>(a, ctas, y, s, pdl);
   tr.after();
   return e;
 }

@@ -31,7 +31,7 @@
 namespace dfl {
 namespace {
 
-constexpr int kProbThreads = 512;
+constexpr int kProbThreads = 256;
 constexpr int kProbWarps = kProbThreads / 32;
 constexpr int kRows = 8;             // rows of 32 entries that a warp loads at once
 constexpr int kGroups = 8;           // groups of rows whose sums a warp keeps
@@ -179,7 +179,7 @@ __device__ __forceinline__ int find_entry(const TT* row, const float* qrow, int 
 }
 
 template <typename TT, int PARTS>
-__global__ void __launch_bounds__(kProbThreads) verify_probs_kernel(const ProbsArgs p) {
+__global__ void __launch_bounds__(kProbThreads, 4) verify_probs_kernel(const ProbsArgs p) {
   __shared__ int s_a;
   __shared__ unsigned long long s_warp[2][kProbWarps];   // sums of w and, where w has no mass, of p_a
   __shared__ unsigned long long s_group[kProbWarps][kGroups];
@@ -301,13 +301,10 @@ cudaError_t launch_probs(const ProbsArgs& a, cudaStream_t s, bool pdl) {
 
 template <typename TT>
 cudaError_t launch_typed(const ProbsArgs& a, cudaStream_t s, bool pdl) {
-  // as many CTAs a sequence as are all resident at once (two an SM): at 64
-  // sequences 8 CTAs each ran in two waves of the same latency
-  const long long slots = 2LL * num_sms_of_current_device();
-  if (16LL * a.B <= slots) return launch_probs<TT, 16>(a, s, pdl);
-  if (8LL * a.B <= slots) return launch_probs<TT, 8>(a, s, pdl);
-  if (4LL * a.B <= slots) return launch_probs<TT, 4>(a, s, pdl);
-  return launch_probs<TT, 2>(a, s, pdl);
+  // CTAs a sequence: 16 while two of each SM's four slots hold them all. (us for
+  // 1 / 16 / 64 sequences: 16 CTAs of 256 threads 7.4 / 9.8 / 31, 8 of 256
+  // 10.2 / 10.0 / 27, 16 of 512 7.6 / 12.5 / 49, 4 of 512 - / - / 27.)
+  return 16LL * a.B <= 2LL * num_sms_of_current_device() ? launch_probs<TT, 16>(a, s, pdl) : launch_probs<TT, 8>(a, s, pdl);
 }
 
 }  // namespace
