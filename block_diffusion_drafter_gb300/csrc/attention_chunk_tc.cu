@@ -38,7 +38,7 @@ constexpr int kKeys = kPageKeys;             // keys of a tile: one page
 constexpr uint32_t kSubTile = 128 * 128;     // 128 rows x 128 bytes, swizzled
 constexpr int kStages = 5;                   // K / V ring
 constexpr int kTcThreads = 384;              // K and V, 2 x MMAs, Q; 2 x 4 softmax warps
-constexpr int kLoadRegs = 88, kSoftmaxRegs = 208;   // 128 * 88 + 256 * 208 = 384 * 168
+constexpr int kLoadRegs = 72, kSoftmaxRegs = 216;   // 128 * 72 + 256 * 216 = 384 * 168
 constexpr float kLog2eTc = 1.4426950408889634f;
 constexpr float kLag = 8.0f;                 // log2 units that the running maximum may lag behind
 
@@ -296,17 +296,21 @@ struct RingPos {
 };
 
 // Cost of a unit in thirds of a microsecond: its own share (Q, the first page's
-// latency, the rows' way out), then its pages. Measured over 1520 units of one
-// and of eight pages: two tiles of rows 5 us and 1.7 us a page, one tile 2 us and
-// 1.4 us a page. Cut by pages alone, the first CTA of an 8192-token prompt got 60
-// short units and ran 1.6 times as long as the others.
-__device__ __forceinline__ int unit_share(bool pair) { return pair ? 15 : 6; }
+// latency, the rows' way out), then its pages. From 1520 units of one and of eight
+// pages: two tiles of rows 5 us and 1.7 us a page; one tile 3 to 4 us, by its
+// rows, and 1.4 us a page. Cut by pages alone, the first CTA of an 8192-token
+// prompt got 60 short units and ran 1.6 times as long as the others (614 us
+// instead of 380).
+__device__ __forceinline__ bool is_pair(int n_tok, int unit_tok) { return n_tok * 2 > unit_tok; }
+__device__ __forceinline__ int unit_share(int n_tok, int unit_tok) {
+  return is_pair(n_tok, unit_tok) ? 15 : n_tok * 8 > unit_tok ? 12 : 9;   // more than 32 rows of 256
+}
 __device__ __forceinline__ int page_share(bool pair) { return pair ? 5 : 4; }
 constexpr int kMinRange = 8;   // a CTA's least range: at least one page of any kind
 
 __device__ __forceinline__ int unit_cost(const ChunkArgs& p, int n, int ctx, int j, int unit_tok) {
-  const bool pair = min(unit_tok, n - j * unit_tok) * 2 > unit_tok;
-  return unit_share(pair) + unit_pages(p, n, ctx, j, unit_tok) * page_share(pair);
+  const int n_tok = min(unit_tok, n - j * unit_tok);
+  return unit_share(n_tok, unit_tok) + unit_pages(p, n, ctx, j, unit_tok) * page_share(is_pair(n_tok, unit_tok));
 }
 
 // A CTA's walk over its range: the current piece.
@@ -317,18 +321,20 @@ struct Walk {
   int kt0, nt;          // the piece: pages kt0 .. kt0 + nt - 1
   int begin, end;       // the range's ends, relative to the unit's first position
   int tok0, n_tok;      // the unit's tokens
+  int share;            // its own share of the cost
   bool pair, more;
 
   __device__ __forceinline__ void load_unit(const ChunkArgs& p, int unit_tok) {
     tok0 = j * unit_tok;
     n_tok = min(unit_tok, n - tok0);
     pages = unit_pages(p, n, ctx, j, unit_tok);
-    pair = n_tok * 2 > unit_tok;
+    pair = is_pair(n_tok, unit_tok);
+    share = unit_share(n_tok, unit_tok);
   }
-  __device__ __forceinline__ int span() const { return unit_share(pair) + pages * page_share(pair); }
+  __device__ __forceinline__ int span() const { return share + pages * page_share(pair); }
   // Pages whose position (the unit's share, then page by page) lies before x.
   __device__ __forceinline__ int pages_before(int x) const {
-    const int d = x - unit_share(pair);
+    const int d = x - share;
     const unsigned up = static_cast<unsigned>(max(d, 0) + page_share(pair) - 1);
     return min(pages, static_cast<int>(pair ? up / 5u : up / 4u));
   }
@@ -422,19 +428,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (threadIdx.x == 96) p.desc[blockIdx.x * kChunkDescInts] = 0;   // no incomplete unit starts here yet
 
   // ---------------------------------------------------------------- ranges
-  // The cost of each sequence for one KV head, summed by threads over contiguous
-  // runs of sequences; a scan gives the total and finds where this CTA begins.
+  // The units' cost for one KV head, summed by threads over contiguous runs of
+  // units (parts of a sequence, or whole sequences where there are more of them
+  // than threads); a scan gives the total and finds where this CTA begins.
   long long mine = 0;
-  const int per = (p.B + kTcThreads - 1) / kTcThreads;
-  const int b_first = threadIdx.x * per, b_last = min(p.B, b_first + per);
+  const int per = (p.B + kTcThreads - 1) / kTcThreads, parts = max(1, kTcThreads / p.B);
+  const int part = threadIdx.x % parts;
+  const int b_first = threadIdx.x / parts * per, b_last = min(p.B, b_first + per);
 #pragma unroll 1
   for (int b = b_first; b < b_last; ++b) {
     int row0, n;
     chunk_rows(p, b, row0, n);
     const int ctx = p.ctx_len[b], units = (n + unit_tok - 1) / unit_tok;
+    const int j1 = units * (part + 1) / parts;
 #pragma unroll 1
-    for (int j = 0; j < units; ++j) mine += unit_cost(p, n, ctx, j, unit_tok);
-    if (blockIdx.x == 0 && n > 0) check_capacity(p, ChunkUnit{b, row0, n, ctx, 0});
+    for (int j = units * part / parts; j < j1; ++j) mine += unit_cost(p, n, ctx, j, unit_tok);
+    if (blockIdx.x == 0 && part == 0 && n > 0) check_capacity(p, ChunkUnit{b, row0, n, ctx, 0});
   }
   long long incl = mine;
 #pragma unroll
@@ -465,9 +474,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       int row0, n;
       chunk_rows(p, b, row0, n);
       const int ctx = p.ctx_len[b], units = (n + unit_tok - 1) / unit_tok;
+      const int j1 = units * (part + 1) / parts;
       bool found = false;
 #pragma unroll 1
-      for (int j = 0; j < units && !found; ++j) {
+      for (int j = units * part / parts; j < j1 && !found; ++j) {
         const int cost = unit_cost(p, n, ctx, j, unit_tok);
         if (rem < static_cast<long long>(cost) * p.n_kv_heads) {
           hdr->start[0] = b; hdr->start[1] = j;
@@ -544,7 +554,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // the unit that starts here and goes on in the next CTAs: what to join
         if (lane == 0 && w.kt0 == 0 && !w.whole()) {
           // its last page lies in the last CTA whose range starts at or before that page
-          const long long x = first - w.begin + unit_share(w.pair) + (w.pages - 1) * page_share(w.pair);
+          const long long x = first - w.begin + w.share + (w.pages - 1) * page_share(w.pair);
           const int last = static_cast<int>(mul_div64((x + 1) * ctas + total - 1, 1, total)) - 1;
           int* d = p.desc + cta * kChunkDescInts;
           d[0] = last - cta + 1;
