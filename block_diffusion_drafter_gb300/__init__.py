@@ -4,7 +4,9 @@ Argument marshalling only: every step of the path runs in the library's CUDA
 kernels, reached through its C ABI (include/dflash.h). PyTorch provides the
 device memory and streams. Functions keep the C names:
 dflash_ctx_fuse, dflash_kv_inject, dflash_draft_block, dflash_verify_accept,
-plus the sizing / helper calls of the header. There is no CPU fallback: if
+the target-side dflash_qk_norm_rope, dflash_kv_append_paged,
+dflash_attention_chunk_paged and dflash_verify_probs, plus the sizing / helper
+calls of the header. There is no CPU fallback: if
 the library is missing, loading raises.
 """
 from __future__ import annotations
@@ -55,6 +57,9 @@ _SZ = ctypes.c_size_t
 PAGE_KEYS = 128
 
 
+_DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
+
+
 class KvPages(ctypes.Structure):
     """dflash_kv_pages: page pools [L, n_pages, Hkv, 128, Dh] and a device page
     table [max_batch, pages_per_seq] (tensors kept alive by the object)."""
@@ -66,6 +71,12 @@ class KvPages(ctypes.Structure):
         super().__init__(k_pool.data_ptr(), v_pool.data_ptr(), page_table.data_ptr(), k_pool.shape[1],
                          page_table.shape[1])
         self._keep = (k_pool, v_pool, page_table)
+        # what the target-side calls compare with their layout: (L, Hkv, Dh, dtype) and the table's sequences
+        fits = (k_pool.dim() == 5 and k_pool.shape == v_pool.shape and k_pool.dtype == v_pool.dtype
+                and k_pool.shape[3] == PAGE_KEYS and k_pool.is_contiguous() and v_pool.is_contiguous()
+                and page_table.dtype == torch.int32 and page_table.is_contiguous())
+        self.layout = (k_pool.shape[0], k_pool.shape[2], k_pool.shape[4], _DTYPES.get(k_pool.dtype)) if fits else None
+        self.sequences = page_table.shape[0]
 
 
 class Heads(ctypes.Structure):
@@ -457,9 +468,6 @@ class ChunkWorkspace:
         self.ptr = self.buf.data_ptr()
 
 
-_DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
-
-
 def _rows(t, n_heads: int, head_dim: int, dtype, fn: str):
     """(pointer, row stride) of [T, heads, Dh] rows whose heads lie side by side."""
     if t is None:
@@ -474,6 +482,40 @@ def _rows(t, n_heads: int, head_dim: int, dtype, fn: str):
     return t.data_ptr(), ld if rows > 1 else max(ld, n_heads * head_dim)
 
 
+def _ints(t, n: int, fn: str):
+    """Pointer of a device int32 vector of at least n entries."""
+    if t.dtype is not torch.int32 or t.numel() < n or not t.is_contiguous():
+        raise DFlashError(fn, ERR_SHAPE if t.dtype is torch.int32 else ERR_DTYPE)
+    return t.data_ptr()
+
+
+def _gain(t, heads: Heads, fn: str):
+    if t is None:
+        return None
+    if t.numel() != heads.head_dim or _DTYPES.get(t.dtype) != heads.dtype or not t.is_contiguous():
+        raise DFlashError(fn, ERR_SHAPE if _DTYPES.get(t.dtype) == heads.dtype else ERR_DTYPE)
+    return t.data_ptr()
+
+
+def _tables(c, s, heads: Heads, fn: str):
+    """Pointers and rows of the RoPE tables (fp32 [n, Dh/2]), None for no rotation."""
+    if c is None or s is None:
+        return _ptr(c), _ptr(s), 0
+    n, half = c.shape
+    if c.shape != s.shape or 2 * half != heads.head_dim or not c.is_contiguous() or not s.is_contiguous():
+        raise DFlashError(fn, ERR_SHAPE)
+    if c.dtype is not torch.float32 or s.dtype is not torch.float32:
+        raise DFlashError(fn, ERR_DTYPE)
+    return c.data_ptr(), s.data_ptr(), n
+
+
+def _view(pages: KvPages, heads: Heads, ctx_len, fn: str):
+    """A page view of the layout, with a table row for every sequence."""
+    if pages.layout != (heads.n_layers, heads.n_kv_heads, heads.head_dim, heads.dtype) or pages.sequences < ctx_len.numel():
+        raise DFlashError(fn, ERR_SHAPE)
+    return ctypes.byref(pages)
+
+
 def dflash_qk_norm_rope(heads: Heads, q, k, positions, rope_cos, rope_sin, q_out, k_out, dev_status, g_q=None, g_k=None,
                         trace=None, stream=None):
     """Per-head RMSNorm (where a gain is given) and RoPE of q [T, Hq, Dh] and
@@ -482,18 +524,19 @@ def dflash_qk_norm_rope(heads: Heads, q, k, positions, rope_cos, rope_sin, q_out
     x = q if q is not None else k
     if x is None:
         raise DFlashError(fn, ERR_INVALID_ARG)
-    dt, T, hq, hk, dh, out = _DTYPES.get(x.dtype, -1), len(x), heads.n_q_heads, heads.n_kv_heads, heads.head_dim, heads.dtype
-    if (q is not None and (q_out is None or len(q_out) < T)) or (
-            k is not None and (k_out is None or len(k_out) < T or len(k) != T)):
+    dt, T, hq, hk, dh, out = _DTYPES.get(x.dtype, -1), x.shape[0], heads.n_q_heads, heads.n_kv_heads, heads.head_dim, heads.dtype
+    if (q is not None and (q_out is None or q_out.shape[0] < T)) or (
+            k is not None and (k_out is None or k_out.shape[0] < T or k.shape[0] != T)):
         raise DFlashError(fn, ERR_SHAPE)
     qp, ldq = _rows(q, hq, dh, dt, fn)
     kp, ldk = _rows(k, hk, dh, dt, fn)
     qo, ldqo = _rows(q_out if q is not None else None, hq, dh, out, fn)
     ko, ldko = _rows(k_out if k is not None else None, hk, dh, out, fn)
+    cos, sin, n = _tables(rope_cos, rope_sin, heads, fn)
     _check(fn, load().dflash_qk_norm_rope(
-        ctypes.byref(heads), dt, qp, ldq, kp, ldk, _ptr(g_q), _ptr(g_k), _ptr(positions), _ptr(rope_cos),
-        _ptr(rope_sin), len(rope_cos) if rope_cos is not None else 0, T, qo, ldqo, ko, ldko, _ptr(dev_status),
-        _tr(trace), _stream(stream)))
+        ctypes.byref(heads), dt, qp, ldq, kp, ldk, _gain(g_q, heads, fn), _gain(g_k, heads, fn),
+        _ints(positions, T, fn) if positions is not None else None, cos, sin, n, T, qo, ldqo, ko, ldko,
+        _ptr(dev_status), _tr(trace), _stream(stream)))
 
 
 def dflash_kv_append_paged(heads: Heads, q, k, v, cu_rows, ctx_len, layer, pages: KvPages, rope_cos, rope_sin, q_out,
@@ -501,17 +544,19 @@ def dflash_kv_append_paged(heads: Heads, q, k, v, cu_rows, ctx_len, layer, pages
     """Appends packed rows k, v [T, Hkv, Dh] to one layer of the paged cache
     (K normed and rotated on the way); q [T, Hq, Dh] (or None) likewise into q_out."""
     fn = "dflash_kv_append_paged"
-    dt, T, hq, hk, dh = _DTYPES.get(k.dtype, -1), len(k), heads.n_q_heads, heads.n_kv_heads, heads.head_dim
-    if len(v) != T or (q is not None and (len(q) != T or q_out is None or len(q_out) < T)):
+    dt, T, hq, hk, dh = _DTYPES.get(k.dtype, -1), k.shape[0], heads.n_q_heads, heads.n_kv_heads, heads.head_dim
+    if v.shape[0] != T or (q is not None and (q.shape[0] != T or q_out is None or q_out.shape[0] < T)):
         raise DFlashError(fn, ERR_SHAPE)
     qp, ldq = _rows(q, hq, dh, dt, fn)
     kp, ldk = _rows(k, hk, dh, dt, fn)
     vp, ldv = _rows(v, hk, dh, dt, fn)
     qo, ldqo = _rows(q_out if q is not None else None, hq, dh, heads.dtype, fn)
+    cos, sin, n = _tables(rope_cos, rope_sin, heads, fn)
+    B = ctx_len.numel()
     _check(fn, load().dflash_kv_append_paged(
-        ctypes.byref(heads), dt, qp, ldq, kp, ldk, vp, ldv, _ptr(g_q), _ptr(g_k), _ptr(rope_cos), _ptr(rope_sin),
-        len(rope_cos) if rope_cos is not None else 0, _ptr(cu_rows), _ptr(ctx_len), len(ctx_len), T, int(layer),
-        ctypes.byref(pages), qo, ldqo, _ptr(dev_status), _tr(trace), _stream(stream)))
+        ctypes.byref(heads), dt, qp, ldq, kp, ldk, vp, ldv, _gain(g_q, heads, fn), _gain(g_k, heads, fn), cos, sin, n,
+        _ints(cu_rows, B + 1, fn), _ints(ctx_len, B, fn), B, T, int(layer), _view(pages, heads, ctx_len, fn), qo, ldqo,
+        _ptr(dev_status), _tr(trace), _stream(stream)))
 
 
 def dflash_attention_chunk_paged(heads: Heads, q, cu_rows, ctx_len, max_rows, max_ctx_hint, layer, pages: KvPages, out,
@@ -519,14 +564,15 @@ def dflash_attention_chunk_paged(heads: Heads, q, cu_rows, ctx_len, max_rows, ma
     """Attention of a ragged batch of chunks q [T, Hq, Dh] over the paged cache
     that already holds the chunks' own keys and values."""
     fn = "dflash_attention_chunk_paged"
-    T, hq, dh, dt = len(q), heads.n_q_heads, heads.head_dim, heads.dtype
-    if len(out) < T:
+    T, hq, dh, dt = q.shape[0], heads.n_q_heads, heads.head_dim, heads.dtype
+    if out.shape[0] < T:
         raise DFlashError(fn, ERR_SHAPE)
     qp, ldq = _rows(q, hq, dh, dt, fn)
     op, ldo = _rows(out, hq, dh, dt, fn)
+    B = ctx_len.numel()
     _check(fn, load().dflash_attention_chunk_paged(
-        ctypes.byref(heads), qp, ldq, _ptr(cu_rows), _ptr(ctx_len), len(ctx_len), T, int(max_rows),
-        int(max_ctx_hint), int(layer), ctypes.byref(pages), 1 if causal else 0, float(scale), op, ldo,
+        ctypes.byref(heads), qp, ldq, _ints(cu_rows, B + 1, fn), _ints(ctx_len, B, fn), B, T, int(max_rows),
+        int(max_ctx_hint), int(layer), _view(pages, heads, ctx_len, fn), 1 if causal else 0, float(scale), op, ldo,
         _ptr(dev_status), ws.ptr, ws.nbytes, _tr(trace), _stream(stream)))
 
 
@@ -534,11 +580,21 @@ def dflash_verify_probs(cfg, target_probs, draft_probs, draft, u_accept, u_draw,
                         dev_status, gamma_b=None, trace=None, stream=None):
     """Verification against given probabilities from given uniforms; draft_probs
     None for greedy drafts."""
-    dt = BF16 if target_probs.dtype == torch.bfloat16 else F32
-    _check("dflash_verify_probs", load().dflash_verify_probs(
-        ctypes.byref(cfg), _ptr(target_probs), dt, _ptr(draft_probs), _ptr(draft), _ptr(gamma_b), _ptr(u_accept),
-        _ptr(u_draw), target_probs.shape[0], _ptr(tau), _ptr(committed), _ptr(next_anchor), _ptr(dev_status),
-        _tr(trace), _stream(stream)))
+    fn = "dflash_verify_probs"
+    B, R, V = target_probs.shape
+    dt = _DTYPES.get(target_probs.dtype, -1)
+    if R != cfg.gamma + 1 or V != cfg.vocab or not target_probs.is_contiguous() or (
+            draft_probs is not None and (draft_probs.shape != (B, R - 1, V) or not draft_probs.is_contiguous())) or (
+            u_accept.numel() < B * (R - 1) or u_draw.numel() < B or not u_accept.is_contiguous()):
+        raise DFlashError(fn, ERR_SHAPE)
+    f32 = torch.float32
+    if u_accept.dtype is not f32 or u_draw.dtype is not f32 or (draft_probs is not None and draft_probs.dtype is not f32):
+        raise DFlashError(fn, ERR_DTYPE)
+    _check(fn, load().dflash_verify_probs(
+        ctypes.byref(cfg), target_probs.data_ptr(), dt, _ptr(draft_probs), _ints(draft, B * (R - 1), fn),
+        _ints(gamma_b, B, fn) if gamma_b is not None else None, u_accept.data_ptr(), u_draw.data_ptr(), B,
+        _ints(tau, B, fn), _ints(committed, B * R, fn), _ints(next_anchor, B, fn), _ptr(dev_status), _tr(trace),
+        _stream(stream)))
 
 
 class TraceRecorder:

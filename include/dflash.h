@@ -472,7 +472,9 @@ dflash_status dflash_verify_accept_noalloc(const dflash_config* cfg,
  * ascending from 0; sequences may have no rows), and stand at positions
  * ctx_len[b], ctx_len[b] + 1, ... Rows t >= cu_rows[B] of any operand are
  * neither read into a result nor written. None of the calls advances ctx_len
- * (every layer of a pass runs over the same lengths).
+ * (every layer of a pass runs over the same lengths). All positions of a
+ * sequence's pages are its own: nothing is kept free for a draft block. Tables
+ * of several sequences may name the same pages for reading (a shared prefix).
  *
  * Row operands (q, k, v, out) hold a row's heads side by side ([T, heads, Dh])
  * with rows ld elements apart, so that they may be parts of one projection's

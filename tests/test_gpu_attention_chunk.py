@@ -302,3 +302,43 @@ def test_empty_batches(dfl):
     s.run()
     torch.cuda.synchronize()
     assert (s.obuf == 9).all() and int(s.st) == 0
+
+
+def test_more_sequences_than_threads(dfl):
+    ns = [(3 * i) % 4 for i in range(900)]
+    ctxs = [(53 * i) % 300 for i in range(900)]
+    s = Scene(dfl, *SHAPES["mha64"], ns, ctxs, seed=41)
+    s.run()
+    s.check(rows=1)
+
+
+@pytest.mark.parametrize("shape", ["g64", "g16_64"])
+def test_many_units_of_one_sequence(dfl, shape):
+    """Units of few tokens: hundreds of them in one sequence, found by threads that share it."""
+    s = Scene(dfl, *SHAPES[shape], [1500, 1], [70, 3], seed=43)
+    s.run()
+    s.check(rows=12)
+
+
+@pytest.mark.parametrize("shape", ["qwen", "f32_64"])
+def test_sequences_that_share_a_prefix(dfl, shape):
+    """Two sequences' tables name the same pages for their common context."""
+    s = Scene(dfl, *SHAPES[shape], [5, 9], [256, 256], seed=45)
+    s.table[1, :2] = s.table[0, :2]
+    s.pages = dfl.KvPages(s.kp, s.vp, s.table.cuda())
+    s.k[1], s.v[1] = s.k[1].clone(), s.v[1].clone()
+    s.k[1][:, :256], s.v[1][:, :256] = s.k[0][:, :256], s.v[0][:, :256]
+    s.run()
+    s.check()
+
+
+def test_tracing_records_the_kernel_and_its_merge(dfl):
+    s = Scene(dfl, *SHAPES["qwen"], [17], [900], seed=47)
+    rec = dfl.TraceRecorder(8)
+    s.run(trace=rec.struct)
+    s.check(rows=4)
+    got = rec.records()
+    assert [k for k, _, _, _ in got] == [dfl.K_ATTN, dfl.K_ATTN]
+    T = s.q.shape[0]      # the rows that the call got: two lie behind the sequence
+    assert got[0][1] == 2.0 * (900 + T) * 8 * 128 * 2 + 2.0 * T * 32 * 128 * 2 and got[1][1] == 0.0
+    assert all(ms >= 0 for _, _, _, ms in got)

@@ -147,3 +147,59 @@ def test_the_binding_refuses_rows_that_do_not_fit_the_layout(lib, heads):
     assert e.value.status == lib.ERR_INVALID_ARG
     with pytest.raises(lib.DFlashError):
         lib.ChunkWorkspace(lib.make_heads(1, 3, 2, 128), device="cpu")
+
+
+def test_the_binding_refuses_what_the_library_cannot_see(lib, heads):
+    """Types, shapes and layouts behind the pointers: refused before any pointer is passed on."""
+    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    q, k = torch.zeros((3, 8, 128), dtype=bf), torch.zeros((3, 2, 128), dtype=bf)
+    pool = torch.zeros((2, 4, 2, 128, 128), dtype=bf)
+    table, cu, ctx = torch.zeros((1, 2), dtype=i32), torch.tensor([0, 3], dtype=i32), torch.zeros(1, dtype=i32)
+    st = torch.zeros(1, dtype=i32)
+    good = lib.KvPages(pool, pool, table)
+    cos = torch.zeros((8, 64))
+
+    class NoScratch:
+        ptr, nbytes = None, 0
+
+    def att(pages=good, cu=cu, ctx=ctx):
+        lib.dflash_attention_chunk_paged(heads, q, cu, ctx, 3, 0, 0, pages, q, st, NoScratch())
+
+    def app(g=None, c=cos, s=cos, pages=good):
+        lib.dflash_kv_append_paged(heads, q, k, k, cu, ctx, 0, pages, c, s, q, st, g_q=g)
+
+    def fails(f, status):
+        with pytest.raises(lib.DFlashError) as e:
+            f()
+        assert e.value.status == status, f
+
+    fails(att, lib.ERR_WORKSPACE)                                                   # all else is right
+    for bad in (lib.KvPages(pool[:1], pool[:1], table), lib.KvPages(pool.float(), pool.float(), table),
+                lib.KvPages(pool[:, :, :1].contiguous(), pool[:, :, :1].contiguous(), table),
+                lib.KvPages(pool, pool[:, :3], table), lib.KvPages(pool, pool, table.long())):
+        fails(lambda: att(pages=bad), lib.ERR_SHAPE)
+    fails(lambda: att(cu=cu[:1]), lib.ERR_SHAPE)
+    fails(lambda: att(cu=cu.long()), lib.ERR_DTYPE)
+    fails(lambda: att(cu=torch.zeros(3, dtype=i32), ctx=torch.zeros(2, dtype=i32)), lib.ERR_SHAPE)   # no table row
+    fails(lambda: att(ctx=ctx.float()), lib.ERR_DTYPE)
+    fails(lambda: app(g=torch.ones(64, dtype=bf)), lib.ERR_SHAPE)
+    fails(lambda: app(g=torch.ones(128)), lib.ERR_DTYPE)
+    fails(lambda: app(c=cos[:, :32], s=cos[:, :32]), lib.ERR_SHAPE)
+    fails(lambda: app(c=cos.double(), s=cos.double()), lib.ERR_DTYPE)
+    fails(lambda: app(s=None), lib.ERR_INVALID_ARG)
+    fails(lambda: lib.dflash_qk_norm_rope(heads, q, None, torch.zeros(2, dtype=i32), cos, cos, q, None, st), lib.ERR_SHAPE)
+
+    cfg = lib.config_from_workload(synth.WORKLOADS["tiny_f32_L1_N128"])
+    B, m, V = 1, cfg.gamma, cfg.vocab
+    p, d = torch.zeros((B, m + 1, V)), torch.zeros((B, m), dtype=i32)
+    one, com = torch.zeros(B, dtype=i32), torch.zeros((B, m + 1), dtype=i32)
+
+    def ver(p=p, q=torch.zeros((B, m, V)), d=d, ua=torch.zeros((B, m)), ud=torch.zeros(B), com=com, st=None):
+        lib.dflash_verify_probs(cfg, p, q, d, ua, ud, one, com, one, st)
+
+    fails(ver, lib.ERR_INVALID_ARG)                                                 # no status word; all else is right
+    for kw, want in [(dict(p=p[:, 1:]), "SHAPE"), (dict(p=p[..., :-1]), "SHAPE"), (dict(p=p.double()), "DTYPE"),
+                     (dict(q=torch.zeros((B, m, V), dtype=bf)), "DTYPE"), (dict(q=torch.zeros((B, m + 1, V))), "SHAPE"),
+                     (dict(d=d.long()), "DTYPE"), (dict(d=d[:, 1:]), "SHAPE"), (dict(ua=torch.zeros((B, m - 1))), "SHAPE"),
+                     (dict(ud=torch.zeros(B).double()), "DTYPE"), (dict(com=com[:, 1:].contiguous()), "SHAPE")]:
+        fails(lambda: ver(**kw), getattr(lib, "ERR_" + want))
