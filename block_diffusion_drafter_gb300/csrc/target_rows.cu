@@ -7,7 +7,7 @@
 // A group of Dh/16 lanes takes one (row, head): each lane holds elements
 // 8l .. 8l+7 of the first half and the same of the second in 16-byte accesses,
 // so a rotation's two values sit in one thread and only the sum of squares
-// crosses lanes (a fixed shuffle tree). A block of 256 threads takes the heads
+// crosses lanes (a fixed shuffle tree). A block of 128 threads takes the heads
 // of a few rows: a row's position, its page and its cos / sin values are
 // fetched once for all its heads, while the first heads are already on
 // their way. Statistics and the rotation are fp32; each output is rounded once,
@@ -21,15 +21,17 @@
 namespace dfl {
 namespace {
 
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 128;
 
-// Eight elements as they lie in memory.
+// Eight elements as they lie in memory. Rows are read and written once
+// (load_once, store8: streaming accesses); gains and tables stay in the caches.
 template <typename T>
 struct Eight;
 template <>
 struct Eight<__nv_bfloat16> {
   uint4 r;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { r = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void load_once(const __nv_bfloat16* p) { r = __ldcs(reinterpret_cast<const uint4*>(p)); }
   __device__ __forceinline__ void get(float* v) const {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -46,6 +48,10 @@ struct Eight<float> {
     r[0] = *reinterpret_cast<const float4*>(p);
     r[1] = *reinterpret_cast<const float4*>(p + 4);
   }
+  __device__ __forceinline__ void load_once(const float* p) {
+    r[0] = __ldcs(reinterpret_cast<const float4*>(p));
+    r[1] = __ldcs(reinterpret_cast<const float4*>(p + 4));
+  }
   __device__ __forceinline__ void get(float* v) const {
 #pragma unroll
     for (int i = 0; i < 2; ++i) { v[4 * i] = r[i].x; v[4 * i + 1] = r[i].y; v[4 * i + 2] = r[i].z; v[4 * i + 3] = r[i].w; }
@@ -56,12 +62,12 @@ __device__ __forceinline__ uint32_t two_bf16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 __device__ __forceinline__ void store8(float* p, const float* v) {
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
+  __stcs(reinterpret_cast<float4*>(p + 4), make_float4(v[4], v[5], v[6], v[7]));
 }
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v) {
-  *reinterpret_cast<uint4*>(p) =
-      make_uint4(two_bf16(v[0], v[1]), two_bf16(v[2], v[3]), two_bf16(v[4], v[5]), two_bf16(v[6], v[7]));
+  __stcs(reinterpret_cast<uint4*>(p),
+         make_uint4(two_bf16(v[0], v[1]), two_bf16(v[2], v[3]), two_bf16(v[4], v[5]), two_bf16(v[6], v[7])));
 }
 
 // The number of entries of cu[1..B] that are <= t, i.e. the sequence of packed
@@ -80,7 +86,7 @@ __device__ __forceinline__ int find_sequence(const int32_t* cu, int B, int t, in
 }
 
 template <typename TI, typename TO, int DH, bool APPEND>
-__global__ void __launch_bounds__(kRowThreads, 4) target_rows_kernel(const RowArgs p, int groups_per_row) {
+__global__ void __launch_bounds__(kRowThreads, 8) target_rows_kernel(const RowArgs p, int groups_per_row) {
   constexpr int GL = DH / 16;                   // lanes per (row, head)
   constexpr int NG = kRowThreads / GL;          // groups per block
   pdl_launch_dependents();
@@ -90,7 +96,8 @@ __global__ void __launch_bounds__(kRowThreads, 4) target_rows_kernel(const RowAr
   const int rows_per_block = NG / groups_per_row;
   // groups_per_row is a power of two; a warp's groups may span several rows
   const int t = blockIdx.x * rows_per_block + group / groups_per_row;
-  const int sub = group % groups_per_row;
+  // a group's heads: first, first + step, ... (several blocks share a row where there are few)
+  const int sub = group % groups_per_row, head0 = sub + blockIdx.y * groups_per_row, step = groups_per_row * gridDim.y;
   const int hq = p.q != nullptr ? p.n_q_heads : 0, hk = p.k != nullptr ? p.n_kv_heads : 0;
   const int heads = hq + hk + (APPEND ? p.n_kv_heads : 0);
   const TI* xq = static_cast<const TI*>(p.q) + t * p.ldq;
@@ -99,11 +106,11 @@ __global__ void __launch_bounds__(kRowThreads, 4) target_rows_kernel(const RowAr
   Eight<TI> lo, hi;
   auto fetch = [&](int h) {
     const TI* x = h < hq ? xq + h * DH : h < hq + hk ? xk + (h - hq) * DH : xv + (h - hq - hk) * DH;
-    lo.load(x + 8 * gl);
-    hi.load(x + DH / 2 + 8 * gl);
+    lo.load_once(x + 8 * gl);
+    hi.load_once(x + DH / 2 + 8 * gl);
   };
   bool live = t < p.T;
-  if (live && sub < heads) fetch(sub);   // on its way while the row's place is looked up
+  if (live && head0 < heads) fetch(head0);   // on its way while the row's place is looked up
 
   int pos = 0, page_row = 0;
   size_t page_base = 0;
@@ -125,10 +132,10 @@ __global__ void __launch_bounds__(kRowThreads, 4) target_rows_kernel(const RowAr
         if (pos >= 0 && at < p.pages.pages_per_seq)
           page = p.pages.table[static_cast<size_t>(b) * p.pages.pages_per_seq + at];
         if (page < 0 || page >= p.pages.n_pages) {
-          if (gl == 0 && sub == 0) report(p.dev_status, DFLASH_ERR_CAPACITY);
+          if (gl == 0 && head0 == 0) report(p.dev_status, DFLASH_ERR_CAPACITY);
           live = false;
         } else if (p.rope_cos != nullptr && pos >= p.rope_positions) {
-          if (gl == 0 && sub == 0) report(p.dev_status, DFLASH_ERR_INVALID_ARG);
+          if (gl == 0 && head0 == 0) report(p.dev_status, DFLASH_ERR_INVALID_ARG);
           live = false;
         } else {
           page_row = pos % kPageKeys;
@@ -139,7 +146,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) target_rows_kernel(const RowAr
   } else if (live && p.rope_cos != nullptr) {
     pos = p.positions[t];
     if (pos < 0 || pos >= p.rope_positions) {
-      if (gl == 0 && sub == 0) report(p.dev_status, DFLASH_ERR_INVALID_ARG);
+      if (gl == 0 && head0 == 0) report(p.dev_status, DFLASH_ERR_INVALID_ARG);
       live = false;
     }
   }
@@ -155,10 +162,11 @@ __global__ void __launch_bounds__(kRowThreads, 4) target_rows_kernel(const RowAr
     c.get(cs);
     s.get(sn);
   }
-  // One head at a time and four blocks an SM: three heads in flight took 117
-  // registers, two blocks, and 167 us for 32768 rows of 40 heads instead of 119.
-  for (int h = sub; h < heads; h += groups_per_row) {
-    if (h != sub) fetch(h);
+  // One head at a time and 64 registers: three heads in flight took 117
+  // registers, half the warps, and 167 us for 32768 rows of 40 heads instead of
+  // 117 (5.9 TB/s).
+  for (int h = head0; h < heads; h += step) {
+    if (h != head0) fetch(h);
     float a[8], b[8];
     lo.get(a);
     hi.get(b);
@@ -223,8 +231,11 @@ cudaError_t launch_rows(const RowArgs& a, cudaStream_t s, bool pdl) {
     gpr = best;
   }
   const int rpb = NG / gpr;
+  const unsigned blocks = static_cast<unsigned>((a.T + rpb - 1) / rpb);
+  // few rows: a head a group, the rest of a row's heads in other blocks
+  const unsigned slices = blocks <= 2u * num_sms_of_current_device() ? (heads + gpr - 1) / gpr : 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.T + rpb - 1) / rpb));
+  cfg.gridDim = dim3(blocks, slices);
   cfg.blockDim = dim3(kRowThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
