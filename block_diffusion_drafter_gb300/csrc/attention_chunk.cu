@@ -325,16 +325,33 @@ cudaError_t launch_merge(const ChunkArgs& a, int ctas, int y, cudaStream_t s, bo
 
 }  // namespace
 
-cudaError_t launch_attention_chunk(const ChunkArgs& a, int bf16, cudaStream_t s, bool pdl, Tracer& tr, double bytes,
+// Over few pages units stay whole, each with the CTA in whose range it starts:
+// the merge of split ones is a launch of its own (1.3 to 4 us) and costs more
+// than the pages one after another. Split / whole, 32 heads over 8, in us:
+//   up to 3 pages: 1 row, 100 keys 9.7 / 8.3; 8 x 17 rows, 317 keys 15.8 / 12.2;
+//     256 rows 16.8 / 12.0
+//   6 pages: 512 rows 19.1 / 15.1, 4 x 300 rows behind 300 keys 30.6 / 26.9, but
+//     1 row, 701 keys 11.1 / 14.1 and 20 x 2 rows, 702 keys 23.4 / 26.8: whole
+//     only where the chunk fills a unit's 256 rows, whose pages cost less
+//     beside the unit's own share.
+bool keep_whole(const ChunkArgs& a) {
+  const long long keys = static_cast<long long>(a.max_ctx) + a.max_rows;
+  const long long rows = static_cast<long long>(a.max_rows) * (a.n_q_heads / a.n_kv_heads);
+  return keys <= (rows > kChunkRows ? 6 : 3) * kPageKeys;
+}
+
+cudaError_t launch_attention_chunk(const ChunkArgs& args, int bf16, cudaStream_t s, bool pdl, Tracer& tr, double bytes,
                                    double flops) {
+  ChunkArgs a = args;
   if (a.head_dim != 64 && a.head_dim != 128) return cudaErrorInvalidValue;
   if (!bf16)
     return a.head_dim == 128 ? launch_f32<128>(a, s, pdl, tr, bytes, flops) : launch_f32<64>(a, s, pdl, tr, bytes, flops);
   int ctas = 0;
+  a.whole_units = keep_whole(a);
   tr.before(DFLASH_K_ATTN, bytes, flops);
   cudaError_t e = launch_chunk_tc(a, &ctas, s, pdl);
   tr.after();
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || a.whole_units) return e;
   // the merge's grid covers the rows of the hinted chunk; its CTAs walk on over further rows
   const int G = a.n_q_heads / a.n_kv_heads;
   const long long rows = static_cast<long long>(a.max_rows) * G;

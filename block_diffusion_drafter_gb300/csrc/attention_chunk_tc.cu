@@ -338,9 +338,14 @@ struct Walk {
     const unsigned up = static_cast<unsigned>(max(d, 0) + page_share(pair) - 1);
     return min(pages, static_cast<int>(pair ? up / 5u : up / 4u));
   }
-  __device__ __forceinline__ void place() {
-    kt0 = pages_before(begin);
-    nt = pages_before(end) - kt0;
+  __device__ __forceinline__ void place(const ChunkArgs& p) {
+    if (p.whole_units) {   // a unit belongs to the range it starts in
+      kt0 = 0;
+      nt = begin <= 0 && end > 0 ? pages : 0;
+    } else {
+      kt0 = pages_before(begin);
+      nt = pages_before(end) - kt0;
+    }
   }
   __device__ __forceinline__ void start(const ChunkArgs& p, const ChunkSmem* h, int count, int unit_tok) {
     more = count > 0;
@@ -350,7 +355,7 @@ struct Walk {
     end = begin + count;
     row0 = h->start[4]; n = h->start[5]; ctx = h->start[6];
     load_unit(p, unit_tok);
-    place();
+    place(p);
     if (nt == 0) next(p, unit_tok);   // behind the last page's position, or before the first one's
   }
   __device__ __forceinline__ void next(const ChunkArgs& p, int unit_tok) {
@@ -373,7 +378,7 @@ struct Walk {
       }
       load_unit(p, unit_tok);
     }
-    place();
+    place(p);
     more = nt > 0;   // a range that ends in a unit's own share has none of its pages
   }
   __device__ __forceinline__ bool whole() const { return nt == pages; }

@@ -273,6 +273,7 @@ struct ChunkArgs {
   long long ldq, ldo;
   const int32_t *cu_rows, *ctx_len;
   int B, T, max_rows, max_ctx, layer, n_layers, causal;
+  int whole_units;           // bf16: units are not split (no merge follows)
   int n_q_heads, n_kv_heads, head_dim;
   float scale;
   const void *k_pool, *v_pool;
