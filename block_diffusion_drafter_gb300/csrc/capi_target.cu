@@ -203,7 +203,7 @@ dflash_status dflash_verify_probs(const dflash_config* c, const void* target_pro
       u_draw == nullptr || tau == nullptr || committed == nullptr || next_anchor == nullptr || dev_status == nullptr ||
       !trace_ok(trace))
     return DFLASH_ERR_INVALID_ARG;
-  if (B > (1 << 24)) return DFLASH_ERR_TOO_LARGE;
+  if (B > (1 << 24) || c->vocab > (1 << 24)) return DFLASH_ERR_TOO_LARGE;
   if ((st = check_arch()) != DFLASH_OK) return st;
   ProbsArgs a{target_probs, probs_dtype == DFLASH_BF16, draft_probs, draft, gamma_b, u_accept, u_draw, B, c->gamma,
               c->vocab, tau, committed, next_anchor, dev_status};

@@ -584,11 +584,13 @@ dflash_status dflash_attention_chunk_paged(const dflash_heads* heads, const void
  *   [B, gamma, V], or NULL for drafts taken without a draw (dflash_draft_block's
  *   argmax): q_j is then one for x_j and zero elsewhere. Entries are
  *   probabilities in [0, 1] (NaN and negative entries count as 0, larger ones
- *   as 1); a row need not sum to one, but must sum to less than 4.
+ *   as 1); a row need not sum to one.
  * u_accept: device fp32 [B, gamma], u_draw: device fp32 [B], uniforms in [0, 1).
  * gamma_b: NULL, or device [B] as in dflash_verify_accept_dyn.
- * A draft id outside [0, V) counts as rejected. A row a without any mass sets
- *   DFLASH_ERR_INVALID_ARG in dev_status and gives y = 0.
+ * A draft id outside [0, V) counts as rejected. A row a without any mass, and
+ *   weights w that sum to 4 or more (no probabilities; less than V 2^-22 + 2^-16
+ *   below 4 counts as 4), set DFLASH_ERR_INVALID_ARG in dev_status and give y = 0.
+ * Limits: B, V <= 2^24, else DFLASH_ERR_TOO_LARGE.
  * The draw is exact: weights are summed as multiples of 2^-62 in integers, so
  *   that the token does not depend on an order of summation. No workspace; one
  *   launch. */

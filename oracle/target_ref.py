@@ -87,7 +87,8 @@ def verify_probs(p, q, draft, u_accept, u_draw):
             w = np.where(whole > f, whole - f, np.uint64(0))
         if not w.any():
             w = whole
-    y = first_above(w, u_draw) if w.any() else 0
+    # without mass, and with more than a probability could have (4 and up), there is nothing to draw from
+    y = first_above(w, u_draw) if 0 < int(w.sum(dtype=object)) < 1 << 64 else 0
     com = np.full(gamma + 1, -1, dtype=np.int64)
     com[:a] = np.asarray(draft)[:a]
     com[a] = y

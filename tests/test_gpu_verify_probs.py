@@ -63,7 +63,7 @@ def inputs(B, gamma, V, seed, greedy=False, dtype=torch.float32):
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("greedy", [False, True])
 @pytest.mark.parametrize("B,gamma,V", [(1, 16, 151936), (5, 16, 1003), (3, 7, 4103), (40, 1, 2), (2, 16, 200003), (9, 4, 131),
-                                       (130, 3, 127)])
+                                       (130, 3, 127), (30, 5, 20011)])
 def test_matches_the_oracle(dfl, dtype, greedy, B, gamma, V):
     x = inputs(B, gamma, V, B + V, greedy, dtype)
     got = run(dfl, *x)
@@ -136,6 +136,45 @@ def test_odd_values(dfl):
     for u in (1.0, 2.0, -1.0, float("nan")):                  # outside the range: still a token
         y = run(dfl, p, q, draft, ua, torch.full((B,), u))[2]
         assert ((y >= 0) & (y < V)).all()
+
+
+@pytest.mark.parametrize("greedy", [False, True])
+@pytest.mark.parametrize("B,V", [(4, 5003), (24, 1999), (48, 1001)])
+@pytest.mark.parametrize("low,high", [(-72, 0), (-72, -11), (-66, -40), (-63, -58)])
+def test_weights_of_every_size_are_summed_exactly(dfl, greedy, B, V, low, high):
+    """Rows whose whole mass lies in the last bits that are kept, as well as in the first, for each number of CTAs."""
+    g = torch.Generator().manual_seed(B + V + low)
+    draw = lambda *n: torch.ldexp(1 + torch.rand(n, generator=g), torch.randint(low, high, n, generator=g))  # noqa: E731
+    p, q = draw(B, 3, V), draw(B, 2, V)
+    p[:, :, 1::7] = torch.ldexp(torch.ones(()), torch.randint(low, high, (B, 3, p[:, :, 1::7].shape[2]), generator=g))
+    q[:, :, ::5] = p[:, :2, ::5]                              # equal: no weight
+    q[:, :, 2::5] = 0.0
+    p[:, :, 3::11], q[:, :, 4::11] = 1e-42, 1e-42             # subnormal
+    draft = torch.randint(0, V, (B, 2), generator=g, dtype=torch.int32)
+    x = (p.clamp(max=1.0), None if greedy else q, draft, torch.rand((B, 2), generator=g) * (0.01 if low == -72 else 1.0),
+         torch.rand((B,), generator=g))
+    got = run(dfl, *x)
+    check(got, *x)
+    assert got[3] == (dfl.ERR_INVALID_ARG if high == 0 else 0)   # those rows' weights sum to 100 and more
+
+
+@pytest.mark.parametrize("B", [2, 24, 48])
+def test_sums_that_are_no_probabilities(dfl, B):
+    """Weights that sum to 4 or more give token 0 and an error, below that a token; in one lane or spread over all."""
+    V = 4001
+    p, q, draft, ua, ud = inputs(B, 1, V, 17, greedy=True)
+    p[:] = 0.0
+    ua[:] = 0.5                                               # the only draft is rejected
+    draft[:] = V - 1
+    for where, over in ((torch.arange(4) * 32, True), (torch.arange(3) * 32, False), (torch.arange(4) * 1000 + 9, True),
+                        (torch.arange(3) * 1000 + 9, False), (torch.arange(64) * 32, True), (torch.arange(128), True)):
+        p[:, 0, :] = 0.0
+        p[:, 0, where] = 1.0
+        x = (p, q, draft, ua, ud)
+        got = run(dfl, *x)
+        check(got, *x)
+        assert got[3] == (dfl.ERR_INVALID_ARG if over else 0)
+        assert not over or (got[2] == 0).all()
 
 
 def test_rows_without_mass(dfl):
