@@ -86,7 +86,7 @@ __device__ __forceinline__ int find_sequence(const int32_t* cu, int B, int t, in
 }
 
 template <typename TI, typename TO, int DH, bool APPEND>
-__global__ void __launch_bounds__(kRowThreads, 8) target_rows_kernel(const RowArgs p, int groups_per_row) {
+__global__ void __launch_bounds__(kRowThreads, sizeof(TI) == 4 ? 7 : 8) target_rows_kernel(const RowArgs p, int groups_per_row) {
   constexpr int GL = DH / 16;                   // lanes per (row, head)
   constexpr int NG = kRowThreads / GL;          // groups per block
   pdl_launch_dependents();
@@ -162,14 +162,18 @@ __global__ void __launch_bounds__(kRowThreads, 8) target_rows_kernel(const RowAr
     c.get(cs);
     s.get(sn);
   }
-  // One head at a time and 64 registers: three heads in flight took 117
-  // registers, half the warps, and 167 us for 32768 rows of 40 heads instead of
-  // 117 (5.9 TB/s).
+  // bf16 rows: the next head's 32 bytes are requested as soon as this one's are in
+  // fp32 registers, which costs no register beyond the 64 of eight blocks an SM
+  // (32768 rows of 40 heads 117 -> 112 us; three heads in flight took 117
+  // registers, half the warps, and 167 us). fp32 rows have 64 bytes a thread in
+  // flight and run at 0.97 - 0.99 of a copy without, at seven blocks (eight spill).
+  constexpr bool kAhead = sizeof(TI) == 2;
   for (int h = head0; h < heads; h += step) {
-    if (h != head0) fetch(h);
+    if (!kAhead && h != head0) fetch(h);
     float a[8], b[8];
     lo.get(a);
     hi.get(b);
+    if (kAhead && h + step < heads) fetch(h + step);
     const bool is_v = APPEND && h >= hq + hk;
     if (!is_v) {
       const TO* gain = static_cast<const TO*>(h < hq ? p.g_q : p.g_k);
@@ -221,13 +225,16 @@ cudaError_t launch_rows(const RowArgs& a, cudaStream_t s, bool pdl) {
                     (APPEND ? a.n_kv_heads : 0);
   // Groups of a row. Few rows: as many as the row has heads, for the most loads
   // at once. Many rows: the split that leaves the fewest groups idle in a row's
-  // last round (40 heads: 8 groups in 5 rounds, not 32 in 2).
+  // last round (40 heads: 8 groups in 5 rounds, not 32 in 2), of those the one
+  // with the most rounds for the row's place and its tables: bf16 down to 4
+  // groups, fp32 to 8 (48 heads of a bf16 append 16 / 8 / 4 / 2 groups 62.2 / 60.2
+  // / 59.7 / 67.5 us, 40 of an fp32 call 8 / 4 / 2 groups 102.4 / 104.7 / 110.7).
   int gpr = 1;
   while (gpr < NG && gpr < heads) gpr *= 2;
   if (static_cast<long long>(a.T) * gpr > 2LL * NG * 8 * num_sms_of_current_device()) {
     int best = gpr;
-    for (int g = gpr; g >= 4; g /= 2)
-      if ((heads + g - 1) / g * g < (heads + best - 1) / best * best) best = g;
+    for (int g = gpr; g >= (sizeof(TI) == 2 ? 4 : 8); g /= 2)
+      if ((heads + g - 1) / g * g <= (heads + best - 1) / best * best) best = g;
     gpr = best;
   }
   const int rpb = NG / gpr;
