@@ -77,6 +77,8 @@ class KvPages(ctypes.Structure):
                 and page_table.dtype == torch.int32 and page_table.is_contiguous())
         self.layout = (k_pool.shape[0], k_pool.shape[2], k_pool.shape[4], _DTYPES.get(k_pool.dtype)) if fits else None
         self.sequences = page_table.shape[0]
+        on = {t.get_device() for t in self._keep}
+        self.device = on.pop() if len(on) == 1 else None
 
 
 class Heads(ctypes.Structure):
@@ -468,10 +470,22 @@ class ChunkWorkspace:
         self.ptr = self.buf.data_ptr()
 
 
+def _here(stream, fn: str, *tensors):
+    """The stream's handle, once every operand is known to lie on the current
+    device (a kernel that met another's or the host's memory would fault)."""
+    handle = _stream(stream)
+    if _cuda or (_cuda is None and torch.cuda.is_available()):
+        device = torch._C._cuda_getDevice()
+        for t in tensors:
+            if t is not None and t.get_device() != device:
+                raise DFlashError(fn, ERR_INVALID_ARG)
+    return handle
+
+
 def _rows(t, n_heads: int, head_dim: int, dtype, fn: str):
-    """(pointer, row stride) of [T, heads, Dh] rows whose heads lie side by side."""
+    """(pointer, row stride, rows) of [T, heads, Dh] rows whose heads lie side by side."""
     if t is None:
-        return None, 0
+        return None, 0, 0
     rows, heads, dh = t.shape
     ld, hs, es = t.stride()
     if heads != n_heads or dh != head_dim or (hs != head_dim and heads > 1) or es != 1:
@@ -479,7 +493,7 @@ def _rows(t, n_heads: int, head_dim: int, dtype, fn: str):
     if _DTYPES.get(t.dtype) != dtype:
         raise DFlashError(fn, ERR_DTYPE)
     # the stride of a single row says nothing
-    return t.data_ptr(), ld if rows > 1 else max(ld, n_heads * head_dim)
+    return t.data_ptr(), ld if rows > 1 else max(ld, n_heads * head_dim), rows
 
 
 def _ints(t, n: int, fn: str):
@@ -487,6 +501,10 @@ def _ints(t, n: int, fn: str):
     if t.dtype is not torch.int32 or t.numel() < n or not t.is_contiguous():
         raise DFlashError(fn, ERR_SHAPE if t.dtype is torch.int32 else ERR_DTYPE)
     return t.data_ptr()
+
+
+def _status(t, fn: str):
+    return _ints(t, 1, fn) if t is not None else None
 
 
 def _gain(t, heads: Heads, fn: str):
@@ -510,9 +528,11 @@ def _tables(c, s, heads: Heads, fn: str):
 
 
 def _view(pages: KvPages, heads: Heads, ctx_len, fn: str):
-    """A page view of the layout, with a table row for every sequence."""
+    """A page view of the layout, with a table row for every sequence, where the lengths lie."""
     if pages.layout != (heads.n_layers, heads.n_kv_heads, heads.head_dim, heads.dtype) or pages.sequences < ctx_len.numel():
         raise DFlashError(fn, ERR_SHAPE)
+    if pages.device != ctx_len.get_device():
+        raise DFlashError(fn, ERR_INVALID_ARG)
     return ctypes.byref(pages)
 
 
@@ -524,19 +544,20 @@ def dflash_qk_norm_rope(heads: Heads, q, k, positions, rope_cos, rope_sin, q_out
     x = q if q is not None else k
     if x is None:
         raise DFlashError(fn, ERR_INVALID_ARG)
-    dt, T, hq, hk, dh, out = _DTYPES.get(x.dtype, -1), x.shape[0], heads.n_q_heads, heads.n_kv_heads, heads.head_dim, heads.dtype
-    if (q is not None and (q_out is None or q_out.shape[0] < T)) or (
-            k is not None and (k_out is None or k_out.shape[0] < T or k.shape[0] != T)):
+    dt, hq, hk, dh, out = _DTYPES.get(x.dtype, -1), heads.n_q_heads, heads.n_kv_heads, heads.head_dim, heads.dtype
+    qp, ldq, n_q = _rows(q, hq, dh, dt, fn)
+    kp, ldk, n_k = _rows(k, hk, dh, dt, fn)
+    qo, ldqo, n_qo = _rows(q_out if q is not None else None, hq, dh, out, fn)
+    ko, ldko, n_ko = _rows(k_out if k is not None else None, hk, dh, out, fn)
+    if n_qo < n_q or n_ko < n_k or (q is not None and k is not None and n_q != n_k):
         raise DFlashError(fn, ERR_SHAPE)
-    qp, ldq = _rows(q, hq, dh, dt, fn)
-    kp, ldk = _rows(k, hk, dh, dt, fn)
-    qo, ldqo = _rows(q_out if q is not None else None, hq, dh, out, fn)
-    ko, ldko = _rows(k_out if k is not None else None, hk, dh, out, fn)
+    T = n_q if q is not None else n_k
     cos, sin, n = _tables(rope_cos, rope_sin, heads, fn)
     _check(fn, load().dflash_qk_norm_rope(
         ctypes.byref(heads), dt, qp, ldq, kp, ldk, _gain(g_q, heads, fn), _gain(g_k, heads, fn),
         _ints(positions, T, fn) if positions is not None else None, cos, sin, n, T, qo, ldqo, ko, ldko,
-        _ptr(dev_status), _tr(trace), _stream(stream)))
+        _status(dev_status, fn), _tr(trace),
+        _here(stream, fn, q, k, q_out, k_out, positions, rope_cos, rope_sin, g_q, g_k, dev_status)))
 
 
 def dflash_kv_append_paged(heads: Heads, q, k, v, cu_rows, ctx_len, layer, pages: KvPages, rope_cos, rope_sin, q_out,
@@ -544,19 +565,20 @@ def dflash_kv_append_paged(heads: Heads, q, k, v, cu_rows, ctx_len, layer, pages
     """Appends packed rows k, v [T, Hkv, Dh] to one layer of the paged cache
     (K normed and rotated on the way); q [T, Hq, Dh] (or None) likewise into q_out."""
     fn = "dflash_kv_append_paged"
-    dt, T, hq, hk, dh = _DTYPES.get(k.dtype, -1), k.shape[0], heads.n_q_heads, heads.n_kv_heads, heads.head_dim
-    if v.shape[0] != T or (q is not None and (q.shape[0] != T or q_out is None or q_out.shape[0] < T)):
+    dt, hq, hk, dh = _DTYPES.get(k.dtype, -1), heads.n_q_heads, heads.n_kv_heads, heads.head_dim
+    qp, ldq, n_q = _rows(q, hq, dh, dt, fn)
+    kp, ldk, T = _rows(k, hk, dh, dt, fn)
+    vp, ldv, n_v = _rows(v, hk, dh, dt, fn)
+    qo, ldqo, n_qo = _rows(q_out if q is not None else None, hq, dh, heads.dtype, fn)
+    if n_v != T or (q is not None and (n_q != T or n_qo < T)):
         raise DFlashError(fn, ERR_SHAPE)
-    qp, ldq = _rows(q, hq, dh, dt, fn)
-    kp, ldk = _rows(k, hk, dh, dt, fn)
-    vp, ldv = _rows(v, hk, dh, dt, fn)
-    qo, ldqo = _rows(q_out if q is not None else None, hq, dh, heads.dtype, fn)
     cos, sin, n = _tables(rope_cos, rope_sin, heads, fn)
     B = ctx_len.numel()
     _check(fn, load().dflash_kv_append_paged(
         ctypes.byref(heads), dt, qp, ldq, kp, ldk, vp, ldv, _gain(g_q, heads, fn), _gain(g_k, heads, fn), cos, sin, n,
         _ints(cu_rows, B + 1, fn), _ints(ctx_len, B, fn), B, T, int(layer), _view(pages, heads, ctx_len, fn), qo, ldqo,
-        _ptr(dev_status), _tr(trace), _stream(stream)))
+        _status(dev_status, fn), _tr(trace),
+        _here(stream, fn, k, v, q, q_out, cu_rows, ctx_len, rope_cos, rope_sin, g_q, g_k, dev_status)))
 
 
 def dflash_attention_chunk_paged(heads: Heads, q, cu_rows, ctx_len, max_rows, max_ctx_hint, layer, pages: KvPages, out,
@@ -564,16 +586,17 @@ def dflash_attention_chunk_paged(heads: Heads, q, cu_rows, ctx_len, max_rows, ma
     """Attention of a ragged batch of chunks q [T, Hq, Dh] over the paged cache
     that already holds the chunks' own keys and values."""
     fn = "dflash_attention_chunk_paged"
-    T, hq, dh, dt = q.shape[0], heads.n_q_heads, heads.head_dim, heads.dtype
-    if out.shape[0] < T:
-        raise DFlashError(fn, ERR_SHAPE)
-    qp, ldq = _rows(q, hq, dh, dt, fn)
-    op, ldo = _rows(out, hq, dh, dt, fn)
+    hq, dh, dt = heads.n_q_heads, heads.head_dim, heads.dtype
+    qp, ldq, T = _rows(q, hq, dh, dt, fn)
+    op, ldo, n_out = _rows(out, hq, dh, dt, fn)
+    if q is None or n_out < T:
+        raise DFlashError(fn, ERR_INVALID_ARG if q is None else ERR_SHAPE)
     B = ctx_len.numel()
     _check(fn, load().dflash_attention_chunk_paged(
         ctypes.byref(heads), qp, ldq, _ints(cu_rows, B + 1, fn), _ints(ctx_len, B, fn), B, T, int(max_rows),
         int(max_ctx_hint), int(layer), _view(pages, heads, ctx_len, fn), 1 if causal else 0, float(scale), op, ldo,
-        _ptr(dev_status), ws.ptr, ws.nbytes, _tr(trace), _stream(stream)))
+        _status(dev_status, fn), ws.ptr, ws.nbytes, _tr(trace),
+        _here(stream, fn, q, out, cu_rows, ctx_len, dev_status, getattr(ws, "buf", None))))
 
 
 def dflash_verify_probs(cfg, target_probs, draft_probs, draft, u_accept, u_draw, tau, committed, next_anchor,
@@ -585,7 +608,7 @@ def dflash_verify_probs(cfg, target_probs, draft_probs, draft, u_accept, u_draw,
     dt = _DTYPES.get(target_probs.dtype, -1)
     if R != cfg.gamma + 1 or V != cfg.vocab or not target_probs.is_contiguous() or (
             draft_probs is not None and (draft_probs.shape != (B, R - 1, V) or not draft_probs.is_contiguous())) or (
-            u_accept.numel() < B * (R - 1) or u_draw.numel() < B or not u_accept.is_contiguous()):
+            u_accept.numel() < B * (R - 1) or u_draw.numel() < B or not u_accept.is_contiguous() or not u_draw.is_contiguous()):
         raise DFlashError(fn, ERR_SHAPE)
     f32 = torch.float32
     if u_accept.dtype is not f32 or u_draw.dtype is not f32 or (draft_probs is not None and draft_probs.dtype is not f32):
@@ -593,8 +616,9 @@ def dflash_verify_probs(cfg, target_probs, draft_probs, draft, u_accept, u_draw,
     _check(fn, load().dflash_verify_probs(
         ctypes.byref(cfg), target_probs.data_ptr(), dt, _ptr(draft_probs), _ints(draft, B * (R - 1), fn),
         _ints(gamma_b, B, fn) if gamma_b is not None else None, u_accept.data_ptr(), u_draw.data_ptr(), B,
-        _ints(tau, B, fn), _ints(committed, B * R, fn), _ints(next_anchor, B, fn), _ptr(dev_status), _tr(trace),
-        _stream(stream)))
+        _ints(tau, B, fn), _ints(committed, B * R, fn), _ints(next_anchor, B, fn), _status(dev_status, fn), _tr(trace),
+        _here(stream, fn, target_probs, draft_probs, draft, u_accept, u_draw, gamma_b, tau, committed, next_anchor,
+              dev_status)))
 
 
 class TraceRecorder:

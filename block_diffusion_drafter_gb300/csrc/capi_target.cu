@@ -25,6 +25,8 @@ bool heads_pages_ok(const dflash_kv_pages* p) {
          static_cast<long long>(p->pages_per_seq) * DFLASH_PAGE_KEYS <= INT32_MAX;
 }
 
+constexpr int kMaxRows = INT32_MAX - 1024;   // row indices of the last block stay in 32 bits
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Element types of the row operators' inputs: cfg.dtype, or fp32 rows (a
@@ -75,6 +77,12 @@ dflash_status dflash_qk_norm_rope(const dflash_heads* h, dflash_dtype in_dtype, 
   if (k != nullptr && ((st = rows_ok(k, ld_k, wk, is)) != DFLASH_OK || (st = rows_ok(k_out, ld_ko, wk, es)) != DFLASH_OK))
     return st;
   if (!aligned16(g_q) || !aligned16(g_k)) return DFLASH_ERR_ALIGN;
+  if (T > kMaxRows) return DFLASH_ERR_TOO_LARGE;
+  // in place: the same rows; no output over another part's rows
+  if ((q != nullptr && q_out == q && (in_dtype != h->dtype || ld_q != ld_qo)) ||
+      (k != nullptr && k_out == k && (in_dtype != h->dtype || ld_k != ld_ko)) ||
+      (q != nullptr && k != nullptr && (q_out == k || k_out == q || q_out == k_out)))
+    return DFLASH_ERR_INVALID_ARG;
   if ((st = check_arch()) != DFLASH_OK) return st;
   RowArgs a{};
   a.q = q; a.k = k; a.ldq = ld_q; a.ldk = ld_k;
@@ -116,6 +124,10 @@ dflash_status dflash_kv_append_paged(const dflash_heads* h, dflash_dtype in_dtyp
   if ((st = rows_ok(k, ld_k, wk, is)) != DFLASH_OK || (st = rows_ok(v, ld_v, wk, is)) != DFLASH_OK) return st;
   if (!aligned16(g_q) || !aligned16(g_k) || !aligned16(pages->k_pool) || !aligned16(pages->v_pool))
     return DFLASH_ERR_ALIGN;
+  if (T > kMaxRows) return DFLASH_ERR_TOO_LARGE;
+  if (pages->k_pool == pages->v_pool ||
+      (q != nullptr && ((q_out == q && (in_dtype != h->dtype || ld_q != ld_qo)) || q_out == k || q_out == v)))
+    return DFLASH_ERR_INVALID_ARG;
   if ((st = check_arch()) != DFLASH_OK) return st;
   RowArgs a{};
   a.q = q; a.k = k; a.v = v; a.ldq = ld_q; a.ldk = ld_k; a.ldv = ld_v;
@@ -165,6 +177,7 @@ dflash_status dflash_attention_chunk_paged(const dflash_heads* h, const void* q,
       static_cast<long long>(T) * (h->n_q_heads / h->n_kv_heads) > INT32_MAX / 2 || B > INT32_MAX / 256)
     return DFLASH_ERR_TOO_LARGE;
   if (ws == nullptr || ws_bytes < dflash_attention_chunk_bytes(h)) return DFLASH_ERR_WORKSPACE;
+  if (q == out) return DFLASH_ERR_INVALID_ARG;
   if ((st = check_arch()) != DFLASH_OK) return st;
   ChunkArgs a{};
   a.q = q; a.out = out; a.ldq = ld_q; a.ldo = ld_o;

@@ -509,8 +509,9 @@ dflash_status dflash_check_heads(const dflash_heads* heads);
  *   were. rope_cos, rope_sin: fp32 [rope_positions, Dh/2]; both NULL: no
  *   rotation (positions may then be NULL).
  * q_out, k_out: heads.dtype; may be q and k themselves (same types and
- *   strides). Partly overlapping operands are not allowed. T == 0 launches
- *   nothing. Statistics are fp32; an output is rounded once. */
+ *   strides). Partly overlapping operands are not allowed (outputs that begin
+ *   where another operand does are refused, DFLASH_ERR_INVALID_ARG). T == 0
+ *   launches nothing. Statistics are fp32; an output is rounded once. */
 dflash_status dflash_qk_norm_rope(const dflash_heads* heads, dflash_dtype in_dtype, const void* q,
                                   long long ld_q, const void* k, long long ld_k, const void* g_q,
                                   const void* g_k, const int32_t* positions, const float* rope_cos,
@@ -553,7 +554,7 @@ size_t dflash_attention_chunk_bytes(const dflash_heads* heads);
  * 0 .. ctx_len[b] + n_b - 1 (causal = 0, as in the drafter's bidirectional
  * block), n_b = cu_rows[b + 1] - cu_rows[b]. A row that sees no key (a negative ctx_len) gives zeros.
  * q, out: [T, Hq, Dh] of heads.dtype, rows ld_q / ld_o elements apart; out must
- *   not overlap q. scale: 0 for 1/sqrt(Dh).
+ *   not overlap q (out == q: DFLASH_ERR_INVALID_ARG). scale: 0 for 1/sqrt(Dh).
  * Key and value rows below ctx_len[b] + n_b must be finite; later rows of a
  *   page are never used and may hold anything.
  * max_rows, max_ctx_hint: host bounds of n_b and ctx_len[b] that only size the

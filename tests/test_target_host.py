@@ -118,8 +118,27 @@ def test_verify_probs_refusals(lib):
             ({name: None}, "INVALID_ARG") for name in ("p", "d", "ua", "ud", "tau", "com", "nxt", "st")]:
         assert verify(lib, cfg, **kw) == getattr(lib, "ERR_" + want), kw
     bad = lib.config_from_workload(synth.WORKLOADS["tiny_f32_L1_N128"])
+    bad.vocab = (1 << 24) + 1
+    assert verify(lib, bad) == lib.ERR_TOO_LARGE
+    bad.vocab = cfg.vocab
     bad.gamma = 17
     assert verify(lib, bad) == lib.ERR_INVALID_ARG
+
+
+def test_outputs_over_other_operands_are_refused(lib, heads):
+    """In place is for rows of one type and stride; an output over another operand's rows is refused."""
+    at = [FAKE + (i << 16) for i in range(8)]
+    apart = dict(q=at[0], k=at[1], qo=at[2], ko=at[3])
+    for kw in (dict(qo=at[0], ldqo=2048), dict(ko=at[1], ldk=512), dict(qo=at[1]), dict(ko=at[0]), dict(ko=at[2]),
+               dict(qo=at[0], in_dtype=lib.F32)):
+        assert norm_rope(lib, heads, **{**apart, **kw}) == lib.ERR_INVALID_ARG, kw
+    assert norm_rope(lib, heads, **apart, T=2 ** 31 - 1) == lib.ERR_TOO_LARGE
+    apart = dict(q=at[0], k=at[1], v=at[2], qo=at[3], pages=pages_of(lib, k=at[4], v=at[5]))
+    for kw in (dict(qo=at[0]), dict(qo=at[0], in_dtype=lib.BF16, ldqo=2048), dict(qo=at[1]), dict(qo=at[2]),
+               dict(pages=pages_of(lib, k=at[4], v=at[4]))):
+        assert append(lib, heads, **{**apart, **kw}) == lib.ERR_INVALID_ARG, kw
+    assert append(lib, heads, **apart, T=2 ** 31 - 1) == lib.ERR_TOO_LARGE
+    assert attend(lib, heads, q=at[0], out=at[0]) == lib.ERR_INVALID_ARG
 
 
 def test_the_binding_refuses_rows_that_do_not_fit_the_layout(lib, heads):
@@ -144,6 +163,9 @@ def test_the_binding_refuses_rows_that_do_not_fit_the_layout(lib, heads):
     assert e.value.status == lib.ERR_DTYPE
     with pytest.raises(lib.DFlashError) as e:
         lib.dflash_qk_norm_rope(heads, None, None, ctx, None, None, None, None, st)
+    assert e.value.status == lib.ERR_INVALID_ARG
+    with pytest.raises(lib.DFlashError) as e:
+        lib.dflash_attention_chunk_paged(heads, None, cu, ctx, 3, 0, 0, pages, q, st, ws)
     assert e.value.status == lib.ERR_INVALID_ARG
     with pytest.raises(lib.DFlashError):
         lib.ChunkWorkspace(lib.make_heads(1, 3, 2, 128), device="cpu")
