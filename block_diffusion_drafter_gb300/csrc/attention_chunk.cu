@@ -318,9 +318,11 @@ template <int DH>
 cudaError_t launch_merge(const ChunkArgs& a, int ctas, int y, cudaStream_t s, bool pdl) {
   // Long chunks have many units, each in two or three parts: two requested at
   // once leave room for more warps than eight (with eight, a 2048-token chunk's
-  // merge took 12 us). Few rows behind a long context have one unit in many parts.
+  // merge took 12 us). Few rows behind a long context have one unit in up to 19
+  // parts: ten at once, two round trips (17 rows behind 32768 keys, batches of
+  // 6 / 8 / 10: 32.6 / 33.1 / 32.5 us; 16 leave too few warps, 35.6).
   return y == kChunkRows / 8 ? launch_plain(chunk_merge_kernel<__nv_bfloat16, DH, 2>, dim3(ctas, y), 128, 0, s, pdl, a)
-                             : launch_plain(chunk_merge_kernel<__nv_bfloat16, DH, 8>, dim3(ctas, y), 128, 0, s, pdl, a);
+                             : launch_plain(chunk_merge_kernel<__nv_bfloat16, DH, 10>, dim3(ctas, y), 128, 0, s, pdl, a);
 }
 
 }  // namespace

@@ -11,7 +11,8 @@
 // and single tokens the batch holds: a CTA walks through its range, and only
 // the first and the last unit of a range can be incomplete. Incomplete units
 // write unnormalised rows to the workspace; chunk_merge_kernel joins them in
-// key order.
+// key order. Over few pages (whole_units) a unit goes to the CTA in whose range it
+// starts, and no merge follows.
 //
 // Two streams keep the tensor core busy: each has its own S / P and O columns in
 // TMEM and its own four softmax warps, one thread a row.
@@ -22,7 +23,7 @@
 //              (O, max, sum) are joined at the end of the piece.
 // So while one stream's scores are in the softmax, the other's products run.
 // P goes back to TMEM over the columns of its own S (bf16, half the columns)
-// and is the A operand of the second product. A thread of its own issues each
+// and is the A operand of the second product. A warp of its own issues each
 // stream's MMAs, S of the next page after P V of the last one on the same
 // columns; the tensor core executes them in that order.
 //
