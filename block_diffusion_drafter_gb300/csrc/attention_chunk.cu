@@ -328,18 +328,30 @@ cudaError_t launch_merge(const ChunkArgs& a, int ctas, int y, cudaStream_t s, bo
 }  // namespace
 
 // Over few pages units stay whole, each with the CTA in whose range it starts:
-// the merge of split ones is a launch of its own (1.3 to 4 us) and costs more
-// than the pages one after another. Split / whole, 32 heads over 8, in us:
-//   up to 3 pages: 1 row, 100 keys 9.7 / 8.3; 8 x 17 rows, 317 keys 15.8 / 12.2;
-//     256 rows 16.8 / 12.0
-//   6 pages: 512 rows 19.1 / 15.1, 4 x 300 rows behind 300 keys 30.6 / 26.9, but
-//     1 row, 701 keys 11.1 / 14.1 and 20 x 2 rows, 702 keys 23.4 / 26.8: whole
-//     only where the chunk fills a unit's 256 rows, whose pages cost less
-//     beside the unit's own share.
+// the merge of split ones is a launch of its own and costs more than the pages
+// one after another. The hints tell what the longest unit costs (in the ranges'
+// measure, 0.39 us each) and the least that equal ranges could take; partial rows
+// and merge cost about 35 beside two tiles of rows, 25 beside one, 19 for a token.
+// Split / whole, 32 heads over 8, in us: 1 row, 101 keys 9.1 / 7.9, 701 keys 10.5 /
+// 13.5; 8 x 17 rows, 317 keys 15.6 / 11.9, 717 keys 17.7 / 15.4; one of them, 717 keys
+// 11.7 / 13.8; prompts of 256 / 512 / 1000 tokens 15.8 / 10.6, 18.2 / 13.9, 25.7 / 20.5;
+// 300 rows behind 900 keys 21.0 / 27.4. With more units than CTAs some take two:
+// whole up to 3 pages, and 6 where the chunk fills a unit (4 x 300 rows behind 300
+// keys 29.2 / 24.5, 20 x 2 rows, 702 keys 22.4 / 26.4). Lengths far below the hints
+// cost at most the longest unit, so that has 8 pages at most.
 bool keep_whole(const ChunkArgs& a) {
-  const long long keys = static_cast<long long>(a.max_ctx) + a.max_rows;
-  const long long rows = static_cast<long long>(a.max_rows) * (a.n_q_heads / a.n_kv_heads);
-  return keys <= (rows > kChunkRows ? 6 : 3) * kPageKeys;
+  const int G = a.n_q_heads / a.n_kv_heads, tok = kChunkRows / G, sms = num_sms_of_current_device();
+  const long long rows = static_cast<long long>(a.max_rows) * G;
+  const long long pages = (static_cast<long long>(a.max_ctx) + a.max_rows + kPageKeys - 1) / kPageKeys;
+  if (pages > 8) return false;
+  const long long most = (static_cast<long long>(a.T) + static_cast<long long>(a.B) * (tok - 1)) / tok;
+  const long long hinted = static_cast<long long>(a.B) * ((a.max_rows + tok - 1) / tok);
+  const long long units = (hinted < most ? hinted : most) * a.n_kv_heads;
+  if (units > sms) return pages <= (rows > kChunkRows ? 6 : 3);
+  const bool two = rows > kChunkRows / 2;
+  const int share = two ? 15 : rows > 32 ? 12 : 9, page = two ? 5 : 4, merge = two ? 35 : rows > 8 ? 25 : 19;
+  const long long before = a.causal ? a.max_rows / (2 * kPageKeys) : 0;   // pages that a unit sees less, on average
+  return share + page * pages <= units * (share + page * (pages - before)) / sms + merge;
 }
 
 cudaError_t launch_attention_chunk(const ChunkArgs& args, int bf16, cudaStream_t s, bool pdl, Tracer& tr, double bytes,

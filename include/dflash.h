@@ -557,9 +557,10 @@ size_t dflash_attention_chunk_bytes(const dflash_heads* heads);
  *   not overlap q (out == q: DFLASH_ERR_INVALID_ARG). scale: 0 for 1/sqrt(Dh).
  * Key and value rows below ctx_len[b] + n_b must be finite; later rows of a
  *   page are never used and may hold anything.
- * max_rows, max_ctx_hint: host bounds of n_b and ctx_len[b] that only size the
- *   grid (any value >= 0 is correct, tight ones are faster); a trace record
- *   counts K/V bytes and flops as if every sequence had max_ctx_hint keys.
+ * max_rows, max_ctx_hint: host bounds of n_b and ctx_len[b] that only size and
+ *   divide the work (any value >= 0 is correct, tight bounds are faster, lengths
+ *   far above them much slower); a trace record counts K/V bytes and flops as if
+ *   every sequence had max_ctx_hint keys.
  * Keys beyond a sequence's table and entries outside [0, n_pages) set
  * DFLASH_ERR_CAPACITY; that sequence's output is then unspecified.
  * Results do not depend on timing or on the hints beyond rounding: splits are
