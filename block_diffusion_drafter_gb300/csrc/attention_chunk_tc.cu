@@ -725,11 +725,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           // page that is cut anywhere is a unit's last one or two.)
           const int seen = lim - kb;      // keys of this page that the row sees
           if (__any_sync(0xffffffffu, seen < kKeys)) {
+            // From the first column that a row of the warp's does not see; behind the last
+            // one that any sees unread. (All columns read and written: six prompts of 500
+            // to 2000 tokens 137 instead of 114 us.)
+            const int all = __reduce_min_sync(0xffffffffu, valid ? max(seen, 0) : kKeys);
+            const int some = __reduce_max_sync(0xffffffffu, seen);
 #pragma unroll 1
-            for (int c = 0; c < kKeys; c += 16) {
+            for (int c = all & ~15; c < kKeys; c += 16) {
               float v[16];
-              tmem_ld16(t_s + c, v);
-              tmem_ld_wait();
+              if (c < some) {
+                tmem_ld16(t_s + c, v);
+                tmem_ld_wait();
+              }
 #pragma unroll
               for (int i = 0; i < 16; ++i) v[i] = c + i < seen ? v[i] : -INFINITY;
               tmem_st16(t_s + c, v);
