@@ -17,9 +17,14 @@ constexpr float kLog2eC = 1.4426950408889634f;
 // ------------------------------------------------------------------ fp32
 // One CTA per (unit of 16 RT packed rows, KV head, split). Keys in tiles of
 // kSimtKeys through shared memory; thread (ty, tx) of 16 x 16 holds an RT x 4 piece
-// of the score tile and rows RT ty.. x columns tx + 16 c of the output. RT is 4,
+// of the score tile and rows RT ty.. x columns 4 tx + 64 c .. + 3 of the output. RT is 4,
 // or less where the chunks are hinted to have fewer rows (a drafted block of 17
-// rows of one head each: 32 rows a unit instead of 64).
+// rows of one head each: 32 rows a unit instead of 64), or 8. Bound by the shared
+// memory's bandwidth: 20 16-byte reads for 192 multiply-adds a thread (RT 4, four
+// columns of the scores and four keys of the products). Values are on their way
+// during the scores and the next keys during the products: 10 sequences of 47 rows
+// of 10 heads behind 6681 keys 677 -> 528 us, with 8 rows a thread and the splits
+// chosen for whole waves (29 TFLOP/s of fp32).
 constexpr int kSimtKeys = 64, kSimtThreads = 256;
 
 template <int DH, int RT>
@@ -27,12 +32,11 @@ constexpr size_t simt_smem() {
   return sizeof(float) * (static_cast<size_t>(16 * RT + 2 * kSimtKeys) * (DH + 4) + 16 * RT * (kSimtKeys + 4));
 }
 
-// CTAs an SM that leave each variant registers enough not to spill and keep its
-// loads together (left to itself the compiler took 80 for 32 rows of 64 columns:
-// three ragged blocks of the tiny shape 14.3 instead of 12.6 us; 200 rows of 32 heads
-// of 128 behind 1000 keys 194 instead of 180).
+// CTAs an SM that leave each variant registers enough to keep its loads together
+// (the compiler's own choice, three of 80 registers, spilled: three ragged blocks
+// of the tiny shape 14.3 instead of 12.6 us).
 template <int DH, int RT>
-constexpr int simt_ctas() { return RT == 1 ? 3 : DH == 64 && RT == 4 ? 2 : 1; }
+constexpr int simt_ctas() { return RT == 1 || (DH == 64 && RT <= 4) ? 2 : 1; }
 
 template <int DH, int RT>
 __global__ void __launch_bounds__(kSimtThreads, (simt_ctas<DH, RT>())) chunk_simt_kernel(const ChunkArgs p, int splits) {
@@ -92,23 +96,29 @@ __global__ void __launch_bounds__(kSimtThreads, (simt_ctas<DH, RT>())) chunk_sim
     for (int c = 0; c < DC; ++c) o[i][c] = 0.f;
   }
   const float scale = p.scale * kLog2eC;
-  for (int t = t0; t < t1; ++t) {
+  // rows of a tile to shared memory, zeros behind the last key (the rows there may hold anything)
+  auto fetch = [&](const void* pool, float* dst, int t) {
     const int k0 = t * kSimtKeys;
-    __syncthreads();
     // a tile lies inside one page
     const int page = page_of(p, u.b, k0);
     const size_t base = ((static_cast<size_t>(p.layer) * p.pages.n_pages + page) * p.n_kv_heads + kvh) *
                             static_cast<size_t>(kPageKeys) + k0 % kPageKeys;
-    const float* kg = static_cast<const float*>(p.k_pool) + base * DH;
-    const float* vg = static_cast<const float*>(p.v_pool) + base * DH;
+    const float* g = static_cast<const float*>(pool) + base * DH;
 #pragma unroll
     for (int i = threadIdx.x; i < kSimtKeys * D4; i += kSimtThreads) {
       const int r = i / D4, d = i % D4 * 4;
-      const bool in = k0 + r < keys;   // rows behind the last key may hold anything
-      *reinterpret_cast<float4*>(&sk[r * LD + d]) = in ? *reinterpret_cast<const float4*>(&kg[r * DH + d]) : none;
-      *reinterpret_cast<float4*>(&sv[r * LD + d]) = in ? *reinterpret_cast<const float4*>(&vg[r * DH + d]) : none;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(&dst[r * LD + d])), "l"(g + r * DH + d),
+                   "r"(k0 + r < keys ? 16 : 0)
+                   : "memory");
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (t0 < t1) fetch(p.k_pool, sk, t0);
+  for (int t = t0; t < t1; ++t) {   // values come during the scores, the next keys during the products
+    const int k0 = t * kSimtKeys;
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
+    fetch(p.v_pool, sv, t);
     float s[RT][4];
 #pragma unroll
     for (int i = 0; i < RT; ++i)
@@ -154,18 +164,30 @@ __global__ void __launch_bounds__(kSimtThreads, (simt_ctas<DH, RT>())) chunk_sim
 #pragma unroll
       for (int c = 0; c < DC; ++c) o[i][c] *= al;
     }
-    __syncwarp();   // a warp's rows of sp are its own
-#pragma unroll 4
-    for (int j = 0; j < kSimtKeys; ++j) {
-      float pr[RT];
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();   // also: all threads have left the keys
+    if (t + 1 < t1) fetch(p.k_pool, sk, t + 1);
+#pragma unroll 2
+    for (int j = 0; j < kSimtKeys; j += 4) {
+      float pr[RT][4];
 #pragma unroll
-      for (int i = 0; i < RT; ++i) pr[i] = sp[(RT * ty + i) * LP + j];
-#pragma unroll
-      for (int c = 0; c < DC; ++c) {
-        const float v = sv[j * LD + tx + 16 * c];
-#pragma unroll
-        for (int i = 0; i < RT; ++i) o[i][c] += pr[i] * v;
+      for (int i = 0; i < RT; ++i) {
+        const float4 e = *reinterpret_cast<const float4*>(&sp[(RT * ty + i) * LP + j]);
+        pr[i][0] = e.x; pr[i][1] = e.y; pr[i][2] = e.z; pr[i][3] = e.w;
       }
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+        for (int c = 0; c < DC; c += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(&sv[(j + jj) * LD + 4 * tx + 16 * c]);
+#pragma unroll
+          for (int i = 0; i < RT; ++i) {
+            o[i][c] += pr[i][jj] * v.x;
+            o[i][c + 1] += pr[i][jj] * v.y;
+            o[i][c + 2] += pr[i][jj] * v.z;
+            o[i][c + 3] += pr[i][jj] * v.w;
+          }
+        }
     }
   }
 #pragma unroll
@@ -176,11 +198,13 @@ __global__ void __launch_bounds__(kSimtThreads, (simt_ctas<DH, RT>())) chunk_sim
       const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
       float* y = static_cast<float*>(p.out) + (u.row0 + u.tok0 + r / G) * p.ldo + (kvh * G + r % G) * DH;
 #pragma unroll
-      for (int c = 0; c < DC; ++c) y[tx + 16 * c] = o[i][c] * inv;
+      for (int c = 0; c < DC; c += 4)
+        *reinterpret_cast<float4*>(&y[4 * tx + 16 * c]) = make_float4(o[i][c] * inv, o[i][c + 1] * inv, o[i][c + 2] * inv, o[i][c + 3] * inv);
     } else {
       float* slot = p.partials + static_cast<size_t>(unit * splits + sp_i) * chunk_slot_floats(DH);
 #pragma unroll
-      for (int c = 0; c < DC; ++c) slot[partial_at<DH>(r, (tx + 16 * c) >> 2) + (tx & 3)] = o[i][c];
+      for (int c = 0; c < DC; c += 4)
+        *reinterpret_cast<float4*>(slot + partial_at<DH>(r, tx + 4 * c)) = make_float4(o[i][c], o[i][c + 1], o[i][c + 2], o[i][c + 3]);
       if (tx == 0)
         reinterpret_cast<float2*>(slot + static_cast<size_t>(kChunkRows) * DH)[r] = make_float2(m[i], l[i]);
     }
@@ -275,21 +299,42 @@ cudaError_t launch_plain(K kernel, dim3 grid, int threads, size_t smem, cudaStre
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// How a batch is cut for units of 16 RT rows: units (at most: every sequence's
+// last one holds one row), and the splits of their keys that leave the fewest
+// tiles one after another, the merge counted as one. cost: in hundredths of the
+// time of a tile of 64 rows.
+struct SimtPlan {
+  long long units, work, cost;
+  int splits;
+};
 template <int DH, int RT>
-cudaError_t launch_simt(const ChunkArgs& a, cudaStream_t s, bool pdl, Tracer& tr, double bytes, double flops) {
-  constexpr int rows = 16 * RT;
-  const int tok = rows / (a.n_q_heads / a.n_kv_heads);
-  // at most: every sequence's last unit holds one row
-  const long long units = (static_cast<long long>(a.T) + static_cast<long long>(a.B) * (tok - 1)) / tok;
-  const long long work = units * a.n_kv_heads;
-  int splits = 1;
-  if (work > 0 && work < num_sms_of_current_device()) {
-    const int tiles = (a.max_ctx + a.max_rows + kSimtKeys - 1) / kSimtKeys;
-    splits = static_cast<int>(2LL * num_sms_of_current_device() / work);
-    if (splits > kChunkSlots / work) splits = static_cast<int>(kChunkSlots / work);
-    if (splits > tiles) splits = tiles;
-    if (splits < 1) splits = 1;
+SimtPlan plan_simt(const ChunkArgs& a) {
+  const int tok = 16 * RT / (a.n_q_heads / a.n_kv_heads);
+  SimtPlan r{};
+  r.units = (static_cast<long long>(a.T) + static_cast<long long>(a.B) * (tok - 1)) / tok;
+  r.work = r.units * a.n_kv_heads;
+  r.splits = 1;
+  const long long hinted = static_cast<long long>(a.B) * ((a.max_rows + tok - 1) / tok) * a.n_kv_heads;
+  const long long busy = hinted > 0 && hinted < r.work ? hinted : r.work;   // the rest of the grid finds no unit
+  const long long slots = static_cast<long long>(num_sms_of_current_device()) * simt_ctas<DH, RT>();
+  const long long tiles = (static_cast<long long>(a.max_ctx) + a.max_rows + kSimtKeys - 1) / kSimtKeys;
+  for (int n = 1; n == 1 || (n <= 64 && n <= tiles && n * r.work <= kChunkSlots); ++n) {
+    const long long waves = (busy * n + slots - 1) / slots;
+    const long long cost = waves * ((tiles + n - 1) / n) * (RT == 8 ? 173 : 100) + (n > 1 ? 100 : 0);
+    if (n == 1 || cost < r.cost) {
+      r.cost = cost;
+      r.splits = n;
+    }
   }
+  return r;
+}
+
+template <int DH, int RT>
+cudaError_t launch_simt(const ChunkArgs& a, const SimtPlan& plan, cudaStream_t s, bool pdl, Tracer& tr, double bytes,
+                        double flops) {
+  constexpr int rows = 16 * RT;
+  const long long units = plan.units, work = plan.work;
+  const int splits = plan.splits;
   constexpr size_t smem = simt_smem<DH, RT>();
   static bool done[64] = {};
   int dev = 0;
@@ -316,9 +361,16 @@ template <int DH>
 cudaError_t launch_f32(const ChunkArgs& a, cudaStream_t s, bool pdl, Tracer& tr, double bytes, double flops) {
   const int G = a.n_q_heads / a.n_kv_heads;
   const long long rows = static_cast<long long>(a.max_rows) * G;
-  if (rows <= 16 && G <= 16) return launch_simt<DH, 1>(a, s, pdl, tr, bytes, flops);
-  if (rows <= 32 && G <= 32) return launch_simt<DH, 2>(a, s, pdl, tr, bytes, flops);
-  return launch_simt<DH, 4>(a, s, pdl, tr, bytes, flops);
+  if (rows <= 16 && G <= 16) return launch_simt<DH, 1>(a, plan_simt<DH, 1>(a), s, pdl, tr, bytes, flops);
+  if (rows <= 32 && G <= 32) return launch_simt<DH, 2>(a, plan_simt<DH, 2>(a), s, pdl, tr, bytes, flops);
+  // 128 rows a unit read the shared tiles half as often for their products (2 x 64
+  // rows of 28 heads behind 9000 keys 609 -> 529 us), where that leaves CTAs enough.
+  const SimtPlan flat = plan_simt<DH, 4>(a);
+  if (DH == 128 && rows > 64) {
+    const SimtPlan tall = plan_simt<DH, 8>(a);
+    if (tall.cost < flat.cost) return launch_simt<DH, 8>(a, tall, s, pdl, tr, bytes, flops);
+  }
+  return launch_simt<DH, 4>(a, flat, s, pdl, tr, bytes, flops);
 }
 
 template <int DH>

@@ -132,6 +132,16 @@ def test_long_contexts_split_over_the_gpu(dfl, shape, ns, ctxs):
     s.check(rows=8)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("hq,hkv", [(28, 4), (8, 2), (64, 1), (3, 3)])
+@pytest.mark.parametrize("ns,ctxs", [([64, 17, 64], [700, 0, 333]), ([1, 200, 0, 131], [64, 1000, 5, 127])])
+def test_fp32_chunks_of_many_rows(dfl, causal, hq, hkv, ns, ctxs):
+    """Units of 64 and of 128 rows, in one part and in several, whichever the sizes call for."""
+    s = Scene(dfl, F32, hq, hkv, 128, ns, ctxs, seed=29)
+    s.run(causal=causal)
+    s.check(causal=causal, rows=12)
+
+
 @pytest.mark.parametrize("shape", ["qwen", "f32_64"])
 def test_hints_do_not_change_what_is_computed(dfl, shape):
     """Any hint is allowed: too small ones, too large ones."""
