@@ -23,8 +23,8 @@ constexpr float kLog2eC = 1.4426950408889634f;
 // memory's bandwidth: 20 16-byte reads for 192 multiply-adds a thread (RT 4, four
 // columns of the scores and four keys of the products). Values are on their way
 // during the scores and the next keys during the products: 10 sequences of 47 rows
-// of 10 heads behind 6681 keys 677 -> 528 us, with 8 rows a thread and the splits
-// chosen for whole waves (29 TFLOP/s of fp32).
+// of 10 heads behind 6681 keys 677 -> 461 us, with 8 rows a thread and the splits
+// chosen for whole waves (35 TFLOP/s of fp32).
 constexpr int kSimtKeys = 64, kSimtThreads = 256;
 
 template <int DH, int RT>
@@ -201,12 +201,12 @@ __global__ void __launch_bounds__(kSimtThreads, (simt_ctas<DH, RT>())) chunk_sim
       for (int c = 0; c < DC; c += 4)
         *reinterpret_cast<float4*>(&y[4 * tx + 16 * c]) = make_float4(o[i][c] * inv, o[i][c + 1] * inv, o[i][c + 2] * inv, o[i][c + 3] * inv);
     } else {
-      float* slot = p.partials + static_cast<size_t>(unit * splits + sp_i) * chunk_slot_floats(DH);
+      float* slot = p.partials + static_cast<size_t>(unit * splits + sp_i) * (kSimtRows * (DH + 2));
 #pragma unroll
       for (int c = 0; c < DC; c += 4)
         *reinterpret_cast<float4*>(slot + partial_at<DH>(r, tx + 4 * c)) = make_float4(o[i][c], o[i][c + 1], o[i][c + 2], o[i][c + 3]);
       if (tx == 0)
-        reinterpret_cast<float2*>(slot + static_cast<size_t>(kChunkRows) * DH)[r] = make_float2(m[i], l[i]);
+        reinterpret_cast<float2*>(slot + kSimtRows * DH)[r] = make_float2(m[i], l[i]);
     }
   }
 }
@@ -216,13 +216,14 @@ __global__ void __launch_bounds__(kSimtThreads, (simt_ctas<DH, RT>())) chunk_sim
 // 8x .. 8x+7, a warp a quarter of the columns, a lane four columns of one row.
 // The parts' rows, maxima and sums of BATCH splits are requested at once;
 // they are added in ascending split order (a batch at a time, under the
-// running maximum), so a result does not depend on timing.
+// running maximum), so a result does not depend on timing. SLOT_ROWS: rows that a
+// part's slot holds.
 __device__ __forceinline__ void store_out(float* y, float4 v) { *reinterpret_cast<float4*>(y) = v; }
 __device__ __forceinline__ void store_out(__nv_bfloat16* y, float4 v) {
   __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
   *reinterpret_cast<uint2*>(y) = make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
 }
-template <typename T, int DH, int BATCH>
+template <typename T, int DH, int BATCH, int SLOT_ROWS>
 __global__ void __launch_bounds__(128) chunk_merge_kernel(const ChunkArgs p) {
   constexpr int NL = DH / 64;   // loads of 16 columns a warp
   pdl_launch_dependents();
@@ -247,8 +248,8 @@ __global__ void __launch_bounds__(128) chunk_merge_kernel(const ChunkArgs p) {
         ml[k] = make_float2(-INFINITY, 0.f);
         if (s0 + k < S) {
           const int at = s0 + k == 0 ? first : rest + (s0 + k - 1) * step;
-          const float* slot = p.partials + static_cast<size_t>(at) * chunk_slot_floats(DH);
-          ml[k] = __ldcg(reinterpret_cast<const float2*>(slot + static_cast<size_t>(kChunkRows) * DH) + r);
+          const float* slot = p.partials + static_cast<size_t>(at) * (SLOT_ROWS * (DH + 2));
+          ml[k] = __ldcg(reinterpret_cast<const float2*>(slot + SLOT_ROWS * DH) + r);
 #pragma unroll
           for (int i = 0; i < NL; ++i) x[k][i] = __ldcg(reinterpret_cast<const float4*>(slot + partial_at<DH>(r, c0 + 4 * i)));
         }
@@ -318,7 +319,9 @@ SimtPlan plan_simt(const ChunkArgs& a) {
   const long long busy = hinted > 0 && hinted < r.work ? hinted : r.work;   // the rest of the grid finds no unit
   const long long slots = static_cast<long long>(num_sms_of_current_device()) * simt_ctas<DH, RT>();
   const long long tiles = (static_cast<long long>(a.max_ctx) + a.max_rows + kSimtKeys - 1) / kSimtKeys;
-  for (int n = 1; n == 1 || (n <= 64 && n <= tiles && n * r.work <= kChunkSlots); ++n) {
+  // the workspace holds this many parts of 16 RT rows, and a descriptor a unit
+  const long long parts = r.work <= kChunkDescs ? static_cast<long long>(kChunkSlots) * (kChunkRows / (16 * RT)) : 0;
+  for (int n = 1; n == 1 || (n <= 64 && n <= tiles && n * r.work <= parts); ++n) {
     const long long waves = (busy * n + slots - 1) / slots;
     const long long cost = waves * ((tiles + n - 1) / n) * (RT == 8 ? 173 : 100) + (n > 1 ? 100 : 0);
     if (n == 1 || cost < r.cost) {
@@ -352,7 +355,7 @@ cudaError_t launch_simt(const ChunkArgs& a, const SimtPlan& plan, cudaStream_t s
   tr.after();
   if (e != cudaSuccess || splits == 1) return e;
   tr.before(DFLASH_K_ATTN, 0.0, 0.0);
-  e = launch_plain(chunk_merge_kernel<float, DH, 8>, dim3(static_cast<unsigned>(work), rows / 8), 128, 0, s, pdl, a);
+  e = launch_plain(chunk_merge_kernel<float, DH, 8, rows>, dim3(static_cast<unsigned>(work), rows / 8), 128, 0, s, pdl, a);
   tr.after();
   return e;
 }
@@ -380,8 +383,8 @@ cudaError_t launch_merge(const ChunkArgs& a, int ctas, int y, cudaStream_t s, bo
   // merge took 12 us). Few rows behind a long context have one unit in up to 19
   // parts: ten at once, two round trips (17 rows behind 32768 keys, batches of
   // 6 / 8 / 10: 32.6 / 33.1 / 32.5 us; 16 leave too few warps, 35.6).
-  return y == kChunkRows / 8 ? launch_plain(chunk_merge_kernel<__nv_bfloat16, DH, 2>, dim3(ctas, y), 128, 0, s, pdl, a)
-                             : launch_plain(chunk_merge_kernel<__nv_bfloat16, DH, 10>, dim3(ctas, y), 128, 0, s, pdl, a);
+  return y == kChunkRows / 8 ? launch_plain(chunk_merge_kernel<__nv_bfloat16, DH, 2, kChunkRows>, dim3(ctas, y), 128, 0, s, pdl, a)
+                             : launch_plain(chunk_merge_kernel<__nv_bfloat16, DH, 10, kChunkRows>, dim3(ctas, y), 128, 0, s, pdl, a);
 }
 
 }  // namespace

@@ -152,7 +152,7 @@ dflash_status dflash_kv_append_paged(const dflash_heads* h, dflash_dtype in_dtyp
 size_t dflash_attention_chunk_bytes(const dflash_heads* h) {
   if (dflash_check_heads(h) != DFLASH_OK) return 0;
   return kChunkSlots * chunk_slot_floats(h->head_dim) * sizeof(float) +
-         static_cast<size_t>(kChunkMaxCtas) * kChunkDescInts * sizeof(int32_t);
+         static_cast<size_t>(kChunkDescs) * kChunkDescInts * sizeof(int32_t);
 }
 
 dflash_status dflash_attention_chunk_paged(const dflash_heads* h, const void* q, long long ld_q,

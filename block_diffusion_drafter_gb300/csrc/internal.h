@@ -287,6 +287,7 @@ struct ChunkArgs {
 constexpr int kChunkRows = 256;
 constexpr int kChunkMaxCtas = 160;
 constexpr int kChunkSlots = 2 * kChunkMaxCtas;
+constexpr int kChunkDescs = 1024;   // merge descriptors: one a CTA (bf16), one a unit (fp32)
 constexpr int kChunkDescInts = 8;
 __host__ __device__ constexpr size_t chunk_slot_floats(int head_dim) {
   return static_cast<size_t>(kChunkRows) * (head_dim + 2);

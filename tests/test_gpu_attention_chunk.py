@@ -142,6 +142,16 @@ def test_fp32_chunks_of_many_rows(dfl, causal, hq, hkv, ns, ctxs):
     s.check(causal=causal, rows=12)
 
 
+@pytest.mark.parametrize("B,hq,hkv", [(47, 8, 2), (300, 4, 4)])
+def test_fp32_units_of_many_sequences_in_parts(dfl, B, hq, hkv):
+    """More split units than CTAs, and more units than can be split."""
+    ns = [9 + (5 * i) % 9 for i in range(B)]
+    ctxs = [640 + (37 * i) % 90 if B < 100 else (91 * i) % 300 for i in range(B)]
+    s = Scene(dfl, F32, hq, hkv, 64, ns, ctxs, seed=31)
+    s.run()
+    s.check(rows=3)
+
+
 @pytest.mark.parametrize("shape", ["qwen", "f32_64"])
 def test_hints_do_not_change_what_is_computed(dfl, shape):
     """Any hint is allowed: too small ones, too large ones."""
