@@ -474,11 +474,13 @@ def _here(stream, fn: str, *tensors):
     """The stream's handle, once every operand is known to lie on the current
     device (a kernel that met another's or the host's memory would fault)."""
     handle = _stream(stream)
-    if _cuda or (_cuda is None and torch.cuda.is_available()):
+    if _cuda is None:   # a stream was given: not asked yet
+        _stream(None)
+    if _cuda:
         device = torch._C._cuda_getDevice()
-        for t in tensors:
-            if t is not None and t.get_device() != device:
-                raise DFlashError(fn, ERR_INVALID_ARG)
+        at = [t.get_device() for t in tensors if t is not None]
+        if at.count(device) != len(at):
+            raise DFlashError(fn, ERR_INVALID_ARG)
     return handle
 
 
@@ -487,13 +489,18 @@ def _rows(t, n_heads: int, head_dim: int, dtype, fn: str):
     if t is None:
         return None, 0, 0
     rows, heads, dh = t.shape
-    ld, hs, es = t.stride()
-    if heads != n_heads or dh != head_dim or (hs != head_dim and heads > 1) or es != 1:
+    ld = heads * dh
+    whole = t.is_contiguous()
+    if not whole:
+        ld, hs, es = t.stride()
+        whole = es == 1 and (hs == dh or heads == 1)
+        if rows <= 1:   # the stride of a single row says nothing
+            ld = max(ld, heads * dh)
+    if heads != n_heads or dh != head_dim or not whole:
         raise DFlashError(fn, ERR_SHAPE)
     if _DTYPES.get(t.dtype) != dtype:
         raise DFlashError(fn, ERR_DTYPE)
-    # the stride of a single row says nothing
-    return t.data_ptr(), ld if rows > 1 else max(ld, n_heads * head_dim), rows
+    return t.data_ptr(), ld, rows
 
 
 def _ints(t, n: int, fn: str):
@@ -520,7 +527,7 @@ def _tables(c, s, heads: Heads, fn: str):
     if c is None or s is None:
         return _ptr(c), _ptr(s), 0
     n, half = c.shape
-    if c.shape != s.shape or 2 * half != heads.head_dim or not c.is_contiguous() or not s.is_contiguous():
+    if s.numel() != n * half or 2 * half != heads.head_dim or not c.is_contiguous() or not s.is_contiguous():
         raise DFlashError(fn, ERR_SHAPE)
     if c.dtype is not torch.float32 or s.dtype is not torch.float32:
         raise DFlashError(fn, ERR_DTYPE)
