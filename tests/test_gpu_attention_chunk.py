@@ -249,6 +249,25 @@ def test_the_same_bits_every_time_and_from_a_graph(dfl):
     s.check(rows=6)
 
 
+@pytest.mark.parametrize("shape,ns,ctxs", [("qwen", [17, 64, 1, 0], [200, 60, 0, 9]), ("qwen", [300], [90]),
+                                           ("f32_128", [64, 17, 3], [900, 0, 333]), ("f32_64", [1, 1], [1900, 7])])
+def test_whole_units_and_fp32_give_the_same_bits_from_a_graph(dfl, shape, ns, ctxs):
+    """Whatever the workspace holds, in one launch or two."""
+    s = Scene(dfl, *SHAPES[shape], ns, ctxs, seed=37)
+    s.run()
+    s.check(rows=6)
+    want = s.obuf.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.run()
+    for fill in (255, 0):
+        s.out[:s.T].zero_()
+        s.ws.buf.fill_(fill)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(s.obuf, want)
+
+
 def test_two_calls_at_once_on_their_own_workspaces(dfl):
     a = Scene(dfl, *SHAPES["qwen"], [17], [8000], seed=31)
     b = Scene(dfl, *SHAPES["qwen"], [200, 1], [500, 7000], seed=32)
