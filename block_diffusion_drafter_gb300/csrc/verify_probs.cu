@@ -259,8 +259,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) verify_probs_kernel(c
       const int x = draft[lane];
       const float u = p.u_accept[static_cast<size_t>(b) * p.gamma + lane];
       if (x >= 0 && x < V) {   // not a token: rejected
-        const float pj = prob_at(target + static_cast<size_t>(lane) * V + x);
-        const float qj = drafter == nullptr ? 1.f : __ldg(drafter + static_cast<size_t>(lane) * V + x);
+        // saturated as the draw's weights are: NaN and negative entries are 0, larger ones 1
+        const float pj = __saturatef(prob_at(target + static_cast<size_t>(lane) * V + x));
+        const float qj = drafter == nullptr ? 1.f : __saturatef(__ldg(drafter + static_cast<size_t>(lane) * V + x));
         keep = static_cast<double>(u) * static_cast<double>(qj) < static_cast<double>(pj);
       }
     }

@@ -46,11 +46,15 @@ def chunk_attention(q, k, v, ctx: int, causal: bool = True, scale: float = 0.0):
     return out, mass, big
 
 
+def probability(p) -> np.ndarray:
+    """Entries as probabilities: NaN and negative ones are 0, larger ones 1."""
+    x = f64(p)
+    return np.where(np.isnan(x), 0.0, np.clip(x, 0.0, 1.0))
+
+
 def fixed62(p) -> np.ndarray:
     """Probabilities as whole multiples of 2^-62 (uint64), truncated."""
-    x = f64(p)
-    x = np.where(np.isnan(x), 0.0, np.clip(x, 0.0, 1.0))
-    return np.floor(x * 2.0 ** 62).astype(np.uint64)
+    return np.floor(probability(p) * 2.0 ** 62).astype(np.uint64)
 
 
 def first_above(w: np.ndarray, u: float) -> int:
@@ -64,8 +68,8 @@ def verify_probs(p, q, draft, u_accept, u_draw):
     """One sequence: p [gamma+1, V], q [gamma, V] or None (drafts taken without
     a draw), draft [gamma], u_accept [gamma], u_draw. Returns (tau, committed
     [gamma+1] padded with -1, next_anchor)."""
-    p = f64(p)
-    q = None if q is None else f64(q)
+    p = probability(p)
+    q = None if q is None else probability(q)
     gamma, V = len(draft), p.shape[-1]
     a = 0
     while a < gamma:

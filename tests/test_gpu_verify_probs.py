@@ -246,3 +246,27 @@ def test_same_answer_every_time_on_a_stream_and_from_a_graph(dfl):
     graph.replay()
     torch.cuda.synchronize()
     check((tau.cpu().numpy(), com.cpu().numpy(), nxt.cpu().numpy(), 0), p.cpu(), q.cpu(), draft.cpu(), ua.cpu(), ud.cpu())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("at", [0, 3])
+def test_acceptance_clamps_entries_to_probabilities(dfl, dtype, at):
+    """The drafted token itself lies on a NaN, negative, infinite or larger entry of q, of p or of both, first or behind kept ones."""
+    from tests.test_oracle_target import ODD_ENTRIES
+    B, V, gamma = len(ODD_ENTRIES), 517, at + 2
+    p, q = torch.zeros((B, gamma + 1, V)), torch.full((B, gamma, V), 2.0 ** -12)
+    p[:, :, 300] = 1.0                                        # the drafts beside the odd one are kept
+    p[:, at, 300], p[:, at, 5] = 0.0, 0.3125
+    draft = torch.full((B, gamma), 300, dtype=torch.int32)
+    draft[:, at] = 500
+    ua = torch.full((B, gamma), 0.5)
+    for b, (u, qx, px, _) in enumerate(ODD_ENTRIES):
+        ua[b, at], q[b, at, 500], p[b, at, 500] = u, qx, px
+    x = (p.to(dtype), q, draft, ua, torch.linspace(0, 0.99, B))
+    got = run(dfl, *x)
+    assert got[0].tolist() == [gamma + 1 if kept else at + 1 for _, _, _, kept in ODD_ENTRIES]
+    assert got[3] == 0
+    check(got, *x)
+    got = run(dfl, x[0], None, *x[2:])
+    assert got[0].tolist() == [gamma + 1 if u < min(px, 1.0) else at + 1 for u, _, px, _ in ODD_ENTRIES]
+    check(got, x[0], None, *x[2:])

@@ -89,3 +89,22 @@ def test_verification_corner_cases():
     t, com, y = tr.verify_probs(same, same[:1], [3], [1.0], 0.6)                 # p == q: drawn from p
     assert (t, com.tolist(), y) == (1, [2, -1], 2)
     assert tr.verify_probs(np.zeros((2, 4)), None, [0], [0.1], 0.3)[2] == 0      # no mass at all
+
+
+# Entries that are no probabilities, (u, q_j(x_j), p_j(x_j), kept): NaN and negative ones count as 0, larger ones as 1.
+ODD_ENTRIES = [(0.6, 2.0, 1.0, True), (0.6, float("nan"), 0.25, True), (0.6, -0.5, 0.0, False), (0.3, -2.0, -0.5, False),
+               (0.0, float("inf"), 0.25, True), (0.5, float("inf"), 0.75, True), (0.5, float("inf"), 0.25, False),
+               (0.0, float("nan"), 0.0, False), (0.9, 0.5, float("nan"), False), (0.9, 0.5, -1.0, False), (0.9, 1.0, 2.0, True),
+               (0.9, 1.0, float("inf"), True), (0.5, float("-inf"), float("nan"), False), (0.5, 0.5, 0.75, True)]
+
+
+@pytest.mark.parametrize("u,q,p,kept", ODD_ENTRIES)
+def test_acceptance_clamps_entries_to_probabilities(u, q, p, kept):
+    P, Q = np.zeros((2, 12)), np.zeros((1, 12))
+    P[0, 5], P[1, 9] = 0.3, 1.0
+    P[0, 3], Q[0, 3] = p, q
+    t, com, _ = tr.verify_probs(P, Q, [3], [u], 0.25)
+    assert t == (2 if kept else 1) and (com[0] == 3) >= kept
+    # a drafter that draws nothing: q is one
+    t, _, _ = tr.verify_probs(P, None, [3], [u], 0.25)
+    assert t == (2 if not np.isnan(p) and u < min(p, 1.0) else 1)
