@@ -369,9 +369,11 @@ cudaError_t launch_f32(const ChunkArgs& a, cudaStream_t s, bool pdl, Tracer& tr,
   // 128 rows a unit read the shared tiles half as often for their products (2 x 64
   // rows of 28 heads behind 9000 keys 609 -> 529 us), where that leaves CTAs enough.
   const SimtPlan flat = plan_simt<DH, 4>(a);
-  if (DH == 128 && rows > 64) {
-    const SimtPlan tall = plan_simt<DH, 8>(a);
-    if (tall.cost < flat.cost) return launch_simt<DH, 8>(a, tall, s, pdl, tr, bytes, flops);
+  if constexpr (DH == 128) {
+    if (rows > 64) {
+      const SimtPlan tall = plan_simt<DH, 8>(a);
+      if (tall.cost < flat.cost) return launch_simt<DH, 8>(a, tall, s, pdl, tr, bytes, flops);
+    }
   }
   return launch_simt<DH, 4>(a, flat, s, pdl, tr, bytes, flops);
 }

@@ -381,3 +381,13 @@ def test_tracing_records_the_kernel_and_its_merge(dfl):
     T = s.q.shape[0]      # the rows that the call got: two lie behind the sequence
     assert got[0][1] == 2.0 * (900 + T) * 8 * 128 * 2 + 2.0 * T * 32 * 128 * 2 and got[1][1] == 0.0
     assert all(ms >= 0 for _, _, _, ms in got)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("hq,hkv", [(16, 2), (64, 1), (3, 3)])
+@pytest.mark.parametrize("ns,ctxs", [([200], [900]), ([70, 1, 129], [0, 500, 60])])
+def test_fp32_chunks_of_many_rows_of_64(dfl, causal, hq, hkv, ns, ctxs):
+    """Heads of 64 keep units of 64 rows, in one part and in several."""
+    s = Scene(dfl, F32, hq, hkv, 64, ns, ctxs, seed=53)
+    s.run(causal=causal)
+    s.check(causal=causal, rows=12)
