@@ -391,3 +391,30 @@ def test_fp32_chunks_of_many_rows_of_64(dfl, causal, hq, hkv, ns, ctxs):
     s = Scene(dfl, F32, hq, hkv, 64, ns, ctxs, seed=53)
     s.run(causal=causal)
     s.check(causal=causal, rows=12)
+
+
+@pytest.mark.parametrize("shape", ["qwen", "g5_64", "f32_64", "f32_128"])
+@pytest.mark.parametrize("cu,right", [([0, 17, 1 << 30], [17, 4]),      # claims more rows than there are: cut at the last
+                                      ([-5, 17, 21], [17, 4]),          # begins before the first row
+                                      ([0, 30, 10], [17, 0]),           # not ascending: sequence 0 takes all rows
+                                      ([40, 50, 60], [0, 0])])          # behind the last row: nothing to do
+def test_rows_of_offsets_that_disagree_are_right_and_none_is_written_behind_them(dfl, shape, cu, right):
+    """q ends with its last row and rows of other use lie behind the output's."""
+    s = Scene(dfl, *SHAPES[shape], [17, 4], [100, 50], seed=55, garbage=0.5, extra=40)
+    s.cu.copy_(torch.tensor(cu, dtype=torch.int32))
+    s.q, s.out = s.q[:s.T], s.out[:s.T]
+    s.run()
+    torch.cuda.synchronize()
+    got = s.out.clone()
+    if right == [17, 4]:
+        s.check()
+    elif right == [17, 0]:       # rows 0..16 see the keys that they would; the four behind them see finite rows of the page
+        for i in range(17):
+            o, mass, _ = tr.chunk_attention(f64(s.q[i:i + 1]), f64(s.k[0])[:, :101 + i], f64(s.v[0])[:, :101 + i], 100 + i)
+            # as for the sequence beside a bad page
+            assert (np.abs(f64(got[i:i + 1]) - o) <= 2.0 ** -8 * (mass + np.abs(o)) + 2.0 ** -9 * mass).all(), i
+        assert torch.isfinite(got).all()
+    else:
+        assert (got == 9).all()
+    assert (s.obuf[s.T:] == 9).all() and (s.obuf[:, -1] == 9).all()
+    assert int(s.st) == 0

@@ -278,3 +278,19 @@ def test_replayed_graph_and_another_stream(dfl):
     torch.cuda.synchronize()
     assert int(s["st"]) == 0
     check_append(s, ns, [c + 3 for c in ctxs])
+
+
+@pytest.mark.parametrize("types", TYPES, ids=list(TYPES))
+@pytest.mark.parametrize("cu,ns", [([0, 6, 1 << 30], [6, 4]),       # claims more rows than there are: cut at the last
+                                   ([0, 30, 10], [10, 0]),          # not ascending: sequence 0 takes all rows
+                                   ([12, 14, 16], [0, 0])])         # behind the last row: nothing to do
+def test_rows_of_offsets_that_disagree_are_written_to_their_places_alone(dfl, types, cu, ns):
+    """The operands end with their last row; pages and the output's rows behind it keep what they hold."""
+    s = scene(dfl, types, 8, 2, 128, [6, 4], [10, 20], extra=40)
+    for part in ("q", "k", "v"):
+        s[part] = s[part][:10]
+    s["cu"] = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    run_append(dfl, s)
+    torch.cuda.synchronize()
+    assert int(s["st"]) == 0
+    check_append(s, ns, [10, 20])
