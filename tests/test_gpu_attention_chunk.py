@@ -418,3 +418,14 @@ def test_rows_of_offsets_that_disagree_are_right_and_none_is_written_behind_them
         assert (got == 9).all()
     assert (s.obuf[s.T:] == 9).all() and (s.obuf[:, -1] == 9).all()
     assert int(s.st) == 0
+
+
+@pytest.mark.parametrize("shape", ["qwen", "g7", "mha64", "f32_64", "f32_128"])
+@pytest.mark.parametrize("ns,ctxs", [([17, 3], [300, 40]), ([1], [0]), ([140], [5]), ([5], [9000])])
+def test_rows_behind_the_last_sequence_may_hold_anything(dfl, shape, ns, ctxs):
+    """A padded batch: infinities and NaN in the rows that share a tile with the last sequence's."""
+    s = Scene(dfl, *SHAPES[shape], ns, ctxs, seed=57, extra=130)
+    s.qbuf[s.T::2] = float("nan")
+    s.qbuf[s.T + 1::2] = float("inf")
+    s.run()
+    s.check(rows=6)
