@@ -402,7 +402,8 @@ cudaError_t launch_merge(const ChunkArgs& a, int ctas, int y, cudaStream_t s, bo
 // 300 rows behind 900 keys 21.0 / 27.4. With more units than CTAs some take two:
 // whole up to 3 pages, and 6 where the chunk fills a unit (4 x 300 rows behind 300
 // keys 29.2 / 24.5, 20 x 2 rows, 702 keys 22.4 / 26.4). Lengths far below the hints
-// cost at most the longest unit, so that has 8 pages at most.
+// cost at most the longest unit, so that has 8 pages at most. The figures are those
+// of 32 heads over 8 of 128; other layouts follow the same rule.
 bool keep_whole(const ChunkArgs& a) {
   const int G = a.n_q_heads / a.n_kv_heads, tok = kChunkRows / G, sms = num_sms_of_current_device();
   const long long rows = static_cast<long long>(a.max_rows) * G;

@@ -22,10 +22,13 @@
 // through distributed shared memory; the warp whose range holds the threshold
 // knows its groups' sums and reads one group once more (from L2) to find the
 // token. Bound by latency for few sequences (the drafts, their probabilities, the
-// rows, the cluster's join, the group once more: 7 us), for many by instructions
-// (20 an entry and its draft's probability) beside the rows' bytes: each further 64
-// sequences of 151936 entries take 16.6 us, 4.7 TB/s; the same kernel with one
-// integer operation a weight takes 19.6 instead of 22 us for 64.
+// rows, the cluster's join, the group once more: 7 us). For many by no single
+// thing: 64 sequences of 151936 entries take 22 us, of which the bytes are 11.6 us at
+// a copy's rate and the instructions (20 an entry and its draft's probability) 5 us
+// of issue. The chain at both ends is not covered by other CTAs (all are in the same
+// phase), and 512 CTAs do not divide over 152 SMs (some hold four, others three).
+// Each further 64 sequences take 16.6 us, 4.7 TB/s; the same kernel with one integer
+// operation a weight took 19.6 instead of 22 us.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -123,7 +126,8 @@ struct Chunk {
   // 1 under rounding towards zero cuts off (the bits of the sums count them), and
   // the multiples of 2^-62 in r likewise. Each step is exact, and the bits' offsets
   // cancel between p and q or are taken off. Added to s1, s2, s3 in units of 2^-23,
-  // 2^-46 and 2^-62, below 2^23 an entry. 20 instructions an entry where
+  // 2^-46 and 2^-62, at most 2^23 an entry (s1 of an entry of one; 248 rows of them
+  // fit an int). 20 instructions an entry where
   // fixed62 and minus take 30 (64 sequences: 26.6 -> 22.0 us).
   __device__ __forceinline__ void add(int v0, int lane, int out, int& s1, int& s2, int& s3) const {
     constexpr float kUp = 8388608.f;   // 2^23

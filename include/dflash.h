@@ -511,7 +511,8 @@ dflash_status dflash_check_heads(const dflash_heads* heads);
  * q_out, k_out: heads.dtype; may be q and k themselves (same types and
  *   strides). Partly overlapping operands are not allowed (outputs that begin
  *   where another operand does are refused, DFLASH_ERR_INVALID_ARG). T == 0
- *   launches nothing. Statistics are fp32; an output is rounded once. */
+ *   launches nothing. Statistics are fp32 (a normed head's squares have to sum
+ *   inside its range: values below 2^60); an output is rounded once. */
 dflash_status dflash_qk_norm_rope(const dflash_heads* heads, dflash_dtype in_dtype, const void* q,
                                   long long ld_q, const void* k, long long ld_k, const void* g_q,
                                   const void* g_k, const int32_t* positions, const float* rope_cos,
@@ -588,6 +589,8 @@ dflash_status dflash_attention_chunk_paged(const dflash_heads* heads, const void
  *   probabilities in [0, 1] (NaN and negative entries count as 0, larger ones
  *   as 1); a row need not sum to one.
  * u_accept: device fp32 [B, gamma], u_draw: device fp32 [B], uniforms in [0, 1).
+ * cfg: gamma, vocab and max_batch are used; the rest only has to pass
+ *   dflash_check_config.
  * gamma_b: NULL, or device [B] as in dflash_verify_accept_dyn.
  * A draft id outside [0, V) counts as rejected. A row a without any mass, and
  *   weights w that sum to 4 or more (no probabilities; less than V 2^-22 + 2^-16
