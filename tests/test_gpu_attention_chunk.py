@@ -429,3 +429,21 @@ def test_rows_behind_the_last_sequence_may_hold_anything(dfl, shape, ns, ctxs):
     s.qbuf[s.T + 1::2] = float("inf")
     s.run()
     s.check(rows=6)
+
+
+@pytest.mark.parametrize("shape", ["qwen", "g7", "mha64", "f32_128"])
+@pytest.mark.parametrize("ns,ctxs", [([17], [9000]), ([300, 1], [5000, 2000]), ([6, 200], [-3, -150]), ([1, 4], [-1, -9])])
+def test_whole_blocks_over_long_contexts_and_before_the_first_position(dfl, shape, ns, ctxs):
+    """Not causal: units split over the GPU, and chunks that begin at negative positions."""
+    s = Scene(dfl, *SHAPES[shape], ns, ctxs, seed=59)
+    s.run(causal=False)
+    s.check(causal=False, rows=6)
+
+
+@pytest.mark.parametrize("shape", ["qwen", "f32_64"])
+def test_a_table_without_a_place_left(dfl, shape):
+    """The last key is the last row of the last page that the table names."""
+    s = Scene(dfl, *SHAPES[shape], [17, 3], [495, 509], seed=61)
+    s.pages = dfl.KvPages(s.kp, s.vp, s.table[:, :4].contiguous().cuda())
+    s.run()
+    s.check()

@@ -294,3 +294,27 @@ def test_rows_of_offsets_that_disagree_are_written_to_their_places_alone(dfl, ty
     torch.cuda.synchronize()
     assert int(s["st"]) == 0
     check_append(s, ns, [10, 20])
+
+
+@pytest.mark.parametrize("types", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 17, 3000])
+def test_parts_of_one_projection_in_place(dfl, types, T):
+    """q and k inside the projection's own rows, a row's heads in one block or in several; the values beside them stay."""
+    ti, to = TYPES[types]
+    hq, hkv, dh = 10, 2, 128
+    g = torch.Generator().manual_seed(T)
+    heads = dfl.make_heads(1, hq, hkv, dh, rms_eps=EPS, dtype=out_code(dfl, to))
+    rows = randn(g, (T, (hq + 2 * hkv) * dh), ti, 2.0)
+    was = rows.clone()
+    part = lambda r, a, n: r[:, a * dh:(a + n) * dh].view(T, n, dh)  # noqa: E731
+    q, k = part(rows, 0, hq), part(rows, hq, hkv)
+    gq, gk = randn(g, (dh,), to, 0.1, 1.0), randn(g, (dh,), to, 0.1, 1.0)
+    pos = torch.randint(0, 4000, (T,), generator=g, dtype=torch.int32)
+    cos, sin = tables(dfl, dh, 4000)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dfl.dflash_qk_norm_rope(heads, q, k, pos.cuda(), cos, sin, q, k, st, g_q=gq, g_k=gk)
+    torch.cuda.synchronize()
+    assert int(st) == 0
+    assert_rows(q, part(was, 0, hq), gq, pos.numpy(), "q")
+    assert_rows(k, part(was, hq, hkv), gk, pos.numpy(), "k")
+    assert torch.equal(part(rows, hq + hkv, hkv), part(was, hq + hkv, hkv))
