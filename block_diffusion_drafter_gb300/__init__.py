@@ -5,8 +5,9 @@ kernels, reached through its C ABI (include/dflash.h). PyTorch provides the
 device memory and streams. Functions keep the C names:
 dflash_ctx_fuse, dflash_kv_inject, dflash_draft_block, dflash_verify_accept,
 the target-side dflash_qk_norm_rope, dflash_kv_append_paged,
-dflash_attention_chunk_paged and dflash_verify_probs, plus the sizing / helper
-calls of the header. There is no CPU fallback: if
+dflash_attention_chunk_paged and dflash_verify_probs, those around drafted trees
+(dflash_tree_masks, dflash_attention_tree_paged, dflash_sample,
+dflash_verify_tree, dflash_pages_*), plus the sizing / helper calls of the header. There is no CPU fallback: if
 the library is missing, loading raises.
 """
 from __future__ import annotations
@@ -22,7 +23,7 @@ from . import _build
 F32, BF16 = 0, 1
 (OK, ERR_INVALID_ARG, ERR_SHAPE, ERR_DTYPE, ERR_CAPACITY, ERR_ARCH, ERR_CUDA, ERR_TIMEOUT,
  ERR_WORKSPACE, ERR_ALIGN, ERR_TOO_LARGE) = 0, -1, -2, -3, -4, -5, -6, -7, -8, -9, -10
-K_GEMM, K_ATTN, K_NORM, K_ARGMAX, K_VERIFY = range(5)
+K_GEMM, K_ATTN, K_NORM, K_ARGMAX, K_VERIFY, K_PAGES = range(6)
 
 
 class DFlashError(RuntimeError):
@@ -141,6 +142,17 @@ _SIGS = {
                                           ctypes.POINTER(Trace), _P]),
     "dflash_verify_probs": (_I, [ctypes.POINTER(Config), _P, _I, _P, _P, _P, _P, _P, _I, _P, _P, _P, _P,
                                  ctypes.POINTER(Trace), _P]),
+    "dflash_tree_masks": (_I, [_P, _P, _P, _I, _I, _I, _P, _P, _P, ctypes.POINTER(Trace), _P]),
+    "dflash_attention_tree_paged": (_I, [ctypes.POINTER(Heads), _P, _LL, _P, _P, _I, _I, _I, _I, _I,
+                                         ctypes.POINTER(KvPages), _P, _I, ctypes.c_float, _P, _LL, _P, _P, _SZ,
+                                         ctypes.POINTER(Trace), _P]),
+    "dflash_sample": (_I, [_P, _I, _LL, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(Trace), _P]),
+    "dflash_verify_tree": (_I, [ctypes.POINTER(Heads), _P, _P, _P, _P, _P, _I, _I, _I, ctypes.POINTER(KvPages), _P, _P, _P,
+                                _P, _P, ctypes.POINTER(Trace), _P]),
+    "dflash_pages_release": (_I, [ctypes.POINTER(KvPages), _P, _P, _I, _P, ctypes.POINTER(Trace), _P]),
+    "dflash_pages_reserve": (_I, [ctypes.POINTER(KvPages), _P, _P, _I, _P, ctypes.POINTER(Trace), _P]),
+    "dflash_pages_fork": (_I, [ctypes.POINTER(Heads), ctypes.POINTER(KvPages), _P, _P, _I, _P, _P, _I, _P,
+                               ctypes.POINTER(Trace), _P]),
 }
 
 _lib = None
@@ -626,6 +638,135 @@ def dflash_verify_probs(cfg, target_probs, draft_probs, draft, u_accept, u_draw,
         _ints(tau, B, fn), _ints(committed, B * R, fn), _ints(next_anchor, B, fn), _status(dev_status, fn), _tr(trace),
         _here(stream, fn, target_probs, draft_probs, draft, u_accept, u_draw, gamma_b, tau, committed, next_anchor,
               dev_status)))
+
+
+# ---------------------------------------------------------------- drafted trees
+def dflash_tree_masks(parents, cu_rows, ctx_len, mask, dev_status, positions=None, trace=None, stream=None):
+    """Masks [T, words] (int32 bits) and positions [T] of a ragged batch of trees
+    given by every node's parent within its sequence (-1 for none)."""
+    fn = "dflash_tree_masks"
+    T, B = parents.numel(), cu_rows.numel() - 1
+    words = _mask_words(mask, T, fn)
+    _check(fn, load().dflash_tree_masks(
+        _ints(parents, T, fn), _ints(cu_rows, B + 1, fn), _ints(ctx_len, B, fn) if ctx_len is not None else None, B, T, words,
+        mask.data_ptr(), _ints(positions, T, fn) if positions is not None else None, _status(dev_status, fn), _tr(trace),
+        _here(stream, fn, parents, cu_rows, ctx_len, mask, positions, dev_status)))
+
+
+def _mask_words(mask, T: int, fn: str) -> int:
+    if mask.dtype is not torch.int32:
+        raise DFlashError(fn, ERR_DTYPE)
+    if mask.dim() != 2 or mask.shape[0] < T or not mask.is_contiguous():
+        raise DFlashError(fn, ERR_SHAPE)
+    return mask.shape[1]
+
+
+def dflash_attention_tree_paged(heads: Heads, q, cu_rows, ctx_len, max_rows, max_ctx_hint, layer, pages: KvPages, mask, out,
+                                dev_status, ws: ChunkWorkspace, scale=0.0, trace=None, stream=None):
+    """Attention of a ragged batch of trees q [T, Hq, Dh] over the paged cache that
+    already holds the nodes' own keys and values; mask [T, words] (int32 bits)."""
+    fn = "dflash_attention_tree_paged"
+    hq, dh, dt = heads.n_q_heads, heads.head_dim, heads.dtype
+    qp, ldq, T = _rows(q, hq, dh, dt, fn)
+    op, ldo, n_out = _rows(out, hq, dh, dt, fn)
+    if q is None or n_out < T:
+        raise DFlashError(fn, ERR_INVALID_ARG if q is None else ERR_SHAPE)
+    B, words = ctx_len.numel(), _mask_words(mask, T, fn)
+    _check(fn, load().dflash_attention_tree_paged(
+        ctypes.byref(heads), qp, ldq, _ints(cu_rows, B + 1, fn), _ints(ctx_len, B, fn), B, T, int(max_rows),
+        int(max_ctx_hint), int(layer), _view(pages, heads, ctx_len, fn), mask.data_ptr(), words, float(scale), op, ldo,
+        _status(dev_status, fn), ws.ptr, ws.nbytes, _tr(trace),
+        _here(stream, fn, q, out, cu_rows, ctx_len, mask, dev_status, getattr(ws, "buf", None))))
+
+
+def _floats(t, n: int, fn: str):
+    """Pointer of a device fp32 vector of at least n entries, None for none."""
+    if t is None:
+        return None
+    if t.dtype is not torch.float32 or t.numel() < n or not t.is_contiguous():
+        raise DFlashError(fn, ERR_SHAPE if t.dtype is torch.float32 else ERR_DTYPE)
+    return t.data_ptr()
+
+
+def dflash_sample(logits, u, tokens, dev_status, temperature=None, top_k=None, top_p=None, min_p=None, probs=None,
+                  trace=None, stream=None):
+    """Tokens [N] drawn from logits [N, V] by the uniforms u [N] after temperature,
+    top-k, top-p and min-p (each a tensor [N] or None), and / or the distributions
+    probs [N, V]; u and tokens None: the distributions alone."""
+    fn = "dflash_sample"
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise DFlashError(fn, ERR_SHAPE)
+    N, V = logits.shape
+    ld = max(logits.stride(0), V) if N <= 1 else logits.stride(0)   # the stride of a single row says nothing
+    if probs is not None and (probs.shape != (N, V) or not probs.is_contiguous()):
+        raise DFlashError(fn, ERR_SHAPE)
+    _check(fn, load().dflash_sample(
+        logits.data_ptr(), _DTYPES.get(logits.dtype, -1), ld, N, V, _floats(temperature, N, fn),
+        _ints(top_k, N, fn) if top_k is not None else None, _floats(top_p, N, fn), _floats(min_p, N, fn), _floats(u, N, fn),
+        _ints(tokens, N, fn) if tokens is not None else None, _floats(probs, N * V, fn), _status(dev_status, fn), _tr(trace),
+        _here(stream, fn, logits, u, tokens, temperature, top_k, top_p, min_p, probs, dev_status)))
+
+
+def dflash_verify_tree(tokens, parents, drawn, cu_rows, tau, committed, path, next_anchor, dev_status, heads=None, ctx_len=None,
+                       pages=None, trace=None, stream=None):
+    """The branch of each tree that the drawn tokens confirm; with heads, ctx_len
+    and pages its rows move behind the context in every layer. committed and path
+    are [B, max_path]."""
+    fn = "dflash_verify_tree"
+    T, B = tokens.numel(), cu_rows.numel() - 1
+    P = path.shape[-1]
+    if committed.shape[-1] != P:
+        raise DFlashError(fn, ERR_SHAPE)
+    view = None
+    if pages is not None:
+        if heads is None or ctx_len is None:
+            raise DFlashError(fn, ERR_INVALID_ARG)
+        if ctx_len.numel() < B:
+            raise DFlashError(fn, ERR_SHAPE)
+        view = _view(pages, heads, ctx_len, fn)
+    _check(fn, load().dflash_verify_tree(
+        ctypes.byref(heads) if heads is not None else None, _ints(tokens, T, fn), _ints(parents, T, fn), _ints(drawn, T, fn),
+        _ints(cu_rows, B + 1, fn), _ints(ctx_len, B, fn) if ctx_len is not None else None, B, T, P, view, _ints(tau, B, fn),
+        _ints(committed, B * P, fn), _ints(path, B * P, fn), _ints(next_anchor, B, fn), _status(dev_status, fn), _tr(trace),
+        _here(stream, fn, tokens, parents, drawn, cu_rows, ctx_len, tau, committed, path, next_anchor, dev_status)))
+
+
+def _book(pages: KvPages, refs, lens, n: int, fn: str):
+    """A page view whose table has n rows, and its counts, where the lengths lie."""
+    if pages.layout is None or pages.sequences < n:
+        raise DFlashError(fn, ERR_SHAPE)
+    if pages.device != lens.get_device():
+        raise DFlashError(fn, ERR_INVALID_ARG)
+    return ctypes.byref(pages), _ints(refs, pages.n_pages, fn)
+
+
+def dflash_pages_release(pages: KvPages, refs, keep_len, dev_status, trace=None, stream=None):
+    """Sequence b keeps the pages of its first keep_len[b] positions."""
+    fn = "dflash_pages_release"
+    B = keep_len.numel()
+    view, counts = _book(pages, refs, keep_len, B, fn)
+    _check(fn, load().dflash_pages_release(view, counts, _ints(keep_len, B, fn), B, _status(dev_status, fn), _tr(trace),
+                                           _here(stream, fn, refs, keep_len, dev_status)))
+
+
+def dflash_pages_reserve(pages: KvPages, refs, want_len, dev_status, trace=None, stream=None):
+    """Free pages for the missing entries of sequence b's first want_len[b] positions."""
+    fn = "dflash_pages_reserve"
+    B = want_len.numel()
+    view, counts = _book(pages, refs, want_len, B, fn)
+    _check(fn, load().dflash_pages_reserve(view, counts, _ints(want_len, B, fn), B, _status(dev_status, fn), _tr(trace),
+                                           _here(stream, fn, refs, want_len, dev_status)))
+
+
+def dflash_pages_fork(heads: Heads, pages: KvPages, refs, ctx_len, src, dst, dev_status, trace=None, stream=None):
+    """Sequence dst[i] becomes a copy of sequence src[i] (ctx_len and the table
+    have a row for every sequence)."""
+    fn = "dflash_pages_fork"
+    n, seqs = src.numel(), ctx_len.numel()
+    view = _view(pages, heads, ctx_len, fn)
+    _check(fn, load().dflash_pages_fork(
+        ctypes.byref(heads), view, _ints(refs, pages.n_pages, fn), _ints(ctx_len, seqs, fn), seqs, _ints(src, n, fn),
+        _ints(dst, n, fn), n, _status(dev_status, fn), _tr(trace), _here(stream, fn, refs, ctx_len, src, dst, dev_status)))
 
 
 class TraceRecorder:

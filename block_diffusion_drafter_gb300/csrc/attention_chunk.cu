@@ -38,7 +38,8 @@ constexpr size_t simt_smem() {
 template <int DH, int RT>
 constexpr int simt_ctas() { return RT == 1 || (DH == 64 && RT <= 4) ? 2 : 1; }
 
-template <int DH, int RT>
+// TREE: behind the context a row sees the keys of its mask (p.mask).
+template <int DH, int RT, bool TREE>
 __global__ void __launch_bounds__(kSimtThreads, (simt_ctas<DH, RT>())) chunk_simt_kernel(const ChunkArgs p, int splits) {
   extern __shared__ __align__(16) float sm[];
   constexpr int kSimtRows = 16 * RT;
@@ -81,11 +82,11 @@ __global__ void __launch_bounds__(kSimtThreads, (simt_ctas<DH, RT>())) chunk_sim
     *reinterpret_cast<float4*>(&sq[r * LD + d]) =
         r < rows ? *reinterpret_cast<const float4*>(&q[(u.row0 + u.tok0 + r / G) * p.ldq + (kvh * G + r % G) * DH + d]) : none;
   }
-  int lim[RT];     // keys that row RT ty + i sees
+  int lim[RT];     // keys that row RT ty + i sees; TREE: up to where its mask begins
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
     const int r = RT * ty + i;
-    lim[i] = r < rows ? row_keys(p, u, u.tok0 + r / G) : 0;
+    lim[i] = r >= rows ? 0 : TREE ? max(0, min(u.ctx, keys)) : row_keys(p, u, u.tok0 + r / G);
   }
   float m[RT], l[RT], o[RT][DC];
 #pragma unroll
@@ -140,9 +141,18 @@ __global__ void __launch_bounds__(kSimtThreads, (simt_ctas<DH, RT>())) chunk_sim
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       float mx = -INFINITY;
+      uint32_t on[4] = {0u, 0u, 0u, 0u};   // this thread's bit of the mask's windows
+      if (TREE && k0 + kSimtKeys > u.ctx && RT * ty + i < rows) {
+        const uint32_t* bits = p.mask + (static_cast<size_t>(u.row0) + u.tok0 + (RT * ty + i) / G) * p.mask_words;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int k = k0 + tx + 16 * j;
+          if (k >= u.ctx && k < keys && (k - u.ctx) >> 5 < p.mask_words) on[j] = __ldg(bits + ((k - u.ctx) >> 5)) >> ((k - u.ctx) & 31) & 1u;
+        }
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        s[i][j] = k0 + tx + 16 * j < lim[i] ? s[i][j] * scale : -INFINITY;
+        s[i][j] = k0 + tx + 16 * j < lim[i] || (TREE && on[j] != 0u) ? s[i][j] * scale : -INFINITY;
         mx = fmaxf(mx, s[i][j]);
       }
 #pragma unroll
@@ -332,7 +342,7 @@ SimtPlan plan_simt(const ChunkArgs& a) {
   return r;
 }
 
-template <int DH, int RT>
+template <int DH, int RT, bool TREE>
 cudaError_t launch_simt(const ChunkArgs& a, const SimtPlan& plan, cudaStream_t s, bool pdl, Tracer& tr, double bytes,
                         double flops) {
   constexpr int rows = 16 * RT;
@@ -343,13 +353,13 @@ cudaError_t launch_simt(const ChunkArgs& a, const SimtPlan& plan, cudaStream_t s
   int dev = 0;
   cudaGetDevice(&dev);
   if (!done[dev & 63]) {
-    const cudaError_t e = cudaFuncSetAttribute(chunk_simt_kernel<DH, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(chunk_simt_kernel<DH, RT, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     done[dev & 63] = true;
   }
   tr.before(DFLASH_K_ATTN, bytes, flops);
-  cudaError_t e = launch_plain(chunk_simt_kernel<DH, RT>,
+  cudaError_t e = launch_plain(chunk_simt_kernel<DH, RT, TREE>,
                                dim3(static_cast<unsigned>(units), a.n_kv_heads, splits), kSimtThreads, smem, s, pdl, a,
                                splits);
   tr.after();
@@ -360,22 +370,22 @@ cudaError_t launch_simt(const ChunkArgs& a, const SimtPlan& plan, cudaStream_t s
   return e;
 }
 
-template <int DH>
+template <int DH, bool TREE>
 cudaError_t launch_f32(const ChunkArgs& a, cudaStream_t s, bool pdl, Tracer& tr, double bytes, double flops) {
   const int G = a.n_q_heads / a.n_kv_heads;
   const long long rows = static_cast<long long>(a.max_rows) * G;
-  if (rows <= 16 && G <= 16) return launch_simt<DH, 1>(a, plan_simt<DH, 1>(a), s, pdl, tr, bytes, flops);
-  if (rows <= 32 && G <= 32) return launch_simt<DH, 2>(a, plan_simt<DH, 2>(a), s, pdl, tr, bytes, flops);
+  if (rows <= 16 && G <= 16) return launch_simt<DH, 1, TREE>(a, plan_simt<DH, 1>(a), s, pdl, tr, bytes, flops);
+  if (rows <= 32 && G <= 32) return launch_simt<DH, 2, TREE>(a, plan_simt<DH, 2>(a), s, pdl, tr, bytes, flops);
   // 128 rows a unit read the shared tiles half as often for their products (2 x 64
   // rows of 28 heads behind 9000 keys 609 -> 529 us), where that leaves CTAs enough.
   const SimtPlan flat = plan_simt<DH, 4>(a);
   if constexpr (DH == 128) {
     if (rows > 64) {
       const SimtPlan tall = plan_simt<DH, 8>(a);
-      if (tall.cost < flat.cost) return launch_simt<DH, 8>(a, tall, s, pdl, tr, bytes, flops);
+      if (tall.cost < flat.cost) return launch_simt<DH, 8, TREE>(a, tall, s, pdl, tr, bytes, flops);
     }
   }
-  return launch_simt<DH, 4>(a, flat, s, pdl, tr, bytes, flops);
+  return launch_simt<DH, 4, TREE>(a, flat, s, pdl, tr, bytes, flops);
 }
 
 template <int DH>
@@ -423,8 +433,10 @@ cudaError_t launch_attention_chunk(const ChunkArgs& args, int bf16, cudaStream_t
                                    double flops) {
   ChunkArgs a = args;
   if (a.head_dim != 64 && a.head_dim != 128) return cudaErrorInvalidValue;
+  if (!bf16 && a.mask != nullptr)
+    return a.head_dim == 128 ? launch_f32<128, true>(a, s, pdl, tr, bytes, flops) : launch_f32<64, true>(a, s, pdl, tr, bytes, flops);
   if (!bf16)
-    return a.head_dim == 128 ? launch_f32<128>(a, s, pdl, tr, bytes, flops) : launch_f32<64>(a, s, pdl, tr, bytes, flops);
+    return a.head_dim == 128 ? launch_f32<128, false>(a, s, pdl, tr, bytes, flops) : launch_f32<64, false>(a, s, pdl, tr, bytes, flops);
   int ctas = 0;
   a.whole_units = keep_whole(a);
   tr.before(DFLASH_K_ATTN, bytes, flops);

@@ -396,7 +396,8 @@ struct Walk {
   __device__ __forceinline__ int tile(int s, int k) const { return pair ? k : 2 * k + s; }
 };
 
-template <int DH>
+// TREE: behind the context a row sees the keys of its mask (p.mask).
+template <int DH, bool TREE>
 __global__ void __launch_bounds__(kTcThreads, 1)
     chunk_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                     const __grid_constant__ CUtensorMap v_map, const ChunkArgs p) {
@@ -702,7 +703,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int tok = (pair ? s * tile_tok : 0) + r_tok;   // token of the unit
       const bool valid = r_tok < tile_tok && tok < w.n_tok;
       const ChunkUnit u{w.b, w.row0, w.n, w.ctx, w.tok0};
-      const int lim = valid ? row_keys(p, u, w.tok0 + tok) : 0;
+      // keys that the row sees; TREE: up to where its mask begins
+      const int lim = !valid ? 0 : TREE ? max(0, min(w.ctx, p.pages.pages_per_seq * kPageKeys)) : row_keys(p, u, w.tok0 + tok);
       const bool live = __any_sync(0xffffffffu, valid) != 0;   // warp-uniform
       const int keys = max(0, min(w.ctx + w.n, p.pages.pages_per_seq * kPageKeys));   // rows of the cache that hold keys
       float m = -INFINITY, l = 0.f;
@@ -737,7 +739,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // one that any sees unread. (All columns read and written: six prompts of 500
             // to 2000 tokens 137 instead of 114 us.)
             const int all = __reduce_min_sync(0xffffffffu, valid ? max(seen, 0) : kKeys);
-            const int some = __reduce_max_sync(0xffffffffu, seen);
+            const int some = TREE ? keys - kb : __reduce_max_sync(0xffffffffu, seen);
+            const uint32_t* bits = nullptr;
+            if (TREE && valid) bits = p.mask + (static_cast<size_t>(w.row0) + w.tok0 + tok) * p.mask_words;
 #pragma unroll 1
             for (int c = all & ~15; c < kKeys; c += 16) {
               float v[16];
@@ -745,8 +749,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 tmem_ld16(t_s + c, v);
                 tmem_ld_wait();
               }
+              if (TREE) {
+                uint32_t on = 0u;
+                if (valid && c < some) {
+                  on = mask_window16(bits, p.mask_words, kb + c - w.ctx);
+                  if (some - c < 16) on &= (1u << (some - c)) - 1u;
+                }
 #pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] = c + i < seen ? v[i] : -INFINITY;
+                for (int i = 0; i < 16; ++i) v[i] = on >> i & 1u ? v[i] : -INFINITY;
+              } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = c + i < seen ? v[i] : -INFINITY;
+              }
               tmem_st16(t_s + c, v);
             }
             tmem_st_wait();
@@ -897,7 +911,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 }
 
-template <int DH>
+template <int DH, bool TREE>
 cudaError_t launch_tc(const ChunkArgs& a, const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, int ctas,
                       cudaStream_t s, bool pdl) {
   constexpr int smem = static_cast<int>((2 + kStages) * static_cast<size_t>(DH / 64) * kSubTile + sizeof(ChunkSmem));
@@ -906,7 +920,7 @@ cudaError_t launch_tc(const ChunkArgs& a, const CUtensorMap& qm, const CUtensorM
   int dev = 0;
   cudaGetDevice(&dev);
   if (!done[dev & 63]) {
-    const cudaError_t e = cudaFuncSetAttribute(chunk_tc_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(chunk_tc_kernel<DH, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     done[dev & 63] = true;
   }
@@ -920,7 +934,7 @@ cudaError_t launch_tc(const ChunkArgs& a, const CUtensorMap& qm, const CUtensorM
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = pdl ? attr : nullptr;
   cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, chunk_tc_kernel<DH>, qm, km, vm, a);
+  return cudaLaunchKernelEx(&cfg, chunk_tc_kernel<DH, TREE>, qm, km, vm, a);
 }
 
 }  // namespace
@@ -935,7 +949,9 @@ cudaError_t launch_chunk_tc(const ChunkArgs& a, int* ctas, cudaStream_t s, bool 
     return cudaErrorInvalidValue;
   const int sms = num_sms_of_current_device();
   *ctas = sms < kChunkMaxCtas ? sms : kChunkMaxCtas;
-  return a.head_dim == 128 ? launch_tc<128>(a, qm, km, vm, *ctas, s, pdl) : launch_tc<64>(a, qm, km, vm, *ctas, s, pdl);
+  if (a.mask != nullptr)
+    return a.head_dim == 128 ? launch_tc<128, true>(a, qm, km, vm, *ctas, s, pdl) : launch_tc<64, true>(a, qm, km, vm, *ctas, s, pdl);
+  return a.head_dim == 128 ? launch_tc<128, false>(a, qm, km, vm, *ctas, s, pdl) : launch_tc<64, false>(a, qm, km, vm, *ctas, s, pdl);
 }
 
 }  // namespace dfl

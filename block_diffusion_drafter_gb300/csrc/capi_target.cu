@@ -1,6 +1,6 @@
 // C ABI of the target-side operators: argument validation and launches of
-// dflash_qk_norm_rope, dflash_kv_append_paged, dflash_attention_chunk_paged
-// and dflash_verify_probs. Host code only.
+// dflash_qk_norm_rope, dflash_kv_append_paged, dflash_attention_chunk_paged,
+// dflash_attention_tree_paged and dflash_verify_probs. Host code only.
 #include <cmath>
 #include <stdint.h>
 
@@ -39,6 +39,58 @@ dflash_status rope_args(const float* c, const float* s, int n) {
   if (c == nullptr && s == nullptr) return DFLASH_OK;
   if (c == nullptr || s == nullptr || n < 1) return DFLASH_ERR_INVALID_ARG;
   return aligned16(c) && aligned16(s) ? DFLASH_OK : DFLASH_ERR_ALIGN;
+}
+
+// Attention of chunks over pages; mask: NULL, or each row's own mask over the
+// chunk's keys (causal is then 0).
+dflash_status attention_chunk(const dflash_heads* h, const void* q, long long ld_q, const int32_t* cu_rows,
+                              const int32_t* ctx_len, int B, int T, int max_rows, int max_ctx_hint, int layer,
+                              const dflash_kv_pages* pages, int causal, float scale, const uint32_t* mask,
+                              int mask_words, void* out, long long ld_o, int32_t* dev_status, void* ws,
+                              size_t ws_bytes, dflash_trace* trace, dflash_stream_t stream) {
+  dflash_status st = dflash_check_heads(h);
+  if (st != DFLASH_OK) return st;
+  if (T < 0 || B < 0 || max_rows < 0 || max_ctx_hint < 0 || layer < 0 || layer >= h->n_layers || !std::isfinite(scale) ||
+      scale < 0.f || (causal != 0 && causal != 1))
+    return DFLASH_ERR_INVALID_ARG;
+  if (T == 0 || B == 0) return DFLASH_OK;
+  if (cu_rows == nullptr || ctx_len == nullptr || dev_status == nullptr || !heads_pages_ok(pages) || !trace_ok(trace))
+    return DFLASH_ERR_INVALID_ARG;
+  const int es = heads_elem_bytes(h);
+  const long long wq = static_cast<long long>(h->n_q_heads) * h->head_dim;
+  if ((st = rows_ok(q, ld_q, wq, es)) != DFLASH_OK || (st = rows_ok(out, ld_o, wq, es)) != DFLASH_OK) return st;
+  if (!aligned16(pages->k_pool) || !aligned16(pages->v_pool) || !aligned16(ws)) return DFLASH_ERR_ALIGN;
+  // tensor-map coordinates are 32-bit
+  if (static_cast<double>(h->n_layers) * pages->n_pages * h->n_kv_heads > 2147483647.0 ||
+      static_cast<long long>(T) * (h->n_q_heads / h->n_kv_heads) > INT32_MAX / 2 || B > INT32_MAX / 256)
+    return DFLASH_ERR_TOO_LARGE;
+  if (ws == nullptr || ws_bytes < dflash_attention_chunk_bytes(h)) return DFLASH_ERR_WORKSPACE;
+  if (q == out) return DFLASH_ERR_INVALID_ARG;
+  if ((st = check_arch()) != DFLASH_OK) return st;
+  ChunkArgs a{};
+  a.q = q; a.out = out; a.ldq = ld_q; a.ldo = ld_o;
+  a.cu_rows = cu_rows; a.ctx_len = ctx_len;
+  a.mask = mask; a.mask_words = mask_words;
+  a.B = B; a.T = T; a.layer = layer; a.n_layers = h->n_layers; a.causal = causal;
+  // bounds that size the grid; no result depends on them
+  const int capacity = pages->pages_per_seq * DFLASH_PAGE_KEYS;
+  a.max_rows = max_rows < T ? max_rows : T;
+  a.max_ctx = max_ctx_hint < capacity ? max_ctx_hint : capacity;
+  a.n_q_heads = h->n_q_heads; a.n_kv_heads = h->n_kv_heads; a.head_dim = h->head_dim;
+  a.scale = scale > 0.f ? scale : 1.0f / sqrtf(static_cast<float>(h->head_dim));
+  a.k_pool = pages->k_pool; a.v_pool = pages->v_pool;
+  a.pages = PageView{pages->page_table, pages->n_pages, pages->pages_per_seq};
+  a.dev_status = dev_status;
+  a.partials = static_cast<float*>(ws);
+  a.desc = reinterpret_cast<int32_t*>(static_cast<float*>(ws) + kChunkSlots * chunk_slot_floats(h->head_dim));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  Tracer tr{trace, s};
+  // as if every sequence had max_ctx_hint context keys (the lengths are on the device)
+  const double keys = static_cast<double>(B) * a.max_ctx + T;
+  const double bytes = 2.0 * keys * h->n_kv_heads * h->head_dim * es + 2.0 * T * static_cast<double>(wq) * es;
+  const double flops = 4.0 * T * static_cast<double>(wq) * (a.max_ctx + (causal ? 0.5 : 1.0) * a.max_rows);
+  const cudaError_t e = launch_attention_chunk(a, h->dtype == DFLASH_BF16, s, use_pdl(), tr, bytes, flops);
+  return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
 }
 
 }  // namespace
@@ -160,48 +212,18 @@ dflash_status dflash_attention_chunk_paged(const dflash_heads* h, const void* q,
                                            int max_ctx_hint, int layer, const dflash_kv_pages* pages, int causal,
                                            float scale, void* out, long long ld_o, int32_t* dev_status, void* ws,
                                            size_t ws_bytes, dflash_trace* trace, dflash_stream_t stream) {
-  dflash_status st = dflash_check_heads(h);
-  if (st != DFLASH_OK) return st;
-  if (T < 0 || B < 0 || max_rows < 0 || max_ctx_hint < 0 || layer < 0 || layer >= h->n_layers || !std::isfinite(scale) ||
-      scale < 0.f || (causal != 0 && causal != 1))
-    return DFLASH_ERR_INVALID_ARG;
-  if (T == 0 || B == 0) return DFLASH_OK;
-  if (cu_rows == nullptr || ctx_len == nullptr || dev_status == nullptr || !heads_pages_ok(pages) || !trace_ok(trace))
-    return DFLASH_ERR_INVALID_ARG;
-  const int es = heads_elem_bytes(h);
-  const long long wq = static_cast<long long>(h->n_q_heads) * h->head_dim;
-  if ((st = rows_ok(q, ld_q, wq, es)) != DFLASH_OK || (st = rows_ok(out, ld_o, wq, es)) != DFLASH_OK) return st;
-  if (!aligned16(pages->k_pool) || !aligned16(pages->v_pool) || !aligned16(ws)) return DFLASH_ERR_ALIGN;
-  // tensor-map coordinates are 32-bit
-  if (static_cast<double>(h->n_layers) * pages->n_pages * h->n_kv_heads > 2147483647.0 ||
-      static_cast<long long>(T) * (h->n_q_heads / h->n_kv_heads) > INT32_MAX / 2 || B > INT32_MAX / 256)
-    return DFLASH_ERR_TOO_LARGE;
-  if (ws == nullptr || ws_bytes < dflash_attention_chunk_bytes(h)) return DFLASH_ERR_WORKSPACE;
-  if (q == out) return DFLASH_ERR_INVALID_ARG;
-  if ((st = check_arch()) != DFLASH_OK) return st;
-  ChunkArgs a{};
-  a.q = q; a.out = out; a.ldq = ld_q; a.ldo = ld_o;
-  a.cu_rows = cu_rows; a.ctx_len = ctx_len;
-  a.B = B; a.T = T; a.layer = layer; a.n_layers = h->n_layers; a.causal = causal;
-  // bounds that size the grid; no result depends on them
-  const int capacity = pages->pages_per_seq * DFLASH_PAGE_KEYS;
-  a.max_rows = max_rows < T ? max_rows : T;
-  a.max_ctx = max_ctx_hint < capacity ? max_ctx_hint : capacity;
-  a.n_q_heads = h->n_q_heads; a.n_kv_heads = h->n_kv_heads; a.head_dim = h->head_dim;
-  a.scale = scale > 0.f ? scale : 1.0f / sqrtf(static_cast<float>(h->head_dim));
-  a.k_pool = pages->k_pool; a.v_pool = pages->v_pool;
-  a.pages = PageView{pages->page_table, pages->n_pages, pages->pages_per_seq};
-  a.dev_status = dev_status;
-  a.partials = static_cast<float*>(ws);
-  a.desc = reinterpret_cast<int32_t*>(static_cast<float*>(ws) + kChunkSlots * chunk_slot_floats(h->head_dim));
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  Tracer tr{trace, s};
-  // as if every sequence had max_ctx_hint context keys (the lengths are on the device)
-  const double keys = static_cast<double>(B) * a.max_ctx + T;
-  const double bytes = 2.0 * keys * h->n_kv_heads * h->head_dim * es + 2.0 * T * static_cast<double>(wq) * es;
-  const double flops = 4.0 * T * static_cast<double>(wq) * (a.max_ctx + (causal ? 0.5 : 1.0) * a.max_rows);
-  const cudaError_t e = launch_attention_chunk(a, h->dtype == DFLASH_BF16, s, use_pdl(), tr, bytes, flops);
-  return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
+  return attention_chunk(h, q, ld_q, cu_rows, ctx_len, B, T, max_rows, max_ctx_hint, layer, pages, causal, scale,
+                         nullptr, 0, out, ld_o, dev_status, ws, ws_bytes, trace, stream);
+}
+
+dflash_status dflash_attention_tree_paged(const dflash_heads* h, const void* q, long long ld_q, const int32_t* cu_rows,
+                                          const int32_t* ctx_len, int B, int T, int max_rows, int max_ctx_hint,
+                                          int layer, const dflash_kv_pages* pages, const uint32_t* mask,
+                                          int mask_words, float scale, void* out, long long ld_o, int32_t* dev_status,
+                                          void* ws, size_t ws_bytes, dflash_trace* trace, dflash_stream_t stream) {
+  if (mask_words < 1 || (mask == nullptr && T > 0 && B > 0)) return DFLASH_ERR_INVALID_ARG;
+  return attention_chunk(h, q, ld_q, cu_rows, ctx_len, B, T, max_rows, max_ctx_hint, layer, pages, 0, scale, mask,
+                         mask_words, out, ld_o, dev_status, ws, ws_bytes, trace, stream);
 }
 
 dflash_status dflash_verify_probs(const dflash_config* c, const void* target_probs, dflash_dtype probs_dtype,

@@ -71,6 +71,16 @@ __device__ __forceinline__ bool find_unit(const ChunkArgs& p, int tok, int i, in
   return false;
 }
 
+// Bits off .. off + 15 of a row's mask over the chunk's keys: word off / 32 on,
+// nothing behind the last word, and ones below bit 0 (the context, which all see).
+__device__ __forceinline__ uint32_t mask_window16(const uint32_t* row, int words, int off) {
+  const int at = max(off, 0) >> 5;
+  const uint32_t lo = at < words ? __ldg(row + at) : 0u;
+  if (off < 0) return off <= -16 ? 0xFFFFu : (lo << -off | ((1u << -off) - 1u)) & 0xFFFFu;
+  const uint32_t hi = at + 1 < words ? __ldg(row + at + 1) : 0u;
+  return __funnelshift_r(lo, hi, off & 31) & 0xFFFFu;
+}
+
 // Reports a sequence whose keys do not fit its page table (they are cut there).
 __device__ __forceinline__ void check_capacity(const ChunkArgs& p, const ChunkUnit& u) {
   if (static_cast<long long>(u.ctx) + u.n > static_cast<long long>(p.pages.pages_per_seq) * kPageKeys)

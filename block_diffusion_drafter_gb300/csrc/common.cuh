@@ -308,6 +308,25 @@ __device__ __forceinline__ uint32_t argmax_key_index(unsigned long long k) {
   return 0xFFFFFFFFu - static_cast<uint32_t>(k & 0xFFFFFFFFull);
 }
 
+// ----------------------------------------------------------------- draws
+// floor(u * total), u clamped to [0, 1 - 2^-24]; `whole`: whether nothing was cut off.
+__device__ __forceinline__ unsigned long long draw_threshold(float u, unsigned long long total, bool& whole) {
+  const uint32_t b = __float_as_uint(fminf(fmaxf(u, 0.f), 0.99999994f));
+  const int e = static_cast<int>(b >> 23);   // 0 .. 126
+  whole = b == 0u || total == 0ull;
+  if (e == 0) return 0ull;                   // below 2^-126
+  const unsigned long long m = (b & 0x7FFFFFu) | 0x800000u;   // u = m * 2^(e - 150)
+  const unsigned long long hi = __umul64hi(total, m), lo = total * m;
+  const int sh = 150 - e;                    // 24 .. 149
+  if (sh >= 128) return 0ull;
+  if (sh >= 64) {
+    whole = lo == 0ull && (sh == 64 || hi << (128 - sh) == 0ull);
+    return hi >> (sh - 64);
+  }
+  whole = lo << (64 - sh) == 0ull;
+  return (hi << (64 - sh)) | (lo >> sh);     // hi < 2^24: the quotient fits
+}
+
 // ----------------------------------------------------------------- sampling RNG
 // Counter-based splitmix64 (Steele, Lea and Flood 2014; Vigna's splitmix64.c):
 // the (c+1)-th output of the generator started at state `seed`. A draw's

@@ -272,6 +272,8 @@ struct ChunkArgs {
   void* out;
   long long ldq, ldo;
   const int32_t *cu_rows, *ctx_len;
+  const uint32_t* mask;      // NULL, or [T, mask_words]: a row's own mask over the chunk's keys
+  int mask_words;
   int B, T, max_rows, max_ctx, layer, n_layers, causal;
   int whole_units;           // bf16: units are not split (no merge follows)
   int n_q_heads, n_kv_heads, head_dim;
@@ -315,6 +317,66 @@ struct ProbsArgs {
   int* dev_status;
 };
 cudaError_t launch_verify_probs(const ProbsArgs& a, cudaStream_t s, bool pdl);
+
+// ---------------------------------------------------------------- drafted trees
+// Masks and positions of trees given by their nodes' parents (tree.cu).
+struct MaskArgs {
+  const int32_t *parents, *cu_rows, *ctx_len;   // ctx_len: NULL without positions
+  int B, T, words;
+  uint32_t* mask;            // [T, words]
+  int32_t* positions;        // NULL or [T]
+  int* dev_status;
+};
+cudaError_t launch_tree_masks(const MaskArgs& a, cudaStream_t s, bool pdl);
+
+// The confirmed branch of each tree, and its rows of the cache (tree.cu).
+struct TreeArgs {
+  const int32_t *tokens, *parents, *drawn, *cu_rows, *ctx_len;
+  int B, T, max_path;
+  int32_t *tau, *committed, *path, *next_anchor;
+  int* dev_status;
+  void *k_pool, *v_pool;     // NULL: nothing moves
+  PageView pages;
+  int n_layers, n_kv_heads, row_bytes;   // bytes of one head's row
+};
+cudaError_t launch_verify_tree(const TreeArgs& a, cudaStream_t s, bool pdl);
+
+// Rows of logits to tokens and shaped distributions (sample_logits.cu).
+struct DrawArgs {
+  const void* logits;        // [N, V], rows ld elements apart
+  long long ld;
+  int bf16, N, V;
+  const float* temperature;  // each NULL or [N]
+  const int32_t* top_k;
+  const float *top_p, *min_p, *u;
+  int32_t* tokens;           // NULL or [N]
+  float* probs;              // NULL or [N, V]
+  int* dev_status;
+};
+constexpr int kDrawMaxVocab = 1 << 19;
+cudaError_t launch_sample_logits(const DrawArgs& a, cudaStream_t s, bool pdl);
+
+// Who holds which page (pages.cu).
+struct PagesArgs {
+  int32_t* table;            // [seqs, pages_per_seq]
+  int32_t* refs;             // [n_pages]
+  int n_pages, pages_per_seq;
+  const int32_t* len;        // release: kept positions; reserve: wanted ones
+  int B;
+  // fork
+  int32_t* ctx_len;
+  const int32_t *src, *dst;
+  int n, seqs;
+  void *k_pool, *v_pool;
+  int n_layers, n_kv_heads, row_bytes;
+  int* dev_status;
+};
+constexpr int kMaxReserve = 4096;   // sequences of one call
+constexpr int kMaxForks = 1024;     // pairs of one call
+cudaError_t launch_pages_release(const PagesArgs& a, cudaStream_t s, bool pdl);
+cudaError_t launch_pages_reserve(const PagesArgs& a, cudaStream_t s, bool pdl);
+cudaError_t launch_pages_fork(const PagesArgs& a, cudaStream_t s, bool pdl);
+cudaError_t launch_pages_copy(const PagesArgs& a, cudaStream_t s, bool pdl);   // the rows of launch_pages_fork
 
 // Records trace events around one launch.
 struct Tracer {

@@ -71,18 +71,6 @@ __device__ __forceinline__ Fixed minus(Fixed a, Fixed b) {
       : "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi));
   return d;
 }
-// floor(u * total), u clamped to [0, 1 - 2^-24].
-__device__ __forceinline__ unsigned long long threshold(float u, unsigned long long total) {
-  const uint32_t b = __float_as_uint(fminf(fmaxf(u, 0.f), 0.99999994f));
-  const int e = static_cast<int>(b >> 23);   // 0 .. 126
-  if (e == 0) return 0ull;                   // below 2^-126
-  const unsigned long long m = (b & 0x7FFFFFu) | 0x800000u;   // u = m * 2^(e - 150)
-  const unsigned long long hi = __umul64hi(total, m), lo = total * m;
-  const int sh = 150 - e;                    // 24 .. 149
-  if (sh >= 128) return 0ull;
-  if (sh >= 64) return hi >> (sh - 64);
-  return (hi << (64 - sh)) | (lo >> sh);     // hi < 2^24: the quotient fits
-}
 __device__ __forceinline__ float prob_at(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float prob_at(const __nv_bfloat16* p) { return __bfloat162float(__ldg(p)); }
 
@@ -315,7 +303,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) verify_probs_kernel(c
     join(1);
   }
   cluster_arrive();      // this CTA's reads of its peers are done
-  const unsigned long long thr = threshold(u_draw, total);
+  bool whole;
+  const unsigned long long thr = draw_threshold(u_draw, total, whole);
   unsigned long long cum = before;
   int y = -1;
   if (total == 0ull || !valid) {   // nothing to draw from, or weights that sum to 4 and more

@@ -118,7 +118,8 @@ typedef enum {
   DFLASH_K_ATTN = 1,      /* split-KV context attention + merge           */
   DFLASH_K_NORM = 2,      /* RMSNorm / embedding / small row kernels      */
   DFLASH_K_ARGMAX = 3,    /* argmax finalisation                          */
-  DFLASH_K_VERIFY = 4     /* verify-accept                                */
+  DFLASH_K_VERIFY = 4,    /* verify-accept, draws                         */
+  DFLASH_K_PAGES = 5      /* page bookkeeping and copies                  */
 } dflash_kernel_kind;
 
 typedef struct {
@@ -605,6 +606,139 @@ dflash_status dflash_verify_probs(const dflash_config* cfg, const void* target_p
                                   const float* u_accept, const float* u_draw, int B, int32_t* tau,
                                   int32_t* committed, int32_t* next_anchor, int32_t* dev_status,
                                   dflash_trace* trace, dflash_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Drafted trees. Instead of one chain of drafts a caller may let the target
+ * verify a tree of them: several candidates for a position, each with
+ * continuations. The nodes of sequence b are its packed rows (cu_rows, as
+ * above), its first row the root (the anchor, a token already committed), and
+ * node i's key and value lie in the cache at position ctx_len[b] + i whatever
+ * its depth; its RoPE position is ctx_len[b] + depth. One step:
+ *   dflash_tree_masks        masks and positions, once for all layers
+ *   per layer                dflash_qk_norm_rope (those positions), dflash_kv_append_paged
+ *                            (no gains, no tables: rows as they are), dflash_attention_tree_paged
+ *   dflash_sample            a token behind every node
+ *   dflash_verify_tree       the branch that the tokens confirm; its rows move behind the context
+ *   ctx_len += tau           by the caller, as for the other target-side calls
+ * parents: device int32 [T], the parent's number within its sequence (0 is the
+ * root), smaller than the node's own; -1 for none. */
+#define DFLASH_MAX_TREE 1024 /* nodes of a sequence in dflash_verify_tree */
+
+/* Masks and positions of a ragged batch of trees:
+ *   bit j % 32 of mask[t][j / 32] = 1 where node j is node t or an ancestor of it
+ *   positions[t] = ctx_len[b] + depth of the node (0 without a parent)
+ * mask: device [T, mask_words]; every word of the rows below cu_rows[B] is
+ *   written. positions: device [T], or NULL (ctx_len may then be NULL).
+ * A parent that is not below its node counts as none, and a node from
+ *   32 * mask_words on has no bit of its own; both set DFLASH_ERR_INVALID_ARG in
+ *   dev_status. T == 0 or B == 0 launches nothing. */
+dflash_status dflash_tree_masks(const int32_t* parents, const int32_t* cu_rows, const int32_t* ctx_len, int B,
+                                int T, int mask_words, uint32_t* mask, int32_t* positions, int32_t* dev_status,
+                                dflash_trace* trace, dflash_stream_t stream);
+
+/* dflash_attention_chunk_paged with a mask over the chunk's own keys: row t of
+ * sequence b sees keys 0 .. ctx_len[b] - 1 and the keys ctx_len[b] + j whose
+ * bit j of mask[t] is set (j below the sequence's rows; bits behind them and
+ * keys behind 32 * mask_words are not seen). Any mask is allowed, not only
+ * those of trees; a row that sees no key gives zeros. mask: device
+ * [T, mask_words], mask_words >= 1. Other arguments, workspace and errors as
+ * there. */
+dflash_status dflash_attention_tree_paged(const dflash_heads* heads, const void* q, long long ld_q,
+                                          const int32_t* cu_rows, const int32_t* ctx_len, int B, int T,
+                                          int max_rows, int max_ctx_hint, int layer,
+                                          const dflash_kv_pages* pages, const uint32_t* mask, int mask_words,
+                                          float scale, void* out, long long ld_o, int32_t* dev_status,
+                                          void* ws, size_t ws_bytes, dflash_trace* trace,
+                                          dflash_stream_t stream);
+
+/* Shaped distributions and draws from given random numbers, for every row n of
+ * logits (device [N, V] of logits_dtype, rows ld elements apart):
+ *   w_v = exp((x_v - max x) / temperature[n])
+ *   tokens in the order of x, larger ones first, equal ones by their index:
+ *   top_k    the first top_k[n] stay;
+ *   top_p    of these, those before which less than top_p[n] of their weight lies;
+ *   min_p    of these, those with w_v >= min_p[n]; the first one always stays
+ *   probs[n][v] = w_v / (sum of the weights that stay), 0 for the others
+ *   tokens[n] = the first v with w_0 + .. + w_v > u[n] * (sum), over those that stay
+ * temperature, top_p, min_p, u: device fp32 [N], top_k: device int32 [N]; each
+ *   but u may be NULL: 1, off, off, off. temperature 0 takes the largest entry
+ *   (the lowest index on ties). top_k < 1, top_p >= 1 (or NaN) and min_p <= 0
+ *   (or NaN) are off; min_p above 1 counts as 1; u is taken in [0, 1).
+ * tokens: device int32 [N] with u, or both NULL; probs: device fp32 [N, V] or
+ *   NULL (dflash_verify_probs takes it for target_probs); one of the two.
+ * -inf and NaN logits have no weight; +inf counts as the largest finite number.
+ *   A row of nothing else, and a temperature that is negative or NaN, set
+ *   DFLASH_ERR_INVALID_ARG in dev_status and give token 0 and a row of zeros.
+ * Weights are exact to 2^-30 and summed as integers (multiples of 2^-43 of the
+ *   largest): no result depends on an order of summation.
+ * Rows may begin at any element and lie at any stride ld >= V (those whose
+ *   addresses are multiples of 16 bytes are a little faster to write).
+ * Limits: N <= 2^20, V <= 2^19, else DFLASH_ERR_TOO_LARGE. No workspace; one
+ *   launch; N == 0 launches nothing. */
+dflash_status dflash_sample(const void* logits, dflash_dtype logits_dtype, long long ld, int N, int V,
+                            const float* temperature, const int32_t* top_k, const float* top_p,
+                            const float* min_p, const float* u, int32_t* tokens, float* probs,
+                            int32_t* dev_status, dflash_trace* trace, dflash_stream_t stream);
+
+/* The branch of each tree that the target's tokens confirm: from the root on,
+ * the first child whose token is the one drawn behind its parent.
+ *   path[b]  = 0, i_1, i_2, ...   tokens[i_j] == drawn[i_{j-1}], parents[i_j] == i_{j-1}
+ *   tau[b]   = nodes of the path; committed[b] = tokens[i_1], ..., drawn[last]
+ *   next_anchor[b] = drawn[last]
+ * path and committed are padded with -1 to max_path entries; a path ends at
+ * max_path nodes. With drawn tokens from dflash_sample (or an argmax) they are
+ * distributed as the target's own, whatever the tree holds.
+ * tokens, parents, drawn: device int32 [T] (drawn[t]: the token behind node t).
+ * With pages, the path's rows of keys and values move in every layer,
+ *   position ctx_len[b] + i_j  ->  ctx_len[b] + j,
+ * so that the sequence goes on with ctx_len[b] + tau[b] tokens; what lies behind
+ * them is then unspecified. Pages holding those positions must belong to one
+ * sequence. pages NULL: nothing moves (heads and ctx_len may be NULL). A
+ * position without a page sets DFLASH_ERR_CAPACITY and its row does not move.
+ * A sequence of more than DFLASH_MAX_TREE nodes, a first row with a parent and
+ * parents outside the tree set DFLASH_ERR_INVALID_ARG: the sequence without rows
+ * taken (tau 0, -1 everywhere, also that of a sequence without rows), the node
+ * left out. One launch; B == 0 launches nothing. */
+dflash_status dflash_verify_tree(const dflash_heads* heads, const int32_t* tokens, const int32_t* parents,
+                                 const int32_t* drawn, const int32_t* cu_rows, const int32_t* ctx_len, int B,
+                                 int T, int max_path, const dflash_kv_pages* pages, int32_t* tau,
+                                 int32_t* committed, int32_t* path, int32_t* next_anchor,
+                                 int32_t* dev_status, dflash_trace* trace, dflash_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Pages of a paged cache: who holds which. refs (device int32 [n_pages]) counts
+ * the table entries that name a page; a page with a count of 0 is free. A table
+ * entry is a page id or -1. These calls write the table of `pages` (the memory
+ * behind its page_table) and refs; both are the caller's, refs starts as the
+ * table says (all 0 for a table of -1). A free page is always the one with the
+ * lowest id, in the order of sequences and their entries, so results do not
+ * depend on timing. Entries outside [0, n_pages) count as -1. Nothing but these
+ * calls may write table and refs while they run.
+ *
+ * release: sequence b keeps the pages of its positions 0 .. keep_len[b] - 1;
+ *   the others' counts go down and their entries become -1 (keep_len 0: all).
+ *   An entry whose page has no count sets DFLASH_ERR_INVALID_ARG. A sequence cut
+ *   back into a page that it shares must not be written on there.
+ * reserve: entries of sequence b that are -1 and belong to a position below
+ *   want_len[b] get a free page each. Positions beyond the table and pages that
+ *   are not there set DFLASH_ERR_CAPACITY; such entries stay -1. B <= 4096.
+ * fork: for every pair i, sequence dst[i] becomes a copy of sequence src[i]:
+ *   dst's pages are released, src's full pages are shared, the page that holds
+ *   the rest of its ctx_len[src] positions is copied (those rows, every layer)
+ *   to a page of dst's own, and ctx_len[dst] = ctx_len[src]. Shared pages hold
+ *   whole pages of committed positions, so nobody writes them. seqs: rows of
+ *   the table and of ctx_len. A pair with a number outside [0, seqs), a length
+ *   outside the table, a target that is another pair's source or an earlier
+ *   pair's target is left out (DFLASH_ERR_INVALID_ARG); one that finds no free
+ *   page, or whose source lacks a page, leaves dst empty with ctx_len 0
+ *   (DFLASH_ERR_CAPACITY). n <= 1024 pairs, two launches. */
+dflash_status dflash_pages_release(const dflash_kv_pages* pages, int32_t* refs, const int32_t* keep_len, int B,
+                                   int32_t* dev_status, dflash_trace* trace, dflash_stream_t stream);
+dflash_status dflash_pages_reserve(const dflash_kv_pages* pages, int32_t* refs, const int32_t* want_len, int B,
+                                   int32_t* dev_status, dflash_trace* trace, dflash_stream_t stream);
+dflash_status dflash_pages_fork(const dflash_heads* heads, const dflash_kv_pages* pages, int32_t* refs,
+                                int32_t* ctx_len, int seqs, const int32_t* src, const int32_t* dst, int n,
+                                int32_t* dev_status, dflash_trace* trace, dflash_stream_t stream);
 
 #ifdef __cplusplus
 }

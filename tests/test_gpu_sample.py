@@ -1,0 +1,254 @@
+"""GPU: shaped distributions and draws (dflash_sample) against the float64 oracle.
+
+Tokens, and which entries have weight, have to be equal: weights carry 2^-30,
+so a border case would need a draw within 2^-30 of a border. A probability is
+off by 2^-30 (its weight) and four roundings of 2^-24 (weight, sum, reciprocal,
+product), and by 2^-43 of the largest weight that the integer cuts off; a row's
+sum is at least that weight."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import tree_ref as tt
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def dfl(lib):
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    return lib
+
+
+def dev(v, dt=torch.float32):
+    return None if v is None else torch.tensor(v, dtype=dt, device="cuda")
+
+
+def run(dfl, x, u, T=None, k=None, p=None, m=None, probs=True, tokens=True, **kw):
+    N, V = x.shape
+    tok = torch.full((N + 1,), -7, dtype=torch.int32, device="cuda")
+    pr = torch.full((N, V), 9.0, device="cuda") if probs else None
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dfl.dflash_sample(x, dev(u) if tokens else None, tok if tokens else None, st, temperature=dev(T), top_k=dev(k, torch.int32),
+                      top_p=dev(p), min_p=dev(m), probs=pr, **kw)
+    torch.cuda.synchronize()
+    assert int(tok[N]) == -7
+    return tok[:N].tolist(), None if pr is None else pr.double().cpu().numpy(), int(st)
+
+
+def check(dfl, x, u, T=None, k=None, p=None, m=None, **kw):
+    """Every row against the oracle, with and without the distributions."""
+    tok, pr, st = run(dfl, x, u, T, k, p, m, **kw)
+    alone, _, _ = run(dfl, x, u, T, k, p, m, probs=False, **kw)
+    _, only, _ = run(dfl, x, u, T, k, p, m, tokens=False, **kw)
+    assert tok == alone and np.array_equal(pr, only)
+    f32 = lambda v: float(np.float32(v))  # noqa: E731
+    xs = x.double().cpu().numpy()
+    big = float(torch.finfo(x.dtype).max)
+    bad = False
+    for n in range(x.shape[0]):
+        want = tt.shape(np.where(xs[n] == np.inf, big, xs[n]), 1.0 if T is None else f32(T[n]), 0 if k is None else k[n],
+                        1.0 if p is None else f32(p[n]), 0.0 if m is None else f32(m[n]))
+        if want is None:
+            assert tok[n] == 0 and not pr[n].any()
+            bad = True
+            continue
+        assert ((pr[n] > 0) <= (want > 0)).all() and ((pr[n] == 0) <= (want < 2.0 ** -42)).all(), (n, (pr[n] > 0).sum(), (want > 0).sum())
+        assert (np.abs(pr[n] - want) <= 2.0 ** -22 * 1.01 * want + 2.0 ** -43).all(), (n, np.abs(pr[n] - want).max())
+        assert tok[n] == tt.draw(want, f32(u[n])), (n, tok[n], tt.draw(want, f32(u[n])))
+    assert st == (dfl.ERR_INVALID_ARG if bad else 0)
+    return tok, pr
+
+
+def logits(N, V, dtype, seed, kind="zipf"):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    if kind == "zipf":
+        x = torch.empty((N, V), device="cuda").exponential_(generator=g) * (1.0 + torch.rand((N, 1), generator=g, device="cuda")) - 5
+    else:
+        x = torch.randn((N, V), generator=g, device="cuda") * 2.5
+    return x.to(dtype)
+
+
+def settings(N, seed):
+    r = np.random.default_rng(seed)
+    return dict(T=r.choice([0.0, 0.3, 0.7, 1.0, 1.3], N).tolist(), k=[int(v) for v in r.choice([0, 0, 1, 2, 20, 50, 700], N)],
+                p=r.choice([1.0, 0.5, 0.9, 0.95, 0.999, 0.0], N).tolist(), m=r.choice([0.0, 0.0, 0.05, 0.3, 1.0], N).tolist())
+
+
+def uniforms(N, seed):
+    return np.random.default_rng(seed).random(N, dtype=np.float32).tolist()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("V", [1, 2, 7, 33, 1003, 4103, 32000, 151936, 200003])
+def test_matches_the_oracle(dfl, V, dtype):
+    N = 24 if V < 100000 else 10
+    for kind in ("zipf", "normal"):
+        check(dfl, logits(N, V, dtype, V + len(kind), kind), uniforms(N, V), **settings(N, V))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("N", [1, 3, 37, 150, 320])
+def test_rows_by_the_number(dfl, N, dtype):
+    """Every way that a row is divided over CTAs."""
+    check(dfl, logits(N, 20011, dtype, N), uniforms(N, N), **settings(N, N))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("one", ["T", "k", "p", "m", "none"])
+def test_each_setting_alone(dfl, one, dtype):
+    N, V = 12, 50257
+    s = settings(N, 5)
+    s["k"] = [5000, 40000, 60000, 50257, 50256, 513, 4097, 3, -1, 0, 1, 100]
+    check(dfl, logits(N, V, dtype, 3), uniforms(N, 3), **{k: v for k, v in s.items() if k == one})
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("V", [500, 30011])
+def test_ties(dfl, V, dtype):
+    """Values on a coarse grid, also around zero and of either sign of it: borders fall among equal entries."""
+    N = 40
+    x = (logits(N, V, F32, 7, "normal") / 1.5).round() * 0.5
+    x[::2] = torch.where(x[::2] == 0, -0.0, x[::2])
+    x[::4, ::3] = torch.where(x[::4, ::3] == 0, 0.0, x[::4, ::3])
+    x[5] = 1.25                                 # all equal
+    x[6] = -3.0
+    x[7] = 0.0
+    check(dfl, x.to(dtype), uniforms(N, 8), **settings(N, 9))
+    s = settings(N, 10)
+    check(dfl, x.to(dtype), uniforms(N, 11), T=[1.0] * N, k=[int(v) for v in np.random.default_rng(1).integers(1, V, N)], p=s["p"])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+def test_masked_infinite_and_extreme_entries(dfl, dtype):
+    N, V = 20, 9001
+    low, big = torch.finfo(dtype).min, torch.finfo(dtype).max
+    x = logits(N, V, dtype, 13)
+    x[0, ::2] = -float("inf")
+    x[1, 1:] = -float("inf")                    # one entry left
+    x[2, :] = -float("inf")                     # none
+    x[3, ::3] = low
+    x[4, :] = low                               # all of the lowest value: even weights
+    x[5, 77] = float("inf")
+    x[6, 77:80] = float("inf")                  # even weights
+    x[7, ::5] = float("nan")
+    x[8, :] = float("nan")
+    x[9, :] = big
+    x[10, ::2] = low
+    x[10, 5] = big
+    x[11] = x[11] * 1e-30
+    x[12] = x[12] * 1e30
+    x[13, :] = -1e-38
+    x[14, :8990] = -float("inf")                # the last entries alone
+    x[15, 11:] = -float("inf")                  # fewer entries than k
+    x[16, 40:] = low
+    for s in (settings(N, 17), dict(T=[1.0] * N), dict(T=[1.0] * N, k=[50] * N), dict(T=[0.8] * N, p=[0.9] * N),
+              dict(T=[1.0] * N, k=[3000] * N, p=[0.9] * N, m=[0.01] * N), dict(T=[0.0] * N)):
+        check(dfl, x, uniforms(N, 19), **s)
+
+
+def test_temperatures_and_uniforms_at_their_ends(dfl):
+    V = 5003
+    T = [1e-30, 1e-6, 1e-2, 30.0, 1e6, 1e30, float("inf"), 0.7, 0.7, 0.7, 0.7, 0.7]
+    N = len(T)
+    x = logits(N, V, F32, 23)
+    u = [0.5] * 7 + [0.0, 1e-40, 1e-30, float(np.float32(1 - 2.0 ** -24)), 0.9999]
+    check(dfl, x, u, T=[min(t, 3e38) for t in T])
+    check(dfl, x, u, T=[min(t, 3e38) for t in T], p=[0.9, 0.9, 0.9, 0.9, 0.9, 0.5, 0.5, 1e-40, 1e-10, 0.0, float(np.float32(1 - 2.0 ** -24)), 0.99])
+    tok, pr, st = run(dfl, x, u, T=T)          # an infinite temperature: even weights
+    assert st == 0 and np.allclose(pr[6], 1 / V, rtol=1e-6)
+    for bad in (-1.0, float("nan")):
+        tok, pr, st = run(dfl, x, u, T=T[:3] + [bad] + T[4:])
+        assert st == dfl.ERR_INVALID_ARG and tok[3] == 0 and not pr[3].any() and pr[2].any()
+
+
+def test_settings_that_are_off(dfl):
+    V, N = 2000, 6
+    x, u = logits(N, V, F32, 29), uniforms(N, 29)
+    want = run(dfl, x, u)
+    nan = float("nan")
+    got = run(dfl, x, u, T=[1.0] * N, k=[0, -1, -2 ** 31, V, V + 1, 2 ** 31 - 1], p=[1.0, 2.0, nan, 1.0, 1.0, 7.0],
+              m=[0.0, -1.0, nan, 0.0, 0.0, -0.0])
+    assert got[0] == want[0] and np.array_equal(got[1], want[1])
+    got = run(dfl, x, u, m=[5.0] * N)          # above 1 counts as 1
+    assert got[0] == x.argmax(-1).tolist()
+    clamped = run(dfl, x, [-3.0, nan, 1.0, 7.0, 0.0, 0.5])
+    assert clamped[0][0] == clamped[0][1] == clamped[0][4] == 0
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("V,ld,off", [(1001, 1001, 0), (1001, 1009, 3), (4096, 4104, 1), (777, 2000, 5), (30000, 30001, 7)])
+def test_rows_at_any_element_and_stride(dfl, V, ld, off, dtype):
+    """Entries beside a row belong to others: larger than all of its own."""
+    N = 5
+    buf = torch.full((N * ld + off + 16,), 30.0, dtype=dtype, device="cuda")
+    x = torch.as_strided(buf, (N, V), (ld, 1), off)
+    x.copy_(logits(N, V, dtype, 31))
+    check(dfl, x, uniforms(N, 31), **settings(N, 37))
+
+
+def test_a_large_vocabulary(dfl):
+    for V, dtype in ((1 << 19, F32), ((1 << 19) - 3, BF), (300007, F32)):
+        check(dfl, logits(3, V, dtype, 41), uniforms(3, 41), T=[1.0, 0.8, 1.5], k=[0, 100, 0], p=[1.0, 0.9, 0.8])
+
+
+def test_many_rows(dfl):
+    N, V = 3000, 1500
+    x = logits(N, V, BF, 43)
+    check(dfl, x, uniforms(N, 43), **settings(N, 43))
+
+
+def test_draws_are_distributed_as_the_distribution(dfl):
+    N, V = 20000, 37
+    x = logits(1, V, F32, 47, "normal").expand(N, V)          # a stride of zero is refused
+    with pytest.raises(dfl.DFlashError):
+        run(dfl, x, uniforms(N, 47), probs=False)
+    tok, _, _ = run(dfl, x.contiguous(), uniforms(N, 47), T=[1.2] * N, k=[20] * N, probs=False)
+    want = tt.shape(x[0].double().cpu().numpy(), float(np.float32(1.2)), 20)
+    got = np.bincount(tok, minlength=V)
+    assert (got[want == 0] == 0).all()
+    on = want > 0
+    chi = ((got[on] - N * want[on]) ** 2 / (N * want[on])).sum()
+    assert chi < 19 + 6 * np.sqrt(2 * 19)                     # 19 degrees of freedom
+
+
+def test_from_a_graph_on_another_stream_and_beside_another_call(dfl):
+    N, V = 17, 151936
+    a, b = logits(N, V, F32, 53), logits(40, V, BF, 59)
+    sa, sb = settings(N, 53), settings(40, 59)
+    ua, ub = uniforms(N, 53), uniforms(40, 59)
+    ta, _ = check(dfl, a, ua, **sa)
+    tb, _ = check(dfl, b, ub, **sb)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = [torch.zeros(n, dtype=torch.int32, device="cuda") for n in (N, 40)]
+    arg = [[dev(u), dict(temperature=dev(s["T"]), top_k=dev(s["k"], torch.int32), top_p=dev(s["p"]), min_p=dev(s["m"]))]
+           for u, s in ((ua, sa), (ub, sb))]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        dfl.dflash_sample(a, arg[0][0], out[0], st, **arg[0][1])
+        dfl.dflash_sample(b, arg[1][0], out[1], st, **arg[1][1], stream=side)
+    torch.cuda.synchronize()
+    assert out[0].tolist() == ta and out[1].tolist() == tb
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dfl.dflash_sample(a, arg[0][0], out[0], st, **arg[0][1])
+    out[0].zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert out[0].tolist() == ta
+    a.copy_(logits(N, V, F32, 54))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert out[0].tolist() == run(dfl, a, ua, **sa, probs=False)[0] and int(st) == 0
+
+
+def test_empty_and_traced(dfl):
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    none = torch.zeros(0, device="cuda")
+    dfl.dflash_sample(torch.zeros((0, 50), device="cuda"), none, none.int(), st)
+    rec = dfl.TraceRecorder(2)
+    run(dfl, logits(3, 500, BF, 61), uniforms(3, 61), trace=rec.struct)
+    assert [(k, b) for k, b, _, _ in rec.records()] == [(dfl.K_VERIFY, 3.0 * 500 * 6)]
