@@ -641,9 +641,9 @@ def dflash_verify_probs(cfg, target_probs, draft_probs, draft, u_accept, u_draw,
 
 
 # ---------------------------------------------------------------- drafted trees
-def dflash_tree_masks(parents, cu_rows, ctx_len, mask, dev_status, positions=None, trace=None, stream=None):
-    """Masks [T, words] (int32 bits) and positions [T] of a ragged batch of trees
-    given by every node's parent within its sequence (-1 for none)."""
+def dflash_tree_masks(parents, cu_rows, ctx_len, mask, positions, dev_status, trace=None, stream=None):
+    """Masks [T, words] (int32 bits) and positions [T] (or None) of a ragged batch of
+    trees given by every node's parent within its sequence (-1 for none)."""
     fn = "dflash_tree_masks"
     T, B = parents.numel(), cu_rows.numel() - 1
     words = _mask_words(mask, T, fn)

@@ -42,7 +42,7 @@ def test_masks_and_positions(dfl, ns, more):
     pos = torch.full((T + 3,), 77, dtype=torch.int32, device="cuda")
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
     par = ints([p for t in trees for p in t] + [5, 5, 5])     # rows behind the last sequence
-    dfl.dflash_tree_masks(par, cu, ctx, mask, st, pos)
+    dfl.dflash_tree_masks(par, cu, ctx, mask, pos, st)
     torch.cuda.synchronize()
     assert int(st) == 0 and (mask[T:] == 77).all() and (pos[T:] == 77).all()
     at = 0
@@ -54,7 +54,7 @@ def test_masks_and_positions(dfl, ns, more):
         assert pos[at:at + len(t)].tolist() == (100 * b + m.sum(1) - 1).tolist()
         at += len(t)
     again = torch.full_like(mask, 77)
-    dfl.dflash_tree_masks(par, cu, None, again, st)           # without positions
+    dfl.dflash_tree_masks(par, cu, None, again, None, st)           # without positions
     torch.cuda.synchronize()
     assert torch.equal(again, mask)
 
@@ -65,7 +65,7 @@ def test_what_is_no_tree_is_reported(dfl):
         n = len(parents)
         mask = torch.full((n, words), 77, dtype=torch.int32, device="cuda")
         pos, st = torch.zeros(n, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
-        dfl.dflash_tree_masks(ints(parents), ints([0, n]), ints([7]), mask, st, pos)
+        dfl.dflash_tree_masks(ints(parents), ints([0, n]), ints([7]), mask, pos, st)
         torch.cuda.synchronize()
         assert int(st) == (dfl.ERR_INVALID_ARG if bad else 0), parents
         t = [p if p < i else -1 for i, p in enumerate(parents)]

@@ -125,7 +125,7 @@ def test_the_binding_refuses_what_the_library_cannot_see(lib, heads):
             f()
         assert e.value.status in [getattr(lib, "ERR_" + s) for s in status], e.value
 
-    masks = lambda par=one(4), cu=cu, ctx=ctx, mask=one(4, 1), pos=one(4): lib.dflash_tree_masks(par, cu, ctx, mask, st, pos)  # noqa: E731
+    masks = lambda par=one(4), cu=cu, ctx=ctx, mask=one(4, 1), pos=one(4): lib.dflash_tree_masks(par, cu, ctx, mask, pos, st)  # noqa: E731
     for kw, want in [(dict(par=one(4).long()), "DTYPE"), (dict(mask=one(3, 1)), "SHAPE"), (dict(mask=one(4)), "SHAPE"),
                      (dict(mask=one(4, 2)[:, :1]), "SHAPE"), (dict(mask=torch.zeros(4, 1)), "DTYPE"), (dict(pos=one(3)), "SHAPE"),
                      (dict(ctx=one(1)), "SHAPE"), (dict(ctx=None), "INVALID_ARG")]:
