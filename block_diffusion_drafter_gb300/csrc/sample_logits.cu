@@ -9,23 +9,25 @@
 //   y = min { v : sum of the kept weights up to v > u * their sum }.
 //
 // Which token a border case gives must not depend on rounding or on an order of
-// summation: weights are integers W = floor(w 2^43), computed to about 2^-31 of
-// themselves by a function of (x, max, T) alone, and every sum of them is exact.
-// At V entries of random weights the drawn token differs from that of exact
-// weights with a probability of about sqrt(V) 2^-31 (2^-31 errors add at random
-// along the prefix), 2e-7 for 151936 entries; fp32 weights would give 1e-3 from
-// the exponent's rounding alone.
+// summation: weights are integers W = floor(w 2^43), computed to 2^-30 of
+// themselves (2^-27.6 at most) by a function of (x, max, T) alone, and every sum of
+// them is exact. At V entries of random weights the drawn token differs from that of
+// exact weights with a probability of about sqrt(V) 2^-30 (the errors add at random
+// along the prefix), 4e-7 for 151936 entries; fp32 weights would give 1e-3 from the
+// exponent's rounding alone.
 //
 // A row belongs to a cluster of CTAs, each of which keeps a contiguous part of it
-// in shared memory, each warp a contiguous part of that: logits are read from
-// HBM once. Borders are found without sorting: a histogram over the candidates
-// (a count or a weight a bin), the clusters' bins added through distributed
-// shared memory, the border's bin taken apart further. The first level's bins
-// are linear in max - x, the further ones cut the range of the values' ordered
-// bit patterns, 11 or 10 bits a level, until a bin holds one entry or one value.
-// Candidates are few: for top-k, k threads hold an entry of the k-th largest
-// thread maximum or more; for top-p, entries below max - T ln(V / (1 - p)) weigh
-// less than 1 - p together.
+// in shared memory, each warp a contiguous part of that: logits are read from HBM
+// once. What a row asks for decides how much follows, always the same for a cluster:
+//   the largest entry (temperature 0, top-k 1): one exchange of the CTAs' maxima;
+//   top-k up to kMostListed, and top-p: a lower bound of the border from the maxima of
+//     the threads' entries, which leaves some k, or some hundreds, of candidates. The
+//     first CTA sorts these and finds border and token by itself;
+//   neither: the weights' sums a warp, and the warp that holds the threshold;
+//   where the candidates do not fit the list or do not hold the border (flat rows, many
+//     equal entries, a large k): histograms over the bits of the values, counts for
+//     top-k, weights for top-p, added over the cluster through distributed shared
+//     memory, the border's bin taken apart further until it holds one entry or value.
 #include <cuda_bf16.h>
 #include <float.h>
 
@@ -39,25 +41,26 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxParts = 16;
 constexpr int kCountBins = 2048, kMassBins = 1024;
 constexpr int kHistInts = 4096;      // 16 KB: counts, or counts and three parts of a weight
+constexpr int kOwnList = 1024, kList = 2048;   // candidates of a CTA and of a row: 24 KB
+constexpr int kMostListed = 1280;    // top-k borders that the list is made for
+constexpr int kHoped = 640;          // candidates among which top-p's border is looked for first
+constexpr int kScratchBytes = (kOwnList + kList) * 8;   // the lists, or the histograms
 constexpr int kInFlight = 5;         // 16-byte loads a thread
 constexpr int kOne = 43;             // the largest weight is 2^43
 typedef unsigned long long u64;
 constexpr unsigned kAll = 0xffffffffu;
 
-// 2^(j/32), j = 0 .. 31, in two floats (from the exponential's definition).
+// 2^(j/32), j = 0 .. 31 (from the exponential's definition): the largest float not
+// above it, and the rest times 2^36.
 __device__ const float kPow2[32][2] = {
-    {1.0f, 0.0f}, {1.0218971967697144f, -4.811559861650494e-08f}, {1.0442737340927124f, 4.8334701574503924e-08f},
-    {1.0671404600143433f, -5.9337519786595294e-08f}, {1.0905077457427979f, -1.3077539939843064e-08f}, {1.114386796951294f, -5.435540018083884e-08f},
-    {1.1387885808944702f, 5.386222312608879e-08f}, {1.1637248992919922f, -4.051441493402308e-08f}, {1.1892070770263672f, 3.797635272917432e-08f},
-    {1.215247392654419f, -3.267394887984665e-08f}, {1.2418577671051025f, 4.496838101886169e-08f}, {1.2690509557724f, 1.419333317542737e-09f},
-    {1.2968395948410034f, -4.018999533172973e-08f}, {1.3252366781234741f, -3.496373324196611e-08f}, {1.3542555570602417f, -1.0123349269974824e-08f},
-    {1.3839099407196045f, -5.875577357983275e-08f}, {1.4142135381698608f, 2.4203234971764687e-08f}, {1.4451807737350464f, 3.324199937537742e-08f},
-    {1.4768261909484863f, -4.500898853621038e-08f}, {1.5091644525527954f, -2.4959373234878512e-08f}, {1.5422108173370361f, 8.070904833346049e-09f},
-    {1.5759809017181396f, -5.661025426206834e-08f}, {1.610490322113037f, 9.836217174097328e-09f}, {1.6457555294036865f, -5.124972091152813e-08f},
-    {1.6817928552627563f, -2.4755326677450284e-08f}, {1.7186193466186523f, -4.8496175963919086e-08f}, {1.7562521696090698f, -9.235770370707996e-09f},
-    {1.7947090864181519f, -1.141504490931311e-08f}, {1.8340080976486206f, -1.1239277952768134e-08f}, {1.8741676807403564f, -4.663005626071026e-08f},
-    {1.9152065515518188f, 9.845328108326612e-09f}, {1.9571441411972046f, -1.7021804410433106e-08f}
-};
+    {1.0f, 0.0f}, {1.0218970775604248f, 4885.521484375f}, {1.0442737340927124f, 3321.535400390625f}, {1.0671403408050537f, 4114.35693359375f},
+    {1.0905076265335083f, 7293.318359375f}, {1.1143866777420044f, 4456.72509765625f}, {1.1387885808944702f, 3701.3837890625f}, {1.1637247800827026f, 5407.87060546875f},
+    {1.1892070770263672f, 2609.715087890625f}, {1.2152472734451294f, 5946.6630859375f}, {1.2418577671051025f, 3090.20361328125f}, {1.2690509557724f, 97.53584289550781f},
+    {1.2968394756317139f, 5430.16455078125f}, {1.3252365589141846f, 5789.310546875f}, {1.3542554378509521f, 7496.32861328125f}, {1.383909821510315f, 4154.333984375f},
+    {1.4142135381698608f, 1663.233642578125f}, {1.4451807737350464f, 2284.372802734375f}, {1.4768260717391968f, 5099.005859375f}, {1.5091643333435059f, 6476.80517578125f},
+    {1.5422108173370361f, 554.6283569335938f}, {1.57598078250885f, 4301.77294921875f}, {1.610490322113037f, 675.939697265625f}, {1.645755410194397f, 4670.14599609375f},
+    {1.6817927360534668f, 6490.82666015625f}, {1.7186192274093628f, 4859.3681640625f}, {1.7562520503997803f, 7557.32275390625f}, {1.7947089672088623f, 7407.56396484375f},
+    {1.834007978439331f, 7419.642578125f}, {1.874167561531067f, 4987.60693359375f}, {1.9152065515518188f, 676.5657958984375f}, {1.957144021987915f, 7022.2705078125f}};
 
 // A value's place in the order: larger float, larger key; -0 is 0.
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -94,8 +97,18 @@ __device__ __forceinline__ uint4 ld_peer_v4(const void* p, int rank) {
                : "memory");
   return v;
 }
+__device__ __forceinline__ void st_peer_u64(const void* p, int rank, u64 v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(mapa_shared(smem_u32(p), rank)), "l"(v) : "memory");
+}
 __device__ __forceinline__ void st_peer_u32(const void* p, int rank, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(p), rank)), "r"(v) : "memory");
+}
+
+// The least whole number of which at least p of `all` lies before: ceil(p * all), 1 or more.
+__device__ __forceinline__ u64 draw_ceil(float p, u64 all) {
+  bool whole;
+  const u64 t = draw_threshold(fmaxf(p, 0.f), all, whole);
+  return t + (whole && t > 0ull ? 0ull : 1ull);
 }
 
 template <typename TT>
@@ -138,64 +151,125 @@ struct Pack<__nv_bfloat16> {
   }
 };
 
-// The weight's function: 2^43 exp((x - m) / T), with c = log2(e) / T in two floats.
-// s + e = m - x exactly; y = (s + e) c = p + pe; y = i / 32 - r with |r| <= 1/64 + |pe|;
-// 2^-y = 2^(-i/32) 2^r, the first factor from the table (a lane an entry, so a
-// shuffle is the lookup: no bank conflicts, where a table in shared memory has three
-// lanes a bank), the second 1 + q by the exponential's series to r^4 (r^5 term
-// below 2^-39). The table's high part, 24 bits, is kept as an integer and only the
-// rest is rounded: hi q + lo, below 2^-5, to 2^-36.
+__device__ __forceinline__ u64 pair2(float lo, float hi) {
+  u64 v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ float lo_of(u64 v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float hi_of(u64 v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+  u64 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ u64 fma2_down(u64 a, u64 b, u64 c) {
+  u64 d;
+  asm("fma.rm.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+  u64 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+  u64 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// The weight's function: 2^43 exp((x - m) / T), up to a factor near 1 that a row's
+// weights share and that changes no ratio: m log2(e) / T is rounded down to 32nds
+// (so that no weight is below its value), and r below is raised by 2^-8. c = log2(e) / T in two floats; z = x c - M with M that
+// rounded maximum; 32 z's floor i comes from one multiply-add rounded down onto
+// 1.5 2^23 (without c's low part, which 2^-8 covers, so that r stays positive);
+// r = z - i / 32 + 2^-8 < 0.036 is one exact sum rounded once, and the low part
+// added: off by at most 2^-29. 2^z = 2^(i >> 5) 2^((i & 31) / 32) 2^r: the
+// second factor from a table whose entries the lanes hold (a shuffle looks it up: no
+// bank conflicts, where shared memory has three lanes a bank), the third 1 + q by
+// the exponential's series to r^4 (r^5: 2^-34). The table's high part stays an
+// integer of 24 bits and only the rest, th q + tl < 2^-4, is rounded, to 2^-36. Where
+// m c is so large that x c would lose r, every entry with a weight lies within a
+// factor of two of m: x - m is then exact and takes x's place (base).
+// Two entries at once: 16 instructions an entry, about 30 with sums of two floats
+// in between (64 rows of 151936 entries, all weighed and summed: 43.6 -> PLAIN64 us).
 struct Weigh {
-  float m, ch, cl;
+  u64 ch32, ch, cl, neg_base, neg_max, start;
   float hi, lo;              // this lane's table entry
-  __device__ __forceinline__ void set(float top, float T, int lane) {
-    m = top;
+  static constexpr float kMagic = 12582912.f;         // 1.5 2^23, bits 0x4B400000
+  __device__ __forceinline__ void set(float m, float T, int lane) {
     T = fminf(fmaxf(T, 0x1p-100f), 0x1p100f);
     constexpr float kLh = 1.44269502162933349609375f, kLl = 1.92596303350e-8f;   // log2(e)
-    ch = __fdiv_rn(kLh, T);
-    cl = __fdiv_rn(__fmaf_rn(-ch, T, kLh) + kLl, T);
+    const float c = __fdiv_rn(kLh, T), d = __fdiv_rn(__fmaf_rn(-c, T, kLh) + kLl, T);
+    const float base = fabsf(m) * c < 65536.f ? 0.f : m;
+    const float top = floorf((m - base) * c * 32.f) * 0.03125f;
+    ch32 = pair2(32.f * c, 32.f * c);
+    ch = pair2(c, c);
+    cl = pair2(d, d);
+    neg_base = pair2(-base, -base);
+    neg_max = pair2(0x1p-8f - top, 0x1p-8f - top);
+    start = pair2(kMagic - 32.f * top, kMagic - 32.f * top);
     hi = kPow2[lane][0];
     lo = kPow2[lane][1];
   }
-  // Called by a whole warp.
+  __device__ __forceinline__ u64 one(float t, float q) const {
+    const uint32_t i = __float_as_uint(t);              // 0x4B400000 + floor(32 z)
+    const float th = __shfl_sync(kAll, hi, i), tl = __shfl_sync(kAll, lo, i);   // the lane is taken modulo 32
+    const uint32_t rest = __float2uint_rz(__fmaf_rn(th, q, tl));
+    const u64 mant = static_cast<u64>((__float_as_uint(th) & 0x7FFFFFu) | 0x800000u) * (1u << 20) + static_cast<u64>(rest) * 128u;
+    const uint32_t n = min((0x4B400000u + 31u - i) >> 5, 63u);   // far below (and -inf): nothing is left
+    return mant >> n;
+  }
+  // Weights of two entries, neither above m. Called by a whole warp.
+  __device__ __forceinline__ void two(float x0, float x1, u64& w0, u64& w1) const {
+    constexpr float kUp = 0x1p36f;
+    const u64 x = add2(pair2(x0, x1), neg_base);
+    const u64 t = fma2_down(x, ch32, start);
+    const u64 f = add2(t, pair2(-kMagic, -kMagic));
+    const u64 e = fma2(f, pair2(-0.03125f, -0.03125f), neg_max);          // exact
+    const u64 r = fma2(x, cl, fma2(x, ch, e));
+    u64 q = fma2(r, pair2(9.61812911e-3f * kUp, 9.61812911e-3f * kUp), pair2(5.55041087e-2f * kUp, 5.55041087e-2f * kUp));
+    q = fma2(r, q, pair2(0.240226507f * kUp, 0.240226507f * kUp));
+    q = mul2(r, fma2(r, q, pair2(0.693147181f * kUp, 0.693147181f * kUp)));
+    w0 = one(lo_of(t), lo_of(q));
+    w1 = one(hi_of(t), hi_of(q));
+  }
   __device__ __forceinline__ u64 operator()(float x) const {
-    const float s = __fsub_rn(m, x), bb = __fsub_rn(s, m);
-    const float e = __fadd_rn(__fsub_rn(m, __fsub_rn(s, bb)), __fsub_rn(-x, bb));
-    float p = __fmul_rn(s, ch);
-    float pe = __fmaf_rn(e, ch, __fmaf_rn(s, cl, __fmaf_rn(s, ch, -p)));
-    const bool in = p < static_cast<float>(kOne + 1);   // false for -inf (and where s c overflows)
-    p = in ? p : 0.f;
-    pe = in ? pe : 0.f;
-    const float t = __fmaf_rn(p, 32.f, 12582912.f);     // 1.5 2^23: the low bits are round(32 p)
-    const int i = 0x4B400000 - __float_as_int(t);       // -round(32 p)
-    const float r = __fsub_rn(__fmaf_rn(__fsub_rn(t, 12582912.f), 0.03125f, -p), pe);
-    float q = __fmaf_rn(r, 9.618129e-3f, 5.5504109e-2f);
-    q = __fmaf_rn(r, q, 0.24022651f);
-    q = __fmul_rn(r, __fmaf_rn(r, q, 0.69314718f));
-    const float th = __shfl_sync(kAll, hi, i & 31), tl = __shfl_sync(kAll, lo, i & 31);
-    const int rest = __float2int_rn(__fmul_rn(__fmaf_rn(th, q, tl), 0x1p36f));
-    const u64 mant = (static_cast<u64>((__float_as_uint(th) & 0x7FFFFFu) | 0x800000u) << 13) + static_cast<long long>(rest);
-    return in ? (mant << (kOne - 36)) >> (-(i >> 5)) : 0ull;
+    u64 a, b;
+    two(x, x, a, b);
+    return a;
   }
 };
 
 // What stays: entries above `thr`, and of those equal to it the ones up to index `cut`.
-struct Border {
+struct __align__(8) Border {
   float thr;
-  int cut;
+  int cut;                   // 8 bytes: sent as one word
   __device__ __forceinline__ bool keeps(float x, int v) const { return x > thr || (x == thr && v <= cut); }
 };
 
+// What a CTA tells its peers: its largest entry (its key and the complement of its
+// index) and a key that at least `share` of its threads' maxima reach; then the weight
+// of its entries, of those that it lists, and their number.
+struct Told {
+  u64 top;
+  u64 floor;
+  u64 sum, listed, count;
+};
+
 struct Shared {
-  float warp_f[2][kWarps];
-  float2 part_f;                   // the CTA's largest entry, and the least thread maximum
+  Told told;
   u64 warp[2][kWarps];             // warps' sums, and the CTA's: two joins in turn
   u64 part[2];
   u64 scan[kWarps];
   u64 above;
+  float warp_f[kWarps];
   unsigned bin, count;
-  int tie;
-  double min_log;                  // T ln(min_p)
+  int tie, at;
+  Border border;                   // what the first CTA found
+  u64 total;
+  float2 min_log;                  // T ln(min_p), in two floats
 };
 
 template <typename TT>
@@ -204,7 +278,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
   constexpr int VEC = P::N;
   extern __shared__ __align__(16) uint4 s_data[];          // [kWarps][rows][32]
   __shared__ Shared sh;
-  unsigned* hist = reinterpret_cast<unsigned*>(s_data + kWarps * rows * 32);
+  unsigned* hist = reinterpret_cast<unsigned*>(s_data + kWarps * rows * 32);   // or: own list, all lists
+  u64* own = reinterpret_cast<u64*>(hist);
+  u64* list = own + kOwnList;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = blockIdx.x / parts, part = blockIdx.x % parts, V = p.V;
   pdl_launch_dependents();
@@ -216,21 +292,24 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
   const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(TT));
   const uint4* base = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(row) & ~static_cast<uintptr_t>(15));
   const int pieces = (shift + V + VEC - 1) / VEC;
-  const int first = (part * kWarps + warp) * rows * 32;    // this warp's first piece
+  // this warp's rows of 32 pieces, an even share of all, and its first piece
+  const int all_rows = (pieces + 31) / 32, id = part * kWarps + warp, warps = parts * kWarps;
+  const int row0 = static_cast<int>(static_cast<unsigned>(all_rows) * id / warps);
+  const int my_rows = static_cast<int>(static_cast<unsigned>(all_rows) * (id + 1) / warps) - row0, first = row0 * 32;
   uint4* mine = s_data + warp * rows * 32;
-  float top = -INFINITY;
+  float thread_top = -INFINITY;
   {
     const float none[8] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY};
-    for (int r0 = 0; r0 < rows; r0 += kInFlight) {
+    for (int r0 = 0; r0 < my_rows; r0 += kInFlight) {
       uint4 q[kInFlight];
 #pragma unroll
       for (int k = 0; k < kInFlight; ++k) {
         const int at = first + (r0 + k) * 32 + lane;
-        q[k] = r0 + k < rows && at < pieces ? __ldcs(base + at) : P::put(none);
+        q[k] = r0 + k < my_rows && at < pieces ? __ldcs(base + at) : P::put(none);
       }
 #pragma unroll
       for (int k = 0; k < kInFlight; ++k) {
-        if (r0 + k >= rows) break;
+        if (r0 + k >= my_rows) break;
         const int at = first + (r0 + k) * 32 + lane;
         float x[VEC];
         P::get(q[k], x);
@@ -247,28 +326,32 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
           q[k] = P::put(x);
         }
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) top = fmaxf(top, x[i]);
+        for (int i = 0; i < VEC; ++i) thread_top = fmaxf(thread_top, x[i]);
         mine[(r0 + k) * 32 + lane] = q[k];
       }
     }
   }
-  const float thread_top = top;
   const float T_in = p.temperature != nullptr ? p.temperature[n] : 1.f;
   const int k_in = p.top_k != nullptr ? p.top_k[n] : 0;
   const float p_in = p.top_p != nullptr ? p.top_p[n] : 1.f;
   const float min_p = p.min_p != nullptr ? p.min_p[n] : 0.f;
-  const bool has_min = min_p > 0.f;
-  if (has_min && threadIdx.x == 0) sh.min_log = static_cast<double>(T_in) * log(static_cast<double>(fminf(min_p, 1.f)));
+  const bool has_min = min_p > 0.f, has_k = k_in > 0 && k_in < V, has_p = p_in < 1.f;
+  const bool greedy = T_in == 0.f || k_in == 1;
+  // entries that are listed, at least: k, or as many as top-p's border is hoped among
+  const int want = greedy ? 0 : has_k ? (k_in <= kMostListed ? k_in : 0) : has_p ? kHoped : 0;
+  if (has_min && threadIdx.x == 0) {
+    const double d = static_cast<double>(T_in) * log(static_cast<double>(fminf(min_p, 1.f)));
+    const float a = static_cast<float>(d);
+    sh.min_log = make_float2(a, static_cast<float>(d - static_cast<double>(a)));
+  }
 
-  // f(value, index) of this warp's entries, all lanes together
+  // f(values, index of the first) of this warp's entries, a piece a lane, all lanes together
   auto each = [&](auto f) {
 #pragma unroll 1
-    for (int r = 0; r < rows; ++r) {
+    for (int r = 0; r < my_rows; ++r) {
       float x[VEC];
       P::get(mine[r * 32 + lane], x);
-      const int v0 = (first + r * 32 + lane) * VEC - shift;
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) f(x[i], v0 + i);
+      f(x, (first + r * 32 + lane) * VEC - shift);
     }
   };
   // Cluster barriers: after reading its peers' memory a CTA tells so (left) and
@@ -288,387 +371,620 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
   };
 
   // ---------------------------------------------------------------- maximum
-  float least = thread_top > -INFINITY ? thread_top : INFINITY;   // of the threads' maxima
+  {
+    float top = thread_top;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-    least = fminf(least, __shfl_xor_sync(kAll, least, o));
-  }
-  if (lane == 0) {
-    sh.warp_f[0][warp] = top;
-    sh.warp_f[1][warp] = least;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    float a = sh.warp_f[0][lane % kWarps], b = sh.warp_f[1][lane % kWarps];
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) {
-      a = fmaxf(a, __shfl_xor_sync(kAll, a, o));
-      b = fminf(b, __shfl_xor_sync(kAll, b, o));
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+    if (lane == 0) sh.warp_f[warp] = top;
+    if (threadIdx.x == 0) {
+      sh.at = INT32_MAX;
+      sh.told.count = 0ull;
     }
-    if (lane == 0) sh.part_f = make_float2(a, b);
+    __syncthreads();
+    top = sh.warp_f[lane % kWarps];
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+    // the first entry that equals it: of few threads, one usually
+    if (thread_top == top && top > -INFINITY) {
+      int at = INT32_MAX;
+#pragma unroll 1
+      for (int r = my_rows - 1; r >= 0; --r) {
+        float x[VEC];
+        P::get(mine[r * 32 + lane], x);
+#pragma unroll
+        for (int i = VEC - 1; i >= 0; --i) at = x[i] == top ? (first + r * 32 + lane) * VEC - shift + i : at;
+      }
+      atomicMin(&sh.at, at);
+    }
+    // The largest 16-bit start of a key that `share` threads' maxima reach: every CTA
+    // has so many entries from its own on, so together they have `want` from the least
+    // of them on, and few more.
+    uint32_t floor = 0u;
+    if (want > 0) {
+      const int share = min((want + parts - 1) / parts, kThreads);
+      const uint32_t key = key_of(thread_top) >> 16;
+#pragma unroll 1
+      for (uint32_t bit = 1u << 15; bit > 0u; bit >>= 1)
+        if (__syncthreads_count(key >= (floor | bit)) >= share) floor |= bit;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      sh.told.top = static_cast<u64>(key_of(top)) << 32 | (kAll - static_cast<uint32_t>(sh.at));
+      sh.told.floor = floor;
+    }
   }
   meet();
+  float m, flo;
+  int first_top;
   {
-    const u64 t = ld_peer_u64(&sh.part_f, lane % parts);   // parts divides 32
-    top = __uint_as_float(static_cast<uint32_t>(t));
-    least = __uint_as_float(static_cast<uint32_t>(t >> 32));
+    u64 a = ld_peer_u64(&sh.told.top, lane % parts), b = ld_peer_u64(&sh.told.floor, lane % parts);   // parts divides 32
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-      least = fminf(least, __shfl_xor_sync(kAll, least, o));
+      const u64 c = __shfl_xor_sync(kAll, a, o), d = __shfl_xor_sync(kAll, b, o);
+      a = c > a ? c : a;
+      b = d < b ? d : b;
     }
+    m = value_of(static_cast<uint32_t>(a >> 32));
+    first_top = static_cast<int>(kAll - static_cast<uint32_t>(a));
+    flo = value_of(max(static_cast<uint32_t>(b) << 16, key_of(-FLT_MAX)));
   }
-  left();
-  const float m = top;
   const bool bad = m == -INFINITY || !(T_in >= 0.f);
   float* probs = p.probs != nullptr ? p.probs + static_cast<size_t>(n) * V : nullptr;
+  Border keep{-FLT_MAX, INT32_MAX};
+  Weigh weigh;
+  weigh.set(m, greedy ? 1.f : T_in, lane);
+  u64 total = 0ull;
+  // min-p: the least float that is not below m + T ln(min_p)
+  float least = -FLT_MAX;
+  if (has_min) {
+    const float a = sh.min_log.x, t = __fadd_rn(m, a), b = __fsub_rn(t, m);   // t + e = m + a
+    const float e = __fadd_rn(__fsub_rn(m, __fsub_rn(t, b)), __fsub_rn(a, b));
+    least = fminf(__fadd_ru(t, __fadd_rn(e, sh.min_log.y)), m);
+  }
 
   // A sum over the cluster of one value a warp: what lies before this warp, and all.
   int turn = 0;
-  auto join = [&](u64 v, u64& before, u64& total) {
+  auto join = [&](u64 v, u64& before, u64& all) {
     turn ^= 1;
     if (lane == 0) sh.warp[turn][warp] = v;
     __syncthreads();
     const u64 w = lane < kWarps ? sh.warp[turn][lane] : 0ull;
-    const u64 all = warp_sum(w);
-    if (threadIdx.x == 0) sh.part[turn] = all;
+    const u64 sum = warp_sum(w);
+    if (threadIdx.x == 0) sh.part[turn] = sum;
     meet();
     const u64 t = lane < parts ? ld_peer_u64(&sh.part[turn], lane) : 0ull;
-    total = warp_sum(t);
+    all = warp_sum(t);
     before = warp_sum((lane < part ? t : 0ull) + (lane < warp ? w : 0ull));
     left();
   };
-  // The index of the r-th entry (from 1) equal to x, in every CTA.
-  auto find_tie = [&](float x, unsigned r) -> int {
-    unsigned c = 0;
-    each([&](float y, int) { c += y == x; });
-    const u64 all = __reduce_add_sync(kAll, c);
-    u64 before, total;
-    join(all, before, total);
-    if (before < r && r <= before + all) {
-      unsigned cum = static_cast<unsigned>(before);
-      int found = -1;
-#pragma unroll 1
-      for (int i = 0; i < rows && found < 0; ++i) {
-        float y[VEC];
-        P::get(mine[i * 32 + lane], y);
-        unsigned k = 0;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) k += y[j] == x;
-        const unsigned incl = static_cast<unsigned>(warp_scan(k, lane));
-        const unsigned hit = __ballot_sync(kAll, cum + incl >= r);
-        if (hit != 0u) {
-          unsigned at = cum + incl - k;
-          int v = (first + i * 32 + lane) * VEC - shift, is = -1;
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            at += y[j] == x;
-            if (is < 0 && at >= r) is = v + j;
-          }
-          found = __shfl_sync(kAll, is, __ffs(static_cast<int>(hit)) - 1);
-        }
-        cum += __shfl_sync(kAll, incl, 31);
-      }
-      settle();   // nobody reads behind the join any more
-      if (lane < parts) st_peer_u32(&sh.tie, lane, static_cast<uint32_t>(found));
-    }
-    meet();
-    return sh.tie;
-  };
-  auto clear = [&](int ints) {
-    settle();
+  // Inclusive sum over the CTA's threads.
+  auto block_scan = [&](u64 v, u64& all) -> u64 {
+    const u64 incl = warp_scan(v, lane);
     __syncthreads();
-    for (int i = threadIdx.x; i < ints / 4; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0u, 0u, 0u, 0u);
-    __syncthreads();
-  };
-  // The bin in which the running sum over the bins (of all CTAs, largest values
-  // first) reaches `need` (from 1): sh.bin, what lies above it and the entries in
-  // it (0 where not counted); false where the sum stays below.
-  auto find_bin = [&](bool mass, bool counted, u64 need) -> bool {
-    meet();
-    const int per = mass ? 2 : 4, b0 = threadIdx.x * per;
-    u64 v[4] = {0ull, 0ull, 0ull, 0ull};
-    unsigned cnt[2] = {0u, 0u};
-    if (!mass) {
-      for (int r = 0; r < parts; ++r) {
-        const uint4 c = ld_peer_v4(hist + b0, r);
-        v[0] += c.x; v[1] += c.y; v[2] += c.z; v[3] += c.w;
-      }
-    } else {
-#pragma unroll 4
-      for (int r = 0; r < parts; ++r) {
-        const u64 c = counted ? ld_peer_u64(hist + b0, r) : 0ull;
-        const u64 a0 = ld_peer_u64(hist + kMassBins + b0, r), a1 = ld_peer_u64(hist + 2 * kMassBins + b0, r),
-                  a2 = ld_peer_u64(hist + 3 * kMassBins + b0, r);
-        cnt[0] += static_cast<unsigned>(c);
-        cnt[1] += static_cast<unsigned>(c >> 32);
-        v[0] += (a0 & kAll) + ((a1 & kAll) << 14) + ((a2 & kAll) << 29);
-        v[1] += (a0 >> 32) + ((a1 >> 32) << 14) + ((a2 >> 32) << 29);
-      }
-    }
-    left();
-    const u64 own = v[0] + v[1] + v[2] + v[3];
-    u64 incl = warp_scan(own, lane);
     if (lane == 31) sh.scan[warp] = incl;
     __syncthreads();
-    u64 total = 0ull, before = 0ull;
-    {
-      const u64 w = lane < kWarps ? sh.scan[lane] : 0ull;
-      total = warp_sum(w);
-      before = warp_sum(lane < warp ? w : 0ull);
-    }
-    incl += before;
-    if (total >= need && incl - own < need && need <= incl) {
-      u64 cum = incl - own;
-      int b = 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (b == k && k + 1 < per && cum + v[k] < need) {
-          cum += v[k];
-          ++b;
-        }
-      }
-      sh.bin = b0 + b;
-      sh.above = cum;
-      sh.count = mass ? cnt[b & 1] : static_cast<unsigned>(b == 0 ? v[0] : b == 1 ? v[1] : b == 2 ? v[2] : v[3]);
-    }
-    __syncthreads();
-    return total >= need;
+    const u64 w = lane < kWarps ? sh.scan[lane] : 0ull;
+    all = warp_sum(w);
+    return incl + warp_sum(lane < warp ? w : 0ull);
   };
-  // Linear bins of 2^-s below m, and the range of keys of one of them: with the
-  // difference rounded down and b 2^-s exact, entry x is in bin b just where
-  // m - (b + 1) 2^-s < x <= m - b 2^-s.
-  auto linear_scale = [&](float lowest, int bins) -> float {
-    const float range = fminf(__fsub_ru(m, lowest), FLT_MAX);
-    const int e = range > 0.f ? max(ilogbf(range) + 1, -100) : -100;   // a difference rounded down is below 2^e
-    return ldexpf(static_cast<float>(bins), -e);                       // bins is a power of two
-  };
-  auto linear_bin = [&](float x, float scale) { return __float2uint_rz(__fsub_rd(m, x) * scale); };
-  auto linear_edge = [&](int b, float scale) { return __fsub_rd(m, static_cast<float>(b) / scale); };   // exact quotient
 
-  Border keep{-FLT_MAX, INT32_MAX};
-  const bool greedy = T_in == 0.f || k_in == 1;
-  Weigh weigh;
-  weigh.set(m, greedy ? 1.f : T_in, lane);
-  int token = 0;
-  u64 total = 0ull;
-  if (bad) {
-    if (part == 0 && threadIdx.x == 0) report(p.dev_status, DFLASH_ERR_INVALID_ARG);
-    keep = Border{FLT_MAX, -1};   // nothing stays
-  } else if (greedy) {
-    token = find_tie(m, 1u);
-    keep = Border{m, token};
-    total = 1ull << kOne;
-  } else {
-    // -------------------------------------------------------------- top-k
-    if (k_in > 1 && k_in < V) {
-      u64 need = static_cast<u64>(k_in);
-      uint32_t lo = key_of(-FLT_MAX), hi = key_of(m);
-      float scale = 0.f;
-      // k threads have a maximum in or above this bin
-      if (k_in <= parts * kThreads) {
-        scale = linear_scale(least, kCountBins);
-        clear(kCountBins);
-        const unsigned b = linear_bin(thread_top, scale);
-        if (b < kCountBins) atomicAdd(&hist[b], 1u);
-        const bool found = find_bin(false, true, need);
-        if (found) lo = max(lo, key_of(linear_edge(static_cast<int>(sh.bin) + 1, scale)) + 1u);
-        scale = found ? linear_scale(value_of(lo), kCountBins) : 0.f;
-      }
-      while (true) {
-        const float flo = value_of(lo), fhi = value_of(hi);
-        const uint32_t range = hi - lo;
-        int step = max(0, 32 - __clz(range) - 11);
-        if (step <= P::kFinal) step = P::kFinal;
-        const bool linear = scale > 0.f;
-        clear(kCountBins);
-        each([&](float x, int) {
-          if (x >= flo && x <= fhi) {
-            const unsigned b = linear ? linear_bin(x, scale) : (hi - key_of(x)) >> step;
-            if (b < kCountBins) atomicAdd(&hist[b], 1u);
-          }
-        });
-        if (!find_bin(false, true, need)) break;        // fewer finite entries than k: all stay
-        need -= sh.above;
-        const unsigned bin = sh.bin, count = sh.count;
-        uint32_t next_lo, next_hi;
-        if (linear) {
-          next_hi = min(hi, key_of(linear_edge(static_cast<int>(bin), scale)));
-          next_lo = max(lo, key_of(linear_edge(static_cast<int>(bin) + 1, scale)) + 1u);
-        } else {
-          next_hi = hi - (bin << step);
-          next_lo = max(lo, next_hi - ((1u << step) - 1u));
-        }
-        if (need == count) {
-          keep.thr = value_of(next_lo);
-          break;
-        }
-        if (!linear && step == P::kFinal) {             // one value
-          keep.thr = value_of(P::at_or_below(next_hi));
-          keep.cut = find_tie(keep.thr, static_cast<unsigned>(need));
-          break;
-        }
-        lo = next_lo;
-        hi = next_hi;
-        scale = 0.f;
-      }
+  if (bad || greedy) {
+    if (part == 0 && threadIdx.x == 0) {
+      if (bad) report(p.dev_status, DFLASH_ERR_INVALID_ARG);
+      if (p.tokens != nullptr) p.tokens[n] = bad ? 0 : first_top;
     }
-    // -------------------------------------------------------------- top-p
-    if (p_in < 1.f) {
-      const Border from = keep;
-      // entries below weigh less than 1 - p together, the largest alone weighs 1
-      const float y0 = log2f(static_cast<float>(V) / (1.f - fmaxf(p_in, 0.f))) + 0.25f;
-      float cut = fmaxf(__fsub_rd(m, y0 / weigh.ch * 1.0001f), -FLT_MAX);
-      cut = fmaxf(cut, from.thr);
-      uint32_t lo = key_of(cut), hi = key_of(m);
-      float scale = linear_scale(cut, kMassBins);
-      u64 need = 0ull, base = 0ull;
-      bool once = true;
-      while (true) {
-        const float flo = value_of(lo), fhi = value_of(hi);
-        const uint32_t range = hi - lo;
-        int step = max(0, 32 - __clz(range) - 10);
-        if (step <= P::kFinal) step = P::kFinal;
-        const bool linear = once;
-        clear(kHistInts);
-        u64 sum = 0ull;
-        each([&](float x, int v) {
-          const bool in = once ? from.keeps(x, v) : x >= flo && x <= fhi && from.keeps(x, v);
-          if (__any_sync(kAll, in)) {
-            const u64 w = weigh(x);
-            if (in) {
-              sum += w;
-              if (x >= flo) {
-                const unsigned b = linear ? linear_bin(x, scale) : (hi - key_of(x)) >> step;
-                if (b < kMassBins) {
-                  if (!once) atomicAdd(&hist[b], 1u);
-                  atomicAdd(&hist[kMassBins + b], static_cast<unsigned>(w) & 0x3FFFu);
-                  atomicAdd(&hist[2 * kMassBins + b], static_cast<unsigned>(w >> 14) & 0x7FFFu);
-                  atomicAdd(&hist[3 * kMassBins + b], static_cast<unsigned>(w >> 29));
+    left();
+    keep = bad ? Border{FLT_MAX, -1} : Border{m, first_top};   // nothing, or the one
+    total = weigh(m);
+  } else {
+    bool found = false;                // the border, through the list
+    u64 Z = 0ull;                      // the weight of all, where top-p has no top-k before it
+    if (want > 0) {
+      // -------------------------------------------------------------- few candidates
+      // Entries from flo on go to the CTA's list, all CTAs' lists to the first one, which
+      // sorts them and knows everything but the weight of the rest.
+      const bool all_weigh = !has_k;
+      u64 sum = 0ull, above = 0ull;
+      unsigned* count = reinterpret_cast<unsigned*>(&sh.told.count);
+      each([&](const float* x, int v0) {
+        u64 w[VEC];
+        if (all_weigh) {
+#pragma unroll
+          for (int i = 0; i < VEC; i += 2) weigh.two(x[i], x[i + 1], w[i], w[i + 1]);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) sum += w[i];
+        }
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          if (x[i] >= flo) {
+            if (all_weigh) above += w[i];
+            const unsigned at = atomicAdd(count, 1u);
+            if (at < kOwnList) own[at] = static_cast<u64>(~key_of(x[i])) << 32 | static_cast<uint32_t>(v0 + i);
+          }
+        }
+      });
+      if (all_weigh) {
+        sum = warp_sum(sum);
+        above = warp_sum(above);
+        if (lane == 0) {
+          sh.warp[0][warp] = sum;
+          sh.warp[1][warp] = above;
+        }
+        __syncthreads();
+        if (warp == 0) {
+          const u64 a = warp_sum(lane < kWarps ? sh.warp[0][lane] : 0ull), b = warp_sum(lane < kWarps ? sh.warp[1][lane] : 0ull);
+          if (lane == 0) {
+            sh.told.sum = a;
+            sh.told.listed = b;
+          }
+        }
+      }
+      meet();
+      const u64 c = lane < parts ? ld_peer_u64(&sh.told.count, lane) : 0ull;
+      unsigned len = __reduce_add_sync(kAll, static_cast<unsigned>(c));
+      found = len <= kList && __reduce_max_sync(kAll, static_cast<unsigned>(c)) <= kOwnList;
+      u64 need = ~0ull;
+      if (all_weigh) {
+        Z = warp_sum(lane < parts ? ld_peer_u64(&sh.told.sum, lane) : 0ull);
+        const u64 has = warp_sum(lane < parts ? ld_peer_u64(&sh.told.listed, lane) : 0ull);
+        need = draw_ceil(p_in, Z);
+        found = found && has >= need;
+      }
+      if (found && part == 0) {
+        // entry i of the joint list lies in the list of the CTA that the counts tell
+        const unsigned incl = static_cast<unsigned>(warp_scan(c, lane));
+        for (unsigned i0 = warp * 32; i0 < kList; i0 += kThreads) {
+          const unsigned i = i0 + lane;
+          unsigned from = 0u, before = 0u;
+          for (int r = 0; r < parts; ++r) {
+            const unsigned e = __shfl_sync(kAll, incl, r);
+            if (i >= e) {
+              from = r + 1;
+              before = e;
+            }
+          }
+          list[i] = i < len ? ld_peer_u64(own + (i - before), from) : ~0ull;
+        }
+      }
+      left();
+      if (found && part == 0) {
+        // larger values first, equal ones by index
+        auto sort = [&](auto* v, int len) {   // ascending; what is behind len is larger than all
+          int size = 32;
+          while (size < len) size *= 2;
+          __syncthreads();
+          for (int k = 2; k <= size; k *= 2)
+            for (int j = k / 2; j > 0; j /= 2) {
+              for (int i = threadIdx.x; i < size / 2; i += kThreads) {
+                const int a = 2 * i - (i & (j - 1)), b = a + j;
+                const auto x = v[a], y = v[b];
+                if ((x > y) == ((a & k) == 0)) {
+                  v[a] = y;
+                  v[b] = x;
+                }
+              }
+              __syncthreads();
+            }
+        };
+        sort(list, static_cast<int>(len));
+        // a thread's entries: PER neighbouring ones
+        constexpr int PER = kList / kThreads;
+        static_assert(PER == 4, "the draw picks one of four");
+        const int kept = has_k ? min(k_in, static_cast<int>(len)) : static_cast<int>(len);
+        u64 w[PER], mass = 0ull;
+        float x[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) x[i] = value_of(~static_cast<uint32_t>(list[PER * threadIdx.x + i] >> 32));
+#pragma unroll
+        for (int i = 0; i < PER; i += 2) weigh.two(fminf(x[i], m), fminf(x[i + 1], m), w[i], w[i + 1]);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          if (PER * static_cast<int>(threadIdx.x) + i >= kept) w[i] = 0ull;
+          mass += w[i];
+        }
+        u64 all, incl = block_scan(mass, all);
+        if (has_k && has_p) need = draw_ceil(p_in, all);
+        // the first of the sorted entries that stays out
+        int stay = 0;
+        u64 before = incl - mass;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int at = PER * threadIdx.x + i;
+          stay += at < kept && (at == 0 || ((!has_p || before < need) && x[i] >= least));
+          before += w[i];
+        }
+        __syncthreads();
+        stay = static_cast<int>(__reduce_add_sync(kAll, static_cast<unsigned>(stay)));
+        if (lane == 0) sh.scan[warp] = stay;
+        __syncthreads();
+        stay = static_cast<int>(warp_sum(lane < kWarps ? sh.scan[lane] : 0ull));
+        __syncthreads();
+        // their weight, and the entry at the border
+        const int last = stay - 1;
+        if (static_cast<int>(threadIdx.x) == last / PER) {
+          before = incl - mass;
+#pragma unroll
+          for (int i = 0; i < PER; ++i)
+            if (i <= last % PER) before += w[i];
+          sh.total = before;
+          const u64 e = list[last];
+          sh.border = Border{value_of(~static_cast<uint32_t>(e >> 32)), static_cast<int>(static_cast<uint32_t>(e))};
+        }
+        unsigned places[PER];   // index << 11 | place: kept ones are sorted by their index
+        static_assert(kList <= 2048 && kDrawMaxVocab <= 1 << 20, "bits of an index and a place");
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          places[i] = static_cast<uint32_t>(list[PER * threadIdx.x + i]) << 11 | (PER * threadIdx.x + i);
+        __syncthreads();
+        total = sh.total;
+        if (p.tokens != nullptr) {
+          bool whole;
+          const u64 thr = draw_threshold(p.u[n], total, whole);
+          unsigned* order = reinterpret_cast<unsigned*>(own);   // 2048 words
+          u64* weight = list;
+#pragma unroll
+          for (int i = 0; i < PER; ++i) {
+            const int at = PER * threadIdx.x + i;
+            weight[at] = w[i];
+            order[at] = at < stay ? places[i] : kAll;
+          }
+          sort(order, stay);
+          mass = 0ull;
+#pragma unroll
+          for (int i = 0; i < PER; ++i) {
+            places[i] = order[PER * threadIdx.x + i];
+            w[i] = PER * static_cast<int>(threadIdx.x) + i < stay ? weight[places[i] & 2047u] : 0ull;
+            mass += w[i];
+          }
+          incl = block_scan(mass, all);
+          if (incl > thr && incl - mass <= thr) {   // one thread
+            u64 c2 = incl - mass;
+            int k = 0;
+#pragma unroll
+            for (int i = 0; i < PER - 1; ++i) {
+              c2 += w[i];
+              k += c2 <= thr;
+            }
+            p.tokens[n] = static_cast<int>((k == 0 ? places[0] : k == 1 ? places[1] : k == 2 ? places[2] : places[3]) >> 11);
+          }
+        }
+        if (probs != nullptr && threadIdx.x < parts) {
+          const u64 b = static_cast<u64>(static_cast<uint32_t>(sh.border.cut)) << 32 | __float_as_uint(sh.border.thr);
+          st_peer_u64(&sh.border, threadIdx.x, b);
+          st_peer_u64(&sh.total, threadIdx.x, sh.total);
+        }
+      }
+      if (found && probs != nullptr) {
+        meet();
+        keep = sh.border;
+        total = sh.total;
+      }
+    } else {
+      left();
+    }
+    if (!found) {
+      // -------------------------------------------------------------- many candidates
+      // The index of the r-th entry (from 1) equal to x, in every CTA.
+      auto find_tie = [&](float x, unsigned r) -> int {
+        unsigned c = 0;
+        each([&](const float* y, int) {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) c += y[i] == x;
+        });
+        const u64 all = __reduce_add_sync(kAll, c);
+        u64 before, sum;
+        join(all, before, sum);
+        if (before < r && r <= before + all) {
+          unsigned cum = static_cast<unsigned>(before);
+          int at = -1;
+#pragma unroll 1
+          for (int i = 0; i < my_rows && at < 0; ++i) {
+            float y[VEC];
+            P::get(mine[i * 32 + lane], y);
+            unsigned k = 0;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) k += y[j] == x;
+            const unsigned incl = static_cast<unsigned>(warp_scan(k, lane));
+            const unsigned hit = __ballot_sync(kAll, cum + incl >= r);
+            if (hit != 0u) {
+              unsigned e = cum + incl - k;
+              int is = -1;
+#pragma unroll
+              for (int j = 0; j < VEC; ++j) {
+                e += y[j] == x;
+                if (is < 0 && e >= r) is = (first + i * 32 + lane) * VEC - shift + j;
+              }
+              at = __shfl_sync(kAll, is, __ffs(static_cast<int>(hit)) - 1);
+            }
+            cum += __shfl_sync(kAll, incl, 31);
+          }
+          if (lane < parts) st_peer_u32(&sh.tie, lane, static_cast<uint32_t>(at));
+        }
+        meet();
+        return sh.tie;
+      };
+      auto clear = [&](int ints) {
+        settle();
+        __syncthreads();
+        for (int i = threadIdx.x; i < ints / 4; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0u, 0u, 0u, 0u);
+        __syncthreads();
+      };
+      // The bin in which the running sum over the bins (of all CTAs, largest values
+      // first) reaches `need` (from 1): sh.bin, what lies above it and the entries in
+      // it (0 where not counted); false where the sum stays below.
+      auto find_bin = [&](bool mass, bool counted, u64 need) -> bool {
+        meet();
+        const int per = mass ? 2 : 4, b0 = threadIdx.x * per;
+        u64 v[4] = {0ull, 0ull, 0ull, 0ull};
+        unsigned cnt[2] = {0u, 0u};
+        for (int r0 = 0; r0 < parts; r0 += 4) {   // four CTAs' bins in flight
+          if (!mass) {
+            uint4 c[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) c[k] = r0 + k < parts ? ld_peer_v4(hist + b0, r0 + k) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              v[0] += c[k].x; v[1] += c[k].y; v[2] += c[k].z; v[3] += c[k].w;
+            }
+          } else {
+            u64 c[4], a0[4], a1[4], a2[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const bool in = r0 + k < parts;
+              c[k] = in && counted ? ld_peer_u64(hist + b0, r0 + k) : 0ull;
+              a0[k] = in ? ld_peer_u64(hist + kMassBins + b0, r0 + k) : 0ull;
+              a1[k] = in ? ld_peer_u64(hist + 2 * kMassBins + b0, r0 + k) : 0ull;
+              a2[k] = in ? ld_peer_u64(hist + 3 * kMassBins + b0, r0 + k) : 0ull;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              cnt[0] += static_cast<unsigned>(c[k]);
+              cnt[1] += static_cast<unsigned>(c[k] >> 32);
+              v[0] += (a0[k] & kAll) + ((a1[k] & kAll) << 14) + ((a2[k] & kAll) << 29);
+              v[1] += (a0[k] >> 32) + ((a1[k] >> 32) << 14) + ((a2[k] >> 32) << 29);
+            }
+          }
+        }
+        left();
+        const u64 own_sum = v[0] + v[1] + v[2] + v[3];
+        u64 all;
+        const u64 incl = block_scan(own_sum, all);
+        if (all >= need && incl - own_sum < need && need <= incl) {
+          u64 cum = incl - own_sum;
+          int b = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (b == k && k + 1 < per && cum + v[k] < need) {
+              cum += v[k];
+              ++b;
+            }
+          }
+          sh.bin = b0 + b;
+          sh.above = cum;
+          sh.count = mass ? cnt[b & 1] : static_cast<unsigned>(b == 0 ? v[0] : b == 1 ? v[1] : b == 2 ? v[2] : v[3]);
+        }
+        __syncthreads();
+        return all >= need;
+      };
+      // Linear bins of 2^-s below m, and the range of keys of one of them: with the
+      // difference rounded down and b 2^-s exact, entry x is in bin b just where
+      // m - (b + 1) 2^-s < x <= m - b 2^-s.
+      auto linear_scale = [&](float lowest, int bins) -> float {
+        const float range = fminf(__fsub_ru(m, lowest), FLT_MAX);
+        const int e = range > 0.f ? max(ilogbf(range) + 1, -100) : -100;   // a difference rounded down is below 2^e
+        return ldexpf(static_cast<float>(bins), -e);                       // bins is a power of two
+      };
+      auto linear_bin = [&](float x, float scale) { return __float2uint_rz(__fsub_rd(m, x) * scale); };
+      auto linear_edge = [&](int b, float scale) { return __fsub_rd(m, static_cast<float>(b) / scale); };   // exact quotient
+      // The keys of a bin, inside lo .. hi.
+      auto narrow = [&](bool linear, float scale, int step, uint32_t& lo, uint32_t& hi) {
+        const unsigned bin = sh.bin;
+        if (linear) {
+          hi = min(hi, key_of(linear_edge(static_cast<int>(bin), scale)));
+          lo = max(lo, key_of(linear_edge(static_cast<int>(bin) + 1, scale)) + 1u);
+        } else {
+          hi -= bin << step;
+          lo = max(lo, hi - ((1u << step) - 1u));
+        }
+      };
+      // top-k: levels of counts
+      if (has_k) {
+        u64 need = static_cast<u64>(k_in);
+        uint32_t lo = key_of(-FLT_MAX), hi = key_of(m);
+        while (true) {
+          const float a = value_of(lo), b = value_of(hi);
+          int step = max(0, 32 - __clz(hi - lo) - 11);
+          if (step <= P::kFinal) step = P::kFinal;
+          clear(kCountBins);
+          each([&](const float* x, int) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+              const unsigned bin = (hi - key_of(x[i])) >> step;
+              if (x[i] >= a && x[i] <= b && bin < kCountBins) atomicAdd(&hist[bin], 1u);
+            }
+          });
+          if (!find_bin(false, true, need)) break;        // fewer finite entries than k: all stay
+          need -= sh.above;
+          const unsigned count = sh.count;
+          narrow(false, 0.f, step, lo, hi);
+          if (need == count) {
+            keep.thr = value_of(lo);
+            break;
+          }
+          if (step == P::kFinal) {                        // one value
+            keep.thr = value_of(P::at_or_below(hi));
+            keep.cut = find_tie(keep.thr, static_cast<unsigned>(need));
+            break;
+          }
+        }
+      }
+      // top-p: levels of weights
+      if (has_p) {
+        const Border from = keep;
+        if (has_k) {
+          u64 sum = 0ull, before;
+          each([&](const float* x, int v0) {
+            bool any = false;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) any = any || from.keeps(x[i], v0 + i);
+            if (__any_sync(kAll, any)) {
+#pragma unroll
+              for (int i = 0; i < VEC; i += 2) {
+                u64 a, b;
+                weigh.two(x[i], x[i + 1], a, b);
+                sum += (from.keeps(x[i], v0 + i) ? a : 0ull) + (from.keeps(x[i + 1], v0 + i + 1) ? b : 0ull);
+              }
+            }
+          });
+          join(warp_sum(sum), before, Z);
+        }
+        const u64 need = draw_ceil(p_in, Z);
+        // entries below this one weigh less than 1 - p of all together
+        const float y0 = log2f(static_cast<float>(V) / ((1.f - fmaxf(p_in, 0.f)) * __ull2float_rn(Z))) + kOne + 0.25f;
+        const float c1 = 1.442695f / fminf(fmaxf(T_in, 0x1p-100f), 0x1p100f);
+        const float cut = fmaxf(fmaxf(__fsub_rd(m, y0 / c1 * 1.0001f), -FLT_MAX), from.thr);
+        uint32_t lo = key_of(cut), hi = key_of(m);
+        const float scale = linear_scale(cut, kMassBins);
+        u64 under = 0ull;   // the weight above the range
+        bool linear = true;
+        while (true) {
+          const float a = value_of(lo), b = value_of(hi);
+          int step = max(0, 32 - __clz(hi - lo) - 10);
+          if (step <= P::kFinal) step = P::kFinal;
+          clear(kHistInts);
+          each([&](const float* x, int v0) {
+            bool any = false;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) any = any || (x[i] >= a && x[i] <= b);
+            if (__any_sync(kAll, any)) {
+              u64 w[VEC];
+#pragma unroll
+              for (int i = 0; i < VEC; i += 2) weigh.two(x[i], x[i + 1], w[i], w[i + 1]);
+#pragma unroll
+              for (int i = 0; i < VEC; ++i) {
+                const unsigned bin = linear ? linear_bin(x[i], scale) : (hi - key_of(x[i])) >> step;
+                if (x[i] >= a && x[i] <= b && from.keeps(x[i], v0 + i) && bin < kMassBins) {
+                  if (!linear) atomicAdd(&hist[bin], 1u);
+                  atomicAdd(&hist[kMassBins + bin], static_cast<unsigned>(w[i]) & 0x3FFFu);
+                  atomicAdd(&hist[2 * kMassBins + bin], static_cast<unsigned>(w[i] >> 14) & 0x7FFFu);
+                  atomicAdd(&hist[3 * kMassBins + bin], static_cast<unsigned>(w[i] >> 29));
                 }
               }
             }
-          }
-        });
-        if (once) {   // the weight of all that top-k left, and how much of it has to lie up to the border
-          u64 before, all;
-          join(warp_sum(sum), before, all);
-          bool whole;
-          need = draw_threshold(fmaxf(p_in, 0.f), all, whole);
-          if (!whole || need == 0ull) ++need;
-        }
-        if (!find_bin(true, !once, need - base)) break;    // not reached: rounding of the cut; all stay
-        base += sh.above;
-        const unsigned bin = sh.bin, count = sh.count;
-        uint32_t next_lo, next_hi;
-        if (linear) {
-          next_hi = min(hi, key_of(linear_edge(static_cast<int>(bin), scale)));
-          next_lo = max(lo, key_of(linear_edge(static_cast<int>(bin) + 1, scale)) + 1u);
-        } else {
-          next_hi = hi - (bin << step);
-          next_lo = max(lo, next_hi - ((1u << step) - 1u));
-        }
-        if (!once && count == 1u) {
-          const float x = value_of(next_lo);
-          keep = x <= from.thr ? from : Border{x, INT32_MAX};
-          break;
-        }
-        if (!linear && step == P::kFinal) {                // one value
-          const float x = value_of(P::at_or_below(next_hi));
-          const u64 w = weigh(x), left_over = need - base;   // w > 0: the sum reaches past `base` in this bin
-          const u64 r = (left_over + w - 1ull) / w;
-          if (r < count) keep = Border{x, find_tie(x, static_cast<unsigned>(r))};
-          else keep = x == from.thr ? from : Border{x, INT32_MAX};
-          break;
-        }
-        lo = next_lo;
-        hi = next_hi;
-        once = false;
-      }
-    }
-    // -------------------------------------------------------------- min-p
-    if (has_min) {
-      const float x = fminf(__double2float_ru(static_cast<double>(m) + sh.min_log), m);
-      if (x > keep.thr) keep = Border{x, INT32_MAX};
-    }
-    // -------------------------------------------------------------- draw
-    u64 sum = 0ull;
-    each([&](float x, int v) {
-      const bool in = keep.keeps(x, v);
-      if (__any_sync(kAll, in)) {
-        const u64 w = weigh(x);
-        if (in) sum += w;
-      }
-    });
-    sum = warp_sum(sum);
-    u64 cum;
-    join(sum, cum, total);
-    if (p.tokens != nullptr) {
-      bool whole;
-      const u64 thr = draw_threshold(p.u[n], total, whole);
-      if (cum <= thr && thr - cum < sum) {   // one warp of the cluster
-#pragma unroll 1
-        for (int r = 0; r < rows; ++r) {
-          float x[VEC];
-          P::get(mine[r * 32 + lane], x);
-          const int v0 = (first + r * 32 + lane) * VEC - shift;
-          u64 w[VEC], own = 0ull;
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            const u64 t = weigh(x[i]);
-            w[i] = keep.keeps(x[i], v0 + i) ? t : 0ull;
-            own += w[i];
-          }
-          const u64 incl = warp_scan(own, lane);
-          const unsigned hit = __ballot_sync(kAll, cum + incl > thr);
-          if (hit != 0u) {
-            u64 c = cum + incl - own;
-            int k = 0;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-              c += w[i];
-              k += c <= thr;
-            }
-            token = __shfl_sync(kAll, v0 + k, __ffs(static_cast<int>(hit)) - 1);
-            if (lane == 0) p.tokens[n] = token;
+          });
+          if (!find_bin(true, !linear, need - under)) break;   // cannot be: everything below the cut would be needed
+          under += sh.above;
+          const unsigned count = sh.count;
+          narrow(linear, scale, step, lo, hi);
+          if (!linear && count == 1u) {
+            const float x = value_of(lo);
+            keep = x <= from.thr ? from : Border{x, INT32_MAX};
             break;
           }
-          cum += __shfl_sync(kAll, incl, 31);
+          if (!linear && step == P::kFinal) {                  // one value
+            const float x = value_of(P::at_or_below(hi));
+            const u64 w = weigh(x);                            // above 0: the sum grows in this bin
+            const u64 r = (need - under + w - 1ull) / w;
+            if (r < count) keep = Border{x, find_tie(x, static_cast<unsigned>(r))};
+            else keep = x == from.thr ? from : Border{x, INT32_MAX};
+            break;
+          }
+          linear = false;
+        }
+      }
+      if (least > keep.thr) keep = Border{least, INT32_MAX};
+      // the draw: every warp's kept weight, then the warp whose range holds the threshold
+      u64 sum = 0ull, cum;
+      each([&](const float* x, int v0) {
+        bool any = false;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) any = any || keep.keeps(x[i], v0 + i);
+        if (__any_sync(kAll, any)) {
+#pragma unroll
+          for (int i = 0; i < VEC; i += 2) {
+            u64 a, b;
+            weigh.two(x[i], x[i + 1], a, b);
+            sum += (keep.keeps(x[i], v0 + i) ? a : 0ull) + (keep.keeps(x[i + 1], v0 + i + 1) ? b : 0ull);
+          }
+        }
+      });
+      sum = warp_sum(sum);
+      join(sum, cum, total);
+      if (p.tokens != nullptr) {
+        bool whole;
+        const u64 thr = draw_threshold(p.u[n], total, whole);
+        if (cum <= thr && thr - cum < sum) {   // one warp of the cluster
+#pragma unroll 1
+          for (int r = 0; r < my_rows; ++r) {
+            float x[VEC];
+            P::get(mine[r * 32 + lane], x);
+            const int v0 = (first + r * 32 + lane) * VEC - shift;
+            u64 w[VEC], own_sum = 0ull;
+#pragma unroll
+            for (int i = 0; i < VEC; i += 2) weigh.two(x[i], x[i + 1], w[i], w[i + 1]);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+              if (!keep.keeps(x[i], v0 + i)) w[i] = 0ull;
+              own_sum += w[i];
+            }
+            const u64 incl = warp_scan(own_sum, lane);
+            const unsigned hit = __ballot_sync(kAll, cum + incl > thr);
+            if (hit != 0u) {
+              u64 c = cum + incl - own_sum;
+              int k = 0;
+#pragma unroll
+              for (int i = 0; i < VEC; ++i) {
+                c += w[i];
+                k += c <= thr;
+              }
+              const int token = __shfl_sync(kAll, v0 + k, __ffs(static_cast<int>(hit)) - 1);
+              if (lane == 0) p.tokens[n] = token;
+              break;
+            }
+            cum += __shfl_sync(kAll, incl, 31);
+          }
         }
       }
     }
   }
-  if ((bad || greedy) && p.tokens != nullptr && part == 0 && threadIdx.x == 0) p.tokens[n] = token;
   // ---------------------------------------------------------------- distribution
   if (probs != nullptr) {
-    const float inv = total > 0ull ? 1.f / __ull2float_rn(total) : 0.f;
+    // 1 / total in two floats, so that a probability is rounded twice: as a weight, and here
+    const float t = __ull2float_rn(total), inv = total > 0ull ? __fdiv_rn(1.f, t) : 0.f;
+    const float rest = static_cast<float>(static_cast<long long>(total - static_cast<u64>(t)));
+    const float low = inv * __fmaf_rn(-inv, rest, __fmaf_rn(-inv, t, 1.f));
+    auto share = [&](u64 w) {
+      const float x = __ull2float_rn(w);
+      return __fmaf_rn(x, inv, x * low);
+    };
     float* out = probs - shift;
     const bool aligned = (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
-#pragma unroll 1
-    for (int r = 0; r < rows; ++r) {
-      const int at = first + r * 32 + lane, v0 = at * VEC - shift;
-      float x[VEC], y[VEC];
-      P::get(mine[r * 32 + lane], x);
+    each([&](const float* x, int v0) {
+      float y[VEC];
+      bool any = false;
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        const bool in = keep.keeps(x[i], v0 + i);
         y[i] = 0.f;
-        if (__any_sync(kAll, in)) {
-          const u64 w = weigh(x[i]);
-          if (in) y[i] = __ull2float_rn(w) * inv;
+        any = any || keep.keeps(x[i], v0 + i);
+      }
+      if (__any_sync(kAll, any)) {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) {
+          u64 a, b;
+          weigh.two(x[i], x[i + 1], a, b);
+          if (keep.keeps(x[i], v0 + i)) y[i] = share(a);
+          if (keep.keeps(x[i + 1], v0 + i + 1)) y[i + 1] = share(b);
         }
       }
       if (aligned && v0 >= 0 && v0 + VEC <= V) {
 #pragma unroll
-        for (int i = 0; i < VEC; i += 4)
-          __stcs(reinterpret_cast<float4*>(out + at * VEC + i), make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]));
+        for (int i = 0; i < VEC; i += 4) __stcs(reinterpret_cast<float4*>(probs + v0 + i), make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]));
       } else {
 #pragma unroll
         for (int i = 0; i < VEC; ++i)
           if (v0 + i >= 0 && v0 + i < V) probs[v0 + i] = y[i];
       }
-    }
+    });
   }
   settle();   // no peer reads this CTA's memory any more
 }
@@ -687,14 +1003,16 @@ cudaError_t launch_typed(const DrawArgs& a, cudaStream_t s, bool pdl) {
   }
   constexpr int VEC = Pack<TT>::N;
   const int pieces = (a.V + 2 * VEC - 2) / VEC;          // whatever the row's alignment
-  auto rows_of = [&](int parts) { return (pieces + parts * kThreads - 1) / (parts * kThreads); };
+  const int all_rows = (pieces + 31) / 32;
+  auto rows_of = [&](int parts) { return (all_rows + parts * kWarps - 1) / (parts * kWarps); };
   // CTAs a row: as many as leave two of them room in an SM's shared memory (ten rows of
-  // 16-byte pieces a warp, 80 KB), and more while they leave SMs idle and have two rows each.
+  // 16-byte pieces a warp, 80 KB), and more while they leave SMs idle and have two rows
+  // each. Clusters of 16 find no room beside one another: only for a few rows.
   int parts = 1;
   while (parts < kMaxParts && rows_of(parts) > 10) parts *= 2;
-  while (parts < kMaxParts && 2LL * parts * a.N <= 2LL * num_sms_of_current_device() && rows_of(parts) > 2) parts *= 2;
+  while (parts < (a.N <= 4 ? kMaxParts : 8) && 2LL * parts * a.N <= 2LL * num_sms_of_current_device() && rows_of(parts) > 2) parts *= 2;
   const int rows = rows_of(parts);
-  const size_t smem = static_cast<size_t>(rows) * kWarps * 32 * 16 + kHistInts * sizeof(unsigned);
+  const size_t smem = static_cast<size_t>(rows) * kWarps * 32 * 16 + kScratchBytes;
   if (smem > kMaxSmem) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.N) * parts);

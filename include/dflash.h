@@ -669,7 +669,7 @@ dflash_status dflash_attention_tree_paged(const dflash_heads* heads, const void*
  * -inf and NaN logits have no weight; +inf counts as the largest finite number.
  *   A row of nothing else, and a temperature that is negative or NaN, set
  *   DFLASH_ERR_INVALID_ARG in dev_status and give token 0 and a row of zeros.
- * Weights are exact to 2^-30 and summed as integers (multiples of 2^-43 of the
+ * Weights are computed to 2^-27 and summed as integers (multiples of 2^-43 of the
  *   largest): no result depends on an order of summation.
  * Rows may begin at any element and lie at any stride ld >= V (those whose
  *   addresses are multiples of 16 bytes are a little faster to write).
