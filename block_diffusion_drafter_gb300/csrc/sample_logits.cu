@@ -41,26 +41,28 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxParts = 16;
 constexpr int kCountBins = 2048, kMassBins = 1024;
 constexpr int kHistInts = 4096;      // 16 KB: counts, or counts and three parts of a weight
-constexpr int kOwnList = 1024, kList = 2048;   // candidates of a CTA and of a row: 24 KB
+constexpr int kList = 2048;          // candidates of a CTA, and of a row: 32 KB
 constexpr int kMostListed = 1280;    // top-k borders that the list is made for
-constexpr int kHoped = 640;          // candidates among which top-p's border is looked for first
-constexpr int kScratchBytes = (kOwnList + kList) * 8;   // the lists, or the histograms
-constexpr int kInFlight = 5;         // 16-byte loads a thread
+constexpr int kHoped = 128, kHopedMost = 1280;   // candidates among which top-p's border is looked for, and then
+constexpr int kCounted = 512;        // candidates whose ranks are counted; more are sorted
+constexpr int kScratchBytes = 2 * kList * 8;   // the lists, or the histograms
+constexpr int kInFlight = 5;         // 16-byte loads a thread, first pass
+constexpr int kAgain = 2;            // and later ones
 constexpr int kOne = 43;             // the largest weight is 2^43
 typedef unsigned long long u64;
 constexpr unsigned kAll = 0xffffffffu;
 
 // 2^(j/32), j = 0 .. 31 (from the exponential's definition): the largest float not
-// above it, and the rest times 2^36.
+// above it, and the relative rest.
 __device__ const float kPow2[32][2] = {
-    {1.0f, 0.0f}, {1.0218970775604248f, 4885.521484375f}, {1.0442737340927124f, 3321.535400390625f}, {1.0671403408050537f, 4114.35693359375f},
-    {1.0905076265335083f, 7293.318359375f}, {1.1143866777420044f, 4456.72509765625f}, {1.1387885808944702f, 3701.3837890625f}, {1.1637247800827026f, 5407.87060546875f},
-    {1.1892070770263672f, 2609.715087890625f}, {1.2152472734451294f, 5946.6630859375f}, {1.2418577671051025f, 3090.20361328125f}, {1.2690509557724f, 97.53584289550781f},
-    {1.2968394756317139f, 5430.16455078125f}, {1.3252365589141846f, 5789.310546875f}, {1.3542554378509521f, 7496.32861328125f}, {1.383909821510315f, 4154.333984375f},
-    {1.4142135381698608f, 1663.233642578125f}, {1.4451807737350464f, 2284.372802734375f}, {1.4768260717391968f, 5099.005859375f}, {1.5091643333435059f, 6476.80517578125f},
-    {1.5422108173370361f, 554.6283569335938f}, {1.57598078250885f, 4301.77294921875f}, {1.610490322113037f, 675.939697265625f}, {1.645755410194397f, 4670.14599609375f},
-    {1.6817927360534668f, 6490.82666015625f}, {1.7186192274093628f, 4859.3681640625f}, {1.7562520503997803f, 7557.32275390625f}, {1.7947089672088623f, 7407.56396484375f},
-    {1.834007978439331f, 7419.642578125f}, {1.874167561531067f, 4987.60693359375f}, {1.9152065515518188f, 676.5657958984375f}, {1.957144021987915f, 7022.2705078125f}};
+    {1.0f, 0.0f}, {1.0218970775604248f, 6.957030507237505e-08f}, {1.0442737340927124f, 4.6285471455576044e-08f}, {1.0671403408050537f, 5.610487008311793e-08f},
+    {1.0905076265335083f, 9.732325167988165e-08f}, {1.1143866777420044f, 5.819693527087111e-08f}, {1.1387885808944702f, 4.7297824323777604e-08f}, {1.1637247800827026f, 6.762326876241787e-08f},
+    {1.1892070770263672f, 3.1934181521364735e-08f}, {1.2152472734451294f, 7.120800660231907e-08f}, {1.2418577671051025f, 3.621057231839586e-08f}, {1.2690509557724f, 1.1184210224612912e-09f},
+    {1.2968394756317139f, 6.093220861203008e-08f}, {1.3252365589141846f, 6.357020509994982e-08f}, {1.3542554378509521f, 8.055049249833246e-08f}, {1.383909821510315f, 4.368313355485043e-08f},
+    {1.4142135381698608f, 1.7114270889351246e-08f}, {1.4451807737350464f, 2.300196655369291e-08f}, {1.4768260717391968f, 5.024308791234944e-08f}, {1.5091643333435059f, 6.245172556873513e-08f},
+    {1.5422108173370361f, 5.233334210430485e-09f}, {1.57598078250885f, 3.9720685407473866e-08f}, {1.610490322113037f, 6.10759176566944e-09f}, {1.645755410194397f, 4.129384478801512e-08f},
+    {1.6817927360534668f, 5.616266562924466e-08f}, {1.7186192274093628f, 4.114530582910447e-08f}, {1.7562520503997803f, 6.261829810227937e-08f}, {1.7947089672088623f, 6.006224140264749e-08f},
+    {1.834007978439331f, 5.887106979685086e-08f}, {1.874167561531067f, 3.872611742394838e-08f}, {1.9152065515518188f, 5.140609271592211e-09f}, {1.957144021987915f, 5.221255250376089e-08f}};
 
 // A value's place in the order: larger float, larger key; -0 is 0.
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -103,6 +105,8 @@ __device__ __forceinline__ void st_peer_u64(const void* p, int rank, u64 v) {
 __device__ __forceinline__ void st_peer_u32(const void* p, int rank, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(p), rank)), "r"(v) : "memory");
 }
+
+__device__ __forceinline__ float largest4(const float* x) { return fmaxf(fmaxf(fmaxf(x[0], x[1]), x[2]), x[3]); }
 
 // The least whole number of which at least p of `all` lies before: ceil(p * all), 1 or more.
 __device__ __forceinline__ u64 draw_ceil(float p, u64 all) {
@@ -158,89 +162,144 @@ __device__ __forceinline__ u64 pair2(float lo, float hi) {
 }
 __device__ __forceinline__ float lo_of(u64 v) { return __uint_as_float(static_cast<uint32_t>(v)); }
 __device__ __forceinline__ float hi_of(u64 v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
-__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
-  u64 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ u64 fma2_down(u64 a, u64 b, u64 c) {
-  u64 d;
-  asm("fma.rm.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ u64 add2(u64 a, u64 b) {
-  u64 d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
-  u64 d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
+#define DFL_F32X2(name, op)                                                   \
+  __device__ __forceinline__ u64 name(u64 a, u64 b) {                         \
+    u64 d;                                                                    \
+    asm(op ".f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));                  \
+    return d;                                                                 \
+  }
+#define DFL_F32X2_FMA(name, op)                                               \
+  __device__ __forceinline__ u64 name(u64 a, u64 b, u64 c) {                  \
+    u64 d;                                                                    \
+    asm(op ".f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));      \
+    return d;                                                                 \
+  }
+DFL_F32X2(add2, "add.rn")
+DFL_F32X2(add2_cut, "add.rz")
+DFL_F32X2(mul2, "mul.rn")
+DFL_F32X2_FMA(fma2, "fma.rn")
+DFL_F32X2_FMA(fma2_down, "fma.rm")
+DFL_F32X2_FMA(fma2_cut, "fma.rz")
+__device__ __forceinline__ u64 both(float x) { return pair2(x, x); }
 
 // The weight's function: 2^43 exp((x - m) / T), up to a factor near 1 that a row's
 // weights share and that changes no ratio: m log2(e) / T is rounded down to 32nds
-// (so that no weight is below its value), and r below is raised by 2^-8. c = log2(e) / T in two floats; z = x c - M with M that
-// rounded maximum; 32 z's floor i comes from one multiply-add rounded down onto
-// 1.5 2^23 (without c's low part, which 2^-8 covers, so that r stays positive);
-// r = z - i / 32 + 2^-8 < 0.036 is one exact sum rounded once, and the low part
-// added: off by at most 2^-29. 2^z = 2^(i >> 5) 2^((i & 31) / 32) 2^r: the
-// second factor from a table whose entries the lanes hold (a shuffle looks it up: no
-// bank conflicts, where shared memory has three lanes a bank), the third 1 + q by
-// the exponential's series to r^4 (r^5: 2^-34). The table's high part stays an
-// integer of 24 bits and only the rest, th q + tl < 2^-4, is rounded, to 2^-36. Where
-// m c is so large that x c would lose r, every entry with a weight lies within a
-// factor of two of m: x - m is then exact and takes x's place (base).
-// Two entries at once: 16 instructions an entry, about 30 with sums of two floats
-// in between (64 rows of 151936 entries, all weighed and summed: 43.6 -> PLAIN64 us).
+// (so that no weight is below its value), and r below is raised by 2^-8.
+// c = log2(e) / T in two floats; z = x c - M with M that rounded maximum; 32 z's
+// floor i comes from one multiply-add rounded down onto 1.5 2^23 (without c's low
+// part, which 2^-8 covers, so that r stays positive); r = z - i / 32 + 2^-8 < 0.036
+// is one exact sum rounded once, and the low part added: off by 2^-29 at most.
+// 2^z = 2^(i >> 5) 2^((i & 31) / 32) 2^r: the second factor from a table whose entries
+// the lanes hold (a shuffle looks it up: no bank conflicts, where shared memory has
+// three lanes a bank), as a float and a relative rest; the third 1 + q by the
+// exponential's series to r^4 (r^5: 2^-33). So w = h + l, h the table's float times a
+// power of two (exact), l = h (q + rest), rounded. As an integer: adding 2 to h and l
+// under rounding towards zero leaves their multiples of 2^-22 in the sums' bits; what
+// is cut off of both, added, likewise gives the multiple of 2^-43.
+// Entries below `low` have no weight and are raised to it; where m c is so large that
+// x c would lose r, every entry with a weight lies within a factor of two of m: x - m
+// is then exact and takes x's place (base). Two entries at once, nearly all of it
+// on the multiply-add pipe (integer shifts and selects run at half its rate: a sum of
+// 64-bit shifted integers took 30 instructions an entry, half of them there).
 struct Weigh {
   u64 ch32, ch, cl, neg_base, neg_max, start;
+  float low;
   float hi, lo;              // this lane's table entry
   static constexpr float kMagic = 12582912.f;         // 1.5 2^23, bits 0x4B400000
+  static constexpr unsigned kTwo = 0x40000000u;       // 2.0
   __device__ __forceinline__ void set(float m, float T, int lane) {
     T = fminf(fmaxf(T, 0x1p-100f), 0x1p100f);
     constexpr float kLh = 1.44269502162933349609375f, kLl = 1.92596303350e-8f;   // log2(e)
-    const float c = __fdiv_rn(kLh, T), d = __fdiv_rn(__fmaf_rn(-c, T, kLh) + kLl, T);
+    float c = __fdiv_rn(kLh, T), d = __fdiv_rn(__fmaf_rn(-c, T, kLh) + kLl, T);
+    // so small a temperature that the float below m has no weight: no smaller one is needed
+    const float most = 46.f * 0x1p24f / fabsf(m);   // 46 and more for the float below m
+    if (c > most) {
+      c = most;
+      d = 0.f;
+    }
+    low = __fsub_rd(m, 46.f / c);
     const float base = fabsf(m) * c < 65536.f ? 0.f : m;
     const float top = floorf((m - base) * c * 32.f) * 0.03125f;
-    ch32 = pair2(32.f * c, 32.f * c);
-    ch = pair2(c, c);
-    cl = pair2(d, d);
-    neg_base = pair2(-base, -base);
-    neg_max = pair2(0x1p-8f - top, 0x1p-8f - top);
-    start = pair2(kMagic - 32.f * top, kMagic - 32.f * top);
+    ch32 = both(32.f * c);
+    ch = both(c);
+    cl = both(d);
+    neg_base = both(-base);
+    neg_max = both(0x1p-8f - top);
+    start = both(kMagic - 32.f * top);
     hi = kPow2[lane][0];
     lo = kPow2[lane][1];
   }
-  __device__ __forceinline__ u64 one(float t, float q) const {
-    const uint32_t i = __float_as_uint(t);              // 0x4B400000 + floor(32 z)
-    const float th = __shfl_sync(kAll, hi, i), tl = __shfl_sync(kAll, lo, i);   // the lane is taken modulo 32
-    const uint32_t rest = __float2uint_rz(__fmaf_rn(th, q, tl));
-    const u64 mant = static_cast<u64>((__float_as_uint(th) & 0x7FFFFFu) | 0x800000u) * (1u << 20) + static_cast<u64>(rest) * 128u;
-    const uint32_t n = min((0x4B400000u + 31u - i) >> 5, 63u);   // far below (and -inf): nothing is left
-    return mant >> n;
-  }
-  // Weights of two entries, neither above m. Called by a whole warp.
-  __device__ __forceinline__ void two(float x0, float x1, u64& w0, u64& w1) const {
-    constexpr float kUp = 0x1p36f;
-    const u64 x = add2(pair2(x0, x1), neg_base);
+  // The bits of 2 + h, 2 + l and 2 + 2^21 (what they cut off), cut, of two entries,
+  // neither above m. Called by a whole warp.
+  struct Bits {
+    u64 h, l, r;
+  };
+  __device__ __forceinline__ Bits bits(float x0, float x1) const {
+    const u64 x = add2(pair2(fmaxf(x0, low), fmaxf(x1, low)), neg_base);
     const u64 t = fma2_down(x, ch32, start);
-    const u64 f = add2(t, pair2(-kMagic, -kMagic));
-    const u64 e = fma2(f, pair2(-0.03125f, -0.03125f), neg_max);          // exact
+    const u64 f = add2(t, both(-kMagic));
+    const u64 e = fma2(f, both(-0.03125f), neg_max);                      // exact
     const u64 r = fma2(x, cl, fma2(x, ch, e));
-    u64 q = fma2(r, pair2(9.61812911e-3f * kUp, 9.61812911e-3f * kUp), pair2(5.55041087e-2f * kUp, 5.55041087e-2f * kUp));
-    q = fma2(r, q, pair2(0.240226507f * kUp, 0.240226507f * kUp));
-    q = mul2(r, fma2(r, q, pair2(0.693147181f * kUp, 0.693147181f * kUp)));
-    w0 = one(lo_of(t), lo_of(q));
-    w1 = one(hi_of(t), hi_of(q));
+    u64 q = fma2(r, both(9.61812911e-3f), both(5.55041087e-2f));
+    q = fma2(r, q, both(0.240226507f));
+    q = fma2(r, q, both(0.693147181f));
+    const uint32_t i0 = __float_as_uint(lo_of(t)), i1 = __float_as_uint(hi_of(t));   // 0x4B400000 + floor(32 z)
+    // the lane is taken modulo 32; the exponent's field grows by i >> 5
+    const u64 rest = pair2(__shfl_sync(kAll, lo, i0), __shfl_sync(kAll, lo, i1));
+    const float a = __shfl_sync(kAll, hi, i0), b = __shfl_sync(kAll, hi, i1);
+    const u64 h = pair2(__uint_as_float(((i0 - 0x4B400000u) >> 5) * 0x800000u + __float_as_uint(a)),
+                        __uint_as_float(((i1 - 0x4B400000u) >> 5) * 0x800000u + __float_as_uint(b)));
+    const u64 l = mul2(h, fma2(r, q, rest));
+    Bits v;
+    v.h = add2_cut(h, both(2.f));
+    v.l = add2_cut(l, both(2.f));
+    // h - (v.h - 2) and l - (v.l - 2), both exact
+    const u64 left = add2(add2(h, fma2(v.h, both(-1.f), both(2.f))), add2(l, fma2(v.l, both(-1.f), both(2.f))));
+    v.r = fma2_cut(left, both(0x1p21f), both(2.f));
+    return v;
   }
+  // One entry's weight.
+  static __device__ __forceinline__ u64 whole(uint32_t h, uint32_t l, uint32_t r) {
+    return (static_cast<u64>(h + l - 2u * kTwo) << 21) + (r - kTwo);
+  }
+  __device__ __forceinline__ void two(float x0, float x1, u64& w0, u64& w1) const {
+    const Bits v = bits(x0, x1);
+    w0 = whole(static_cast<uint32_t>(v.h), static_cast<uint32_t>(v.l), static_cast<uint32_t>(v.r));
+    w1 = whole(static_cast<uint32_t>(v.h >> 32), static_cast<uint32_t>(v.l >> 32), static_cast<uint32_t>(v.r >> 32));
+  }
+  // The weights' sum of four entries.
+  __device__ __forceinline__ void add4(const float* x, u64& high, u64& rest) const {
+    const Bits a = bits(x[0], x[1]), b = bits(x[2], x[3]);
+    auto sum = [](u64 p) { return static_cast<uint32_t>(p) + static_cast<uint32_t>(p >> 32); };
+    high += sum(a.h) + sum(b.h) + sum(a.l) + sum(b.l);      // 8 kTwo = 0 in 32 bits
+    rest += sum(a.r) + sum(b.r);                            // 4 kTwo = 0
+  }
+  __device__ __forceinline__ float scale() const { return lo_of(ch); }   // log2(e) / T
   __device__ __forceinline__ u64 operator()(float x) const {
     u64 a, b;
     two(x, x, a, b);
     return a;
   }
 };
+
+// Whether p of a row's weight lies in more than kHopedMost entries, as a power law
+// through the weights of the 1st, the kHoped-th and the kHopedMost-th has it (such rows
+// go to the histograms at once). A guess: either way gives the same result.
+__device__ __forceinline__ bool looks_flat(float m, float upo, float flo, float c, float p, int V) {
+  constexpr float kLogHoped = 7.f, kLogMost = 3.321928f;     // log2 of kHoped, of kHopedMost / kHoped
+  static_assert(kHoped == 128 && kHopedMost == 1280, "their logarithms");
+  const float y1 = fminf((m - upo) * c, 60.f), y2 = fminf((upo - flo) * c, 60.f);
+  // the sum of r^-s from r = 1 to 2^l, as an integral
+  auto area = [](float s, float l) {
+    const float d = (1.f - s) * l;
+    return fabsf(d) < 0.01f ? 0.693147f * l : (exp2f(d) - 1.f) / (1.f - s);
+  };
+  const float s1 = y1 / kLogHoped, s2 = y2 / kLogMost;
+  const float w1 = exp2f(-y1) * kHoped, w2 = w1 * exp2f(-y2) * (static_cast<float>(kHopedMost) / kHoped);
+  const float top = 1.f + area(s1, kLogHoped) + w1 * area(s2, kLogMost);
+  const float tail = V > kHopedMost ? w2 * area(s2, log2f(static_cast<float>(V) / kHopedMost)) : 0.f;
+  return top < p * (top + tail);
+}
 
 // What stays: entries above `thr`, and of those equal to it the ones up to index `cut`.
 struct __align__(8) Border {
@@ -250,12 +309,13 @@ struct __align__(8) Border {
 };
 
 // What a CTA tells its peers: its largest entry (its key and the complement of its
-// index) and a key that at least `share` of its threads' maxima reach; then the weight
-// of its entries, of those that it lists, and their number.
+// index) and two starts of keys that so many of its threads' maxima reach; then the
+// weight of its entries, of those from the lower and from the upper start on, and how
+// many it lists.
 struct Told {
   u64 top;
-  u64 floor;
-  u64 sum, listed, count;
+  u64 floors;
+  u64 sum, listed, upper, count;
 };
 
 struct Shared {
@@ -266,7 +326,7 @@ struct Shared {
   u64 above;
   float warp_f[kWarps];
   unsigned bin, count;
-  int tie, at;
+  int tie, at, len;
   Border border;                   // what the first CTA found
   u64 total;
   float2 min_log;                  // T ln(min_p), in two floats
@@ -280,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
   __shared__ Shared sh;
   unsigned* hist = reinterpret_cast<unsigned*>(s_data + kWarps * rows * 32);   // or: own list, all lists
   u64* own = reinterpret_cast<u64*>(hist);
-  u64* list = own + kOwnList;
+  u64* list = own + kList;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = blockIdx.x / parts, part = blockIdx.x % parts, V = p.V;
   pdl_launch_dependents();
@@ -296,41 +356,71 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
   const int all_rows = (pieces + 31) / 32, id = part * kWarps + warp, warps = parts * kWarps;
   const int row0 = static_cast<int>(static_cast<unsigned>(all_rows) * id / warps);
   const int my_rows = static_cast<int>(static_cast<unsigned>(all_rows) * (id + 1) / warps) - row0, first = row0 * 32;
+  // Held in shared memory (rows > 0), or read again from L2.
+  const bool held = rows > 0;
   uint4* mine = s_data + warp * rows * 32;
+  // Piece `at` of the row: what is not the row's and NaN become -inf, +inf the largest number.
+  bool odd_row = false;   // whether any of this thread's entries was NaN or +inf
+  auto clean = [&](uint4 q, int at, bool look) -> uint4 {
+    float x[VEC];
+    P::get(q, x);
+    bool odd = at * VEC < shift || (at + 1) * VEC > shift + V;   // also pieces behind the row
+    if (look) {
+      bool bad = false;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) bad = bad || !(x[i] <= FLT_MAX);   // NaN or +inf
+      odd_row = odd_row || bad;
+      odd = odd || bad;
+    }
+    if (odd) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const int v = at * VEC + i - shift;
+        if (v < 0 || v >= V || x[i] != x[i]) x[i] = -INFINITY;
+        x[i] = fminf(x[i], P::largest());
+      }
+      q = P::put(x);
+    }
+    return q;
+  };
   float thread_top = -INFINITY;
-  {
-    const float none[8] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY};
-    for (int r0 = 0; r0 < my_rows; r0 += kInFlight) {
-      uint4 q[kInFlight];
+  int top_at = 0;      // the piece that holds it
+  for (int r0 = 0; r0 < my_rows; r0 += kInFlight) {
+    uint4 q[kInFlight];
 #pragma unroll
-      for (int k = 0; k < kInFlight; ++k) {
-        const int at = first + (r0 + k) * 32 + lane;
-        q[k] = r0 + k < my_rows && at < pieces ? __ldcs(base + at) : P::put(none);
+    for (int k = 0; k < kInFlight; ++k) {
+      const int at = first + (r0 + k) * 32 + lane;
+      q[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (r0 + k < my_rows && at < pieces) q[k] = held ? __ldcs(base + at) : __ldg(base + at);
+    }
+#pragma unroll
+    for (int k = 0; k < kInFlight; ++k) {
+      if (r0 + k >= my_rows) break;
+      const int at = first + (r0 + k) * 32 + lane;
+      q[k] = clean(q[k], at, true);
+      float x[VEC], top;
+      P::get(q[k], x);
+      top = x[0];
+#pragma unroll
+      for (int i = 1; i < VEC; ++i) top = fmaxf(top, x[i]);
+      if (top > thread_top) {
+        thread_top = top;
+        top_at = at;
       }
-#pragma unroll
-      for (int k = 0; k < kInFlight; ++k) {
-        if (r0 + k >= my_rows) break;
-        const int at = first + (r0 + k) * 32 + lane;
-        float x[VEC];
-        P::get(q[k], x);
-        bool odd = at * VEC < shift || (at + 1) * VEC > shift + V;   // also pieces behind the row: -inf already
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) odd = odd || !(x[i] <= FLT_MAX);   // NaN or +inf
-        if (odd) {
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            const int v = at * VEC + i - shift;
-            if (v < 0 || v >= V || x[i] != x[i]) x[i] = -INFINITY;
-            x[i] = fminf(x[i], P::largest());
-          }
-          q[k] = P::put(x);
-        }
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) thread_top = fmaxf(thread_top, x[i]);
-        mine[(r0 + k) * 32 + lane] = q[k];
-      }
+      if (held) mine[(r0 + k) * 32 + lane] = q[k];
     }
   }
+  // Row r of this warp's pieces, this lane's, as values.
+  auto piece = [&](int r, float* x) {
+    const int at = first + r * 32 + lane;
+    if (held) {
+      P::get(mine[r * 32 + lane], x);
+    } else {
+      uint4 q = make_uint4(0u, 0u, 0u, 0u);
+      if (at < pieces) q = __ldg(base + at);
+      P::get(clean(q, at, odd_row), x);
+    }
+  };
   const float T_in = p.temperature != nullptr ? p.temperature[n] : 1.f;
   const int k_in = p.top_k != nullptr ? p.top_k[n] : 0;
   const float p_in = p.top_p != nullptr ? p.top_p[n] : 1.f;
@@ -338,20 +428,45 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
   const bool has_min = min_p > 0.f, has_k = k_in > 0 && k_in < V, has_p = p_in < 1.f;
   const bool greedy = T_in == 0.f || k_in == 1;
   // entries that are listed, at least: k, or as many as top-p's border is hoped among
-  const int want = greedy ? 0 : has_k ? (k_in <= kMostListed ? k_in : 0) : has_p ? kHoped : 0;
+  const int want = greedy ? 0 : has_k ? (k_in <= kMostListed ? k_in : 0) : has_p ? kHopedMost : 0;
   if (has_min && threadIdx.x == 0) {
     const double d = static_cast<double>(T_in) * log(static_cast<double>(fminf(min_p, 1.f)));
     const float a = static_cast<float>(d);
     sh.min_log = make_float2(a, static_cast<float>(d - static_cast<double>(a)));
   }
 
-  // f(values, index of the first) of this warp's entries, a piece a lane, all lanes together
+  // f(values, index of the first) of this warp's entries, four neighbours a lane, all
+  // lanes together. From L2 the last row first: it was read last.
   auto each = [&](auto f) {
+    if (held) {
 #pragma unroll 1
-    for (int r = 0; r < my_rows; ++r) {
-      float x[VEC];
-      P::get(mine[r * 32 + lane], x);
-      f(x, (first + r * 32 + lane) * VEC - shift);
+      for (int r = 0; r < my_rows; ++r) {
+        float x[VEC];
+        P::get(mine[r * 32 + lane], x);
+#pragma unroll
+        for (int i = 0; i < VEC; i += 4) f(x + i, (first + r * 32 + lane) * VEC - shift + i);
+      }
+      return;
+    }
+    auto ask = [&](int r) {
+      const int at = first + r * 32 + lane;
+      return r >= 0 && at < pieces ? __ldg(base + at) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    uint4 q[kAgain];
+#pragma unroll
+    for (int k = 0; k < kAgain; ++k) q[k] = ask(my_rows - 1 - k);
+#pragma unroll 1
+    for (int r0 = my_rows - 1; r0 >= 0; r0 -= kAgain) {
+#pragma unroll
+      for (int k = 0; k < kAgain; ++k) {
+        const int r = r0 - k;
+        if (r < 0) break;
+        float x[VEC];
+        P::get(clean(q[k], first + r * 32 + lane, odd_row), x);
+        q[k] = ask(r - kAgain);
+#pragma unroll
+        for (int i = 0; i < VEC; i += 4) f(x + i, (first + r * 32 + lane) * VEC - shift + i);
+      }
     }
   };
   // Cluster barriers: after reading its peers' memory a CTA tells so (left) and
@@ -384,49 +499,62 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
     top = sh.warp_f[lane % kWarps];
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-    // the first entry that equals it: of few threads, one usually
+    // the first entry that equals it, in the first piece of one of few threads
     if (thread_top == top && top > -INFINITY) {
+      float x[VEC];
+      piece((top_at - first) / 32, x);
       int at = INT32_MAX;
-#pragma unroll 1
-      for (int r = my_rows - 1; r >= 0; --r) {
-        float x[VEC];
-        P::get(mine[r * 32 + lane], x);
 #pragma unroll
-        for (int i = VEC - 1; i >= 0; --i) at = x[i] == top ? (first + r * 32 + lane) * VEC - shift + i : at;
-      }
+      for (int i = VEC - 1; i >= 0; --i) at = x[i] == top ? top_at * VEC - shift + i : at;
       atomicMin(&sh.at, at);
     }
     // The largest 16-bit start of a key that `share` threads' maxima reach: every CTA
     // has so many entries from its own on, so together they have `want` from the least
-    // of them on, and few more.
-    uint32_t floor = 0u;
-    if (want > 0) {
-      const int share = min((want + parts - 1) / parts, kThreads);
-      const uint32_t key = key_of(thread_top) >> 16;
+    // of them on, and few more. Where that takes more than a quarter of the threads,
+    // several of the wanted entries share a thread: of T threads T (1 - exp(-w / T)) hold
+    // one or more of w entries in no order. That many maxima, for a few entries more
+    // than are wanted; what the list then holds is looked at.
+    const uint32_t key = key_of(thread_top) >> 16;
+    auto start = [&](int of) -> uint32_t {
+      int share = (of + parts - 1) / parts;
+      if (4 * share > kThreads) {
+        const float w = 1.1f * static_cast<float>(share) + 4.f * sqrtf(static_cast<float>(share));
+        share = static_cast<int>(kThreads * (1.f - expf(w * (-1.f / kThreads))));
+      }
+      uint32_t floor = 0u;
 #pragma unroll 1
       for (uint32_t bit = 1u << 15; bit > 0u; bit >>= 1)
         if (__syncthreads_count(key >= (floor | bit)) >= share) floor |= bit;
+      return floor;
+    };
+    uint32_t floor = 0u, upper = 0u;
+    if (want > 0) {
+      floor = start(want);
+      upper = has_k ? floor : start(kHoped);
     }
     __syncthreads();
     if (threadIdx.x == 0) {
       sh.told.top = static_cast<u64>(key_of(top)) << 32 | (kAll - static_cast<uint32_t>(sh.at));
-      sh.told.floor = floor;
+      sh.told.floors = static_cast<u64>(floor) << 32 | upper;
     }
   }
   meet();
-  float m, flo;
+  float m, flo, upo;       // the maximum, and the two starts
   int first_top;
   {
-    u64 a = ld_peer_u64(&sh.told.top, lane % parts), b = ld_peer_u64(&sh.told.floor, lane % parts);   // parts divides 32
+    u64 a = ld_peer_u64(&sh.told.top, lane % parts), b = ld_peer_u64(&sh.told.floors, lane % parts);   // parts divides 32
+    uint32_t lower = static_cast<uint32_t>(b >> 32), upper = static_cast<uint32_t>(b);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      const u64 c = __shfl_xor_sync(kAll, a, o), d = __shfl_xor_sync(kAll, b, o);
+      const u64 c = __shfl_xor_sync(kAll, a, o);
       a = c > a ? c : a;
-      b = d < b ? d : b;
     }
+    lower = __reduce_min_sync(kAll, lower);
+    upper = __reduce_min_sync(kAll, upper);
     m = value_of(static_cast<uint32_t>(a >> 32));
     first_top = static_cast<int>(kAll - static_cast<uint32_t>(a));
-    flo = value_of(max(static_cast<uint32_t>(b) << 16, key_of(-FLT_MAX)));
+    flo = value_of(max(lower << 16, key_of(-FLT_MAX)));
+    upo = value_of(max(upper << 16, key_of(-FLT_MAX)));
   }
   const bool bad = m == -INFINITY || !(T_in >= 0.f);
   float* probs = p.probs != nullptr ? p.probs + static_cast<size_t>(n) * V : nullptr;
@@ -468,6 +596,199 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
     return incl + warp_sum(lane < warp ? w : 0ull);
   };
 
+  // Sum over the CTA's threads.
+  auto block_sum = [&](u64 v, u64& all) {
+    v = warp_sum(v);
+    __syncthreads();
+    if (lane == 0) sh.scan[warp] = v;
+    __syncthreads();
+    all = warp_sum(lane < kWarps ? sh.scan[lane] : 0ull);
+  };
+
+  // The first CTA's joint list of the entries whose inverted keys are not above
+  // last_key, from all CTAs' lists; c: this lane's CTA's entries.
+  auto pull = [&](unsigned c, unsigned all_len, uint32_t last_key) {
+    // entry i of the joint list lies in the list of the CTA that the counts tell
+    const unsigned incl = static_cast<unsigned>(warp_scan(c, lane));
+    for (unsigned i0 = warp * 32; i0 < all_len; i0 += kThreads) {
+      const unsigned i = i0 + lane;
+      unsigned of = 0u, before = 0u;
+      for (int r = 0; r < parts; ++r) {
+        const unsigned e = __shfl_sync(kAll, incl, r);
+        if (i >= e) {
+          of = r + 1;
+          before = e;
+        }
+      }
+      const u64 e = i < all_len ? ld_peer_u64(own + (i - before), of) : ~0ull;
+      if (i < all_len && static_cast<uint32_t>(e >> 32) <= last_key) list[atomicAdd(&sh.len, 1)] = e;
+    }
+  };
+  // The border among the joint list's entries: of the first `most` in order those with
+  // less than `need` before them (of_most: need is top-p's part of their weight) and not
+  // below `lowest`, the first one always: sh.border, their weight sh.total, and the token
+  // drawn from them. The first CTA alone.
+  auto order = [&](int most, bool of_most, u64 need, float lowest, bool draw) {
+    const int len = sh.len;
+    u64 all;
+    int stay = 0;
+    if (len <= kCounted) {
+      // Ranks and the weight before an entry by comparing all with all: a group of
+      // threads an entry, no order is made.
+      int group = 1;
+      while (2 * group * len <= kThreads && group < 32) group *= 2;
+      const int i = threadIdx.x / group, s0 = threadIdx.x % group;
+      const bool mine_is = i < len;
+      const u64 key = mine_is ? list[i] : ~0ull;
+      const float x = mine_is ? value_of(~static_cast<uint32_t>(key >> 32)) : -INFINITY;
+      const u64 w = weigh(x);
+      if (mine_is && s0 == 0) own[i] = w;
+      __syncthreads();
+      int rank = 0;
+      u64 before = 0ull;
+#pragma unroll 4
+      for (int j = s0; j < len; j += group) {
+        const bool less = list[j] < key;
+        rank += less;
+        before += less ? own[j] : 0ull;
+      }
+      for (int o = group / 2; o > 0; o /= 2) {
+        rank += __shfl_xor_sync(kAll, rank, o);
+        before += __shfl_xor_sync(kAll, before, o);
+      }
+      const bool first_of = mine_is && s0 == 0;
+      if (of_most) {
+        block_sum(first_of && rank < most ? w : 0ull, all);
+        need = draw_ceil(p_in, all);
+      }
+      const bool kept = first_of && rank < most && (rank == 0 || (before < need && x >= lowest));
+      block_sum(kept ? w : 0ull, total);
+      stay = __syncthreads_count(kept);
+      if (first_of) own[i] = kept ? w : 0ull;
+      if (kept && rank == stay - 1) {
+        sh.border = Border{x, static_cast<int>(static_cast<uint32_t>(key))};
+        sh.total = total;
+      }
+      if (threadIdx.x == 0) sh.at = INT32_MAX;
+      __syncthreads();
+      if (draw) {
+        bool whole;
+        const u64 thr = draw_threshold(p.u[n], total, whole);
+        const uint32_t index = static_cast<uint32_t>(key);
+        u64 upto = 0ull;
+#pragma unroll 4
+        for (int j = s0; j < len; j += group) upto += static_cast<uint32_t>(list[j]) <= index ? own[j] : 0ull;
+        for (int o = group / 2; o > 0; o /= 2) upto += __shfl_xor_sync(kAll, upto, o);
+        if (kept && upto > thr) atomicMin(&sh.at, static_cast<int>(index));
+        __syncthreads();
+        if (threadIdx.x == 0) p.tokens[n] = sh.at;
+      }
+    } else {
+      auto sort = [&](auto* v, int len) {   // ascending; what is behind len is larger than all
+        int size = 32;
+        while (size < len) size *= 2;
+        __syncthreads();
+        for (int k = 2; k <= size; k *= 2)
+          for (int j = k / 2; j > 0; j /= 2) {
+            for (int i = threadIdx.x; i < size / 2; i += kThreads) {
+              const int a = 2 * i - (i & (j - 1)), b = a + j;
+              const auto x = v[a], y = v[b];
+              if ((x > y) == ((a & k) == 0)) {
+                v[a] = y;
+                v[b] = x;
+              }
+            }
+            __syncthreads();
+          }
+      };
+      for (int i = len + threadIdx.x; i < kList; i += kThreads) list[i] = ~0ull;
+      sort(list, len);
+      // a thread's entries: PER neighbouring ones
+      constexpr int PER = kList / kThreads;
+      static_assert(PER == 4, "the draw picks one of four");
+      const int kept = min(most, len), at0 = PER * threadIdx.x;
+      u64 w[PER], mass = 0ull;
+      float x[PER];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) x[i] = at0 + i < kept ? value_of(~static_cast<uint32_t>(list[at0 + i] >> 32)) : -INFINITY;
+#pragma unroll
+      for (int i = 0; i < PER; i += 2) weigh.two(x[i], x[i + 1], w[i], w[i + 1]);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        w[i] = at0 + i < kept ? w[i] : 0ull;
+        mass += w[i];
+      }
+      u64 incl = block_scan(mass, all);
+      if (of_most) need = draw_ceil(p_in, all);
+      // the sorted entries that stay: the first ones
+      u64 before = incl - mass;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        stay += at0 + i < kept && (at0 + i == 0 || (before < need && x[i] >= lowest));
+        before += w[i];
+      }
+      block_sum(static_cast<u64>(stay), all);
+      stay = static_cast<int>(all);
+      // their weight, and the entry at the border
+      const int last = stay - 1;
+      if (static_cast<int>(threadIdx.x) == last / PER) {
+        before = incl - mass;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          if (i <= last % PER) before += w[i];
+        sh.total = before;
+        const u64 e = list[last];
+        sh.border = Border{value_of(~static_cast<uint32_t>(e >> 32)), static_cast<int>(static_cast<uint32_t>(e))};
+      }
+      unsigned places[PER];   // index << 11 | place: kept ones are sorted by their index
+      static_assert(kList <= 2048 && kDrawMaxVocab <= 1 << 20, "bits of an index and a place");
+#pragma unroll
+      for (int i = 0; i < PER; ++i) places[i] = static_cast<uint32_t>(list[at0 + i]) << 11 | (at0 + i);
+      __syncthreads();
+      total = sh.total;
+      if (draw) {
+        bool whole;
+        const u64 thr = draw_threshold(p.u[n], total, whole);
+        unsigned* order = reinterpret_cast<unsigned*>(own);   // 2048 words
+        u64* weight = list;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          weight[at0 + i] = w[i];
+          order[at0 + i] = at0 + i < stay ? places[i] : kAll;
+        }
+        sort(order, stay);
+        mass = 0ull;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          places[i] = order[at0 + i];
+          w[i] = at0 + i < stay ? weight[places[i] & 2047u] : 0ull;
+          mass += w[i];
+        }
+        incl = block_scan(mass, all);
+        if (incl > thr && incl - mass <= thr) {   // one thread
+          u64 c2 = incl - mass;
+          int k = 0;
+#pragma unroll
+          for (int i = 0; i < PER - 1; ++i) {
+            c2 += w[i];
+            k += c2 <= thr;
+          }
+          p.tokens[n] = static_cast<int>((k == 0 ? places[0] : k == 1 ? places[1] : k == 2 ? places[2] : places[3]) >> 11);
+        }
+      }
+    }
+  };
+
+  // The border and the weight above it, from the first CTA to all.
+  auto send = [&]() {
+    if (threadIdx.x < parts) {
+      const u64 b = static_cast<u64>(static_cast<uint32_t>(sh.border.cut)) << 32 | __float_as_uint(sh.border.thr);
+      st_peer_u64(&sh.border, threadIdx.x, b);
+      st_peer_u64(&sh.total, threadIdx.x, sh.total);
+    }
+  };
+
+  unsigned* own_count = reinterpret_cast<unsigned*>(&sh.told.count);   // of this CTA's list
   if (bad || greedy) {
     if (part == 0 && threadIdx.x == 0) {
       if (bad) report(p.dev_status, DFLASH_ERR_INVALID_ARG);
@@ -479,180 +800,72 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
   } else {
     bool found = false;                // the border, through the list
     u64 Z = 0ull;                      // the weight of all, where top-p has no top-k before it
-    if (want > 0) {
+    // where no float lies below m (the lowest number), what has no weight cannot be raised to one
+    const bool sums = weigh.low > -INFINITY, listed = want > 0 && sums && !(has_p && !has_k && looks_flat(m, upo, flo, weigh.scale(), p_in, V));
+    if (listed) {
       // -------------------------------------------------------------- few candidates
       // Entries from flo on go to the CTA's list, all CTAs' lists to the first one, which
-      // sorts them and knows everything but the weight of the rest.
+      // orders them and knows everything but the weight of the rest. Where the entries
+      // from upo on hold top-p's border, these are enough.
       const bool all_weigh = !has_k;
-      u64 sum = 0ull, above = 0ull;
-      unsigned* count = reinterpret_cast<unsigned*>(&sh.told.count);
-      each([&](const float* x, int v0) {
-        u64 w[VEC];
-        if (all_weigh) {
+      auto append = [&](const float* x, int v0) {
+        if (largest4(x) >= flo) {
 #pragma unroll
-          for (int i = 0; i < VEC; i += 2) weigh.two(x[i], x[i + 1], w[i], w[i + 1]);
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) sum += w[i];
-        }
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          if (x[i] >= flo) {
-            if (all_weigh) above += w[i];
-            const unsigned at = atomicAdd(count, 1u);
-            if (at < kOwnList) own[at] = static_cast<u64>(~key_of(x[i])) << 32 | static_cast<uint32_t>(v0 + i);
+          for (int i = 0; i < 4; ++i) {
+            if (x[i] >= flo) {
+              const unsigned at = atomicAdd(own_count, 1u);
+              if (at < kList) own[at] = static_cast<u64>(~key_of(x[i])) << 32 | static_cast<uint32_t>(v0 + i);
+            }
           }
         }
-      });
+      };
       if (all_weigh) {
-        sum = warp_sum(sum);
-        above = warp_sum(above);
-        if (lane == 0) {
-          sh.warp[0][warp] = sum;
-          sh.warp[1][warp] = above;
+        u64 sum = 0ull, low_sum = 0ull, all;
+        each([&](const float* x, int v0) {
+          weigh.add4(x, sum, low_sum);
+          append(x, v0);
+        });
+        block_sum((sum << 21) + low_sum, all);
+        if (threadIdx.x == 0) sh.told.sum = all;
+        const int len = min(static_cast<int>(*own_count), kList);
+        u64 above = 0ull, top_sum = 0ull;
+        for (int i0 = warp * 32; i0 < len; i0 += kThreads) {
+          const bool in = i0 + lane < len;
+          const float x = in ? value_of(~static_cast<uint32_t>(own[i0 + lane] >> 32)) : m;
+          const u64 w = weigh(x);
+          above += in ? w : 0ull;
+          top_sum += in && x >= upo ? w : 0ull;
         }
-        __syncthreads();
-        if (warp == 0) {
-          const u64 a = warp_sum(lane < kWarps ? sh.warp[0][lane] : 0ull), b = warp_sum(lane < kWarps ? sh.warp[1][lane] : 0ull);
-          if (lane == 0) {
-            sh.told.sum = a;
-            sh.told.listed = b;
-          }
-        }
+        block_sum(above, all);
+        if (threadIdx.x == 0) sh.told.listed = all;
+        block_sum(top_sum, all);
+        if (threadIdx.x == 0) sh.told.upper = all;
+      } else {
+        each(append);
       }
+      if (threadIdx.x == 0) sh.len = 0;
       meet();
-      const u64 c = lane < parts ? ld_peer_u64(&sh.told.count, lane) : 0ull;
-      unsigned len = __reduce_add_sync(kAll, static_cast<unsigned>(c));
-      found = len <= kList && __reduce_max_sync(kAll, static_cast<unsigned>(c)) <= kOwnList;
+      const unsigned c = lane < parts ? static_cast<unsigned>(ld_peer_u64(&sh.told.count, lane)) : 0u;
+      const unsigned all_len = __reduce_add_sync(kAll, c);
+      found = all_len <= kList && (!has_k || all_len >= static_cast<unsigned>(k_in));
       u64 need = ~0ull;
+      float from = flo;
       if (all_weigh) {
         Z = warp_sum(lane < parts ? ld_peer_u64(&sh.told.sum, lane) : 0ull);
         const u64 has = warp_sum(lane < parts ? ld_peer_u64(&sh.told.listed, lane) : 0ull);
+        const u64 high = warp_sum(lane < parts ? ld_peer_u64(&sh.told.upper, lane) : 0ull);
         need = draw_ceil(p_in, Z);
         found = found && has >= need;
+        if (high >= need) from = upo;
       }
       if (found && part == 0) {
-        // entry i of the joint list lies in the list of the CTA that the counts tell
-        const unsigned incl = static_cast<unsigned>(warp_scan(c, lane));
-        for (unsigned i0 = warp * 32; i0 < kList; i0 += kThreads) {
-          const unsigned i = i0 + lane;
-          unsigned from = 0u, before = 0u;
-          for (int r = 0; r < parts; ++r) {
-            const unsigned e = __shfl_sync(kAll, incl, r);
-            if (i >= e) {
-              from = r + 1;
-              before = e;
-            }
-          }
-          list[i] = i < len ? ld_peer_u64(own + (i - before), from) : ~0ull;
-        }
+        pull(c, all_len, ~key_of(from));
       }
       left();
       if (found && part == 0) {
-        // larger values first, equal ones by index
-        auto sort = [&](auto* v, int len) {   // ascending; what is behind len is larger than all
-          int size = 32;
-          while (size < len) size *= 2;
-          __syncthreads();
-          for (int k = 2; k <= size; k *= 2)
-            for (int j = k / 2; j > 0; j /= 2) {
-              for (int i = threadIdx.x; i < size / 2; i += kThreads) {
-                const int a = 2 * i - (i & (j - 1)), b = a + j;
-                const auto x = v[a], y = v[b];
-                if ((x > y) == ((a & k) == 0)) {
-                  v[a] = y;
-                  v[b] = x;
-                }
-              }
-              __syncthreads();
-            }
-        };
-        sort(list, static_cast<int>(len));
-        // a thread's entries: PER neighbouring ones
-        constexpr int PER = kList / kThreads;
-        static_assert(PER == 4, "the draw picks one of four");
-        const int kept = has_k ? min(k_in, static_cast<int>(len)) : static_cast<int>(len);
-        u64 w[PER], mass = 0ull;
-        float x[PER];
-#pragma unroll
-        for (int i = 0; i < PER; ++i) x[i] = value_of(~static_cast<uint32_t>(list[PER * threadIdx.x + i] >> 32));
-#pragma unroll
-        for (int i = 0; i < PER; i += 2) weigh.two(fminf(x[i], m), fminf(x[i + 1], m), w[i], w[i + 1]);
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          if (PER * static_cast<int>(threadIdx.x) + i >= kept) w[i] = 0ull;
-          mass += w[i];
-        }
-        u64 all, incl = block_scan(mass, all);
-        if (has_k && has_p) need = draw_ceil(p_in, all);
-        // the first of the sorted entries that stays out
-        int stay = 0;
-        u64 before = incl - mass;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const int at = PER * threadIdx.x + i;
-          stay += at < kept && (at == 0 || ((!has_p || before < need) && x[i] >= least));
-          before += w[i];
-        }
         __syncthreads();
-        stay = static_cast<int>(__reduce_add_sync(kAll, static_cast<unsigned>(stay)));
-        if (lane == 0) sh.scan[warp] = stay;
-        __syncthreads();
-        stay = static_cast<int>(warp_sum(lane < kWarps ? sh.scan[lane] : 0ull));
-        __syncthreads();
-        // their weight, and the entry at the border
-        const int last = stay - 1;
-        if (static_cast<int>(threadIdx.x) == last / PER) {
-          before = incl - mass;
-#pragma unroll
-          for (int i = 0; i < PER; ++i)
-            if (i <= last % PER) before += w[i];
-          sh.total = before;
-          const u64 e = list[last];
-          sh.border = Border{value_of(~static_cast<uint32_t>(e >> 32)), static_cast<int>(static_cast<uint32_t>(e))};
-        }
-        unsigned places[PER];   // index << 11 | place: kept ones are sorted by their index
-        static_assert(kList <= 2048 && kDrawMaxVocab <= 1 << 20, "bits of an index and a place");
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-          places[i] = static_cast<uint32_t>(list[PER * threadIdx.x + i]) << 11 | (PER * threadIdx.x + i);
-        __syncthreads();
-        total = sh.total;
-        if (p.tokens != nullptr) {
-          bool whole;
-          const u64 thr = draw_threshold(p.u[n], total, whole);
-          unsigned* order = reinterpret_cast<unsigned*>(own);   // 2048 words
-          u64* weight = list;
-#pragma unroll
-          for (int i = 0; i < PER; ++i) {
-            const int at = PER * threadIdx.x + i;
-            weight[at] = w[i];
-            order[at] = at < stay ? places[i] : kAll;
-          }
-          sort(order, stay);
-          mass = 0ull;
-#pragma unroll
-          for (int i = 0; i < PER; ++i) {
-            places[i] = order[PER * threadIdx.x + i];
-            w[i] = PER * static_cast<int>(threadIdx.x) + i < stay ? weight[places[i] & 2047u] : 0ull;
-            mass += w[i];
-          }
-          incl = block_scan(mass, all);
-          if (incl > thr && incl - mass <= thr) {   // one thread
-            u64 c2 = incl - mass;
-            int k = 0;
-#pragma unroll
-            for (int i = 0; i < PER - 1; ++i) {
-              c2 += w[i];
-              k += c2 <= thr;
-            }
-            p.tokens[n] = static_cast<int>((k == 0 ? places[0] : k == 1 ? places[1] : k == 2 ? places[2] : places[3]) >> 11);
-          }
-        }
-        if (probs != nullptr && threadIdx.x < parts) {
-          const u64 b = static_cast<u64>(static_cast<uint32_t>(sh.border.cut)) << 32 | __float_as_uint(sh.border.thr);
-          st_peer_u64(&sh.border, threadIdx.x, b);
-          st_peer_u64(&sh.total, threadIdx.x, sh.total);
-        }
+        order(has_k ? k_in : kList, has_k && has_p, need, least, p.tokens != nullptr);
+        if (probs != nullptr) send();
       }
       if (found && probs != nullptr) {
         meet();
@@ -669,7 +882,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
         unsigned c = 0;
         each([&](const float* y, int) {
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) c += y[i] == x;
+          for (int i = 0; i < 4; ++i) c += y[i] == x;
         });
         const u64 all = __reduce_add_sync(kAll, c);
         u64 before, sum;
@@ -680,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
 #pragma unroll 1
           for (int i = 0; i < my_rows && at < 0; ++i) {
             float y[VEC];
-            P::get(mine[i * 32 + lane], y);
+            piece(i, y);
             unsigned k = 0;
 #pragma unroll
             for (int j = 0; j < VEC; ++j) k += y[j] == x;
@@ -798,7 +1011,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
           clear(kCountBins);
           each([&](const float* x, int) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
+            for (int i = 0; i < 4; ++i) {
               const unsigned bin = (hi - key_of(x[i])) >> step;
               if (x[i] >= a && x[i] <= b && bin < kCountBins) atomicAdd(&hist[bin], 1u);
             }
@@ -821,15 +1034,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
       // top-p: levels of weights
       if (has_p) {
         const Border from = keep;
+        const bool unknown = !has_k && !listed;   // Z is: weighed with the first level
         if (has_k) {
           u64 sum = 0ull, before;
           each([&](const float* x, int v0) {
-            bool any = false;
+            if (__any_sync(kAll, largest4(x) >= from.thr)) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) any = any || from.keeps(x[i], v0 + i);
-            if (__any_sync(kAll, any)) {
-#pragma unroll
-              for (int i = 0; i < VEC; i += 2) {
+              for (int i = 0; i < 4; i += 2) {
                 u64 a, b;
                 weigh.two(x[i], x[i + 1], a, b);
                 sum += (from.keeps(x[i], v0 + i) ? a : 0ull) + (from.keeps(x[i + 1], v0 + i + 1) ? b : 0ull);
@@ -838,11 +1049,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
           });
           join(warp_sum(sum), before, Z);
         }
-        const u64 need = draw_ceil(p_in, Z);
-        // entries below this one weigh less than 1 - p of all together
-        const float y0 = log2f(static_cast<float>(V) / ((1.f - fmaxf(p_in, 0.f)) * __ull2float_rn(Z))) + kOne + 0.25f;
-        const float c1 = 1.442695f / fminf(fmaxf(T_in, 0x1p-100f), 0x1p100f);
-        const float cut = fmaxf(fmaxf(__fsub_rd(m, y0 / c1 * 1.0001f), -FLT_MAX), from.thr);
+        u64 need = unknown ? 0ull : draw_ceil(p_in, Z);
+        // entries below this one weigh less than 1 - p of all together (or of the largest)
+        const float y0 = log2f(static_cast<float>(V) / ((1.f - fmaxf(p_in, 0.f)) * (unknown ? 0x1p43f : __ull2float_rn(Z)))) + kOne + 0.25f;
+        const float cut = fmaxf(fmaxf(__fsub_rd(m, y0 / weigh.scale() * 1.0001f), -FLT_MAX), from.thr);
         uint32_t lo = key_of(cut), hi = key_of(m);
         const float scale = linear_scale(cut, kMassBins);
         u64 under = 0ull;   // the weight above the range
@@ -852,16 +1062,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
           int step = max(0, 32 - __clz(hi - lo) - 10);
           if (step <= P::kFinal) step = P::kFinal;
           clear(kHistInts);
+          const bool all_of = linear && unknown;
+          u64 sum = 0ull;
           each([&](const float* x, int v0) {
-            bool any = false;
+            if (__any_sync(kAll, all_of || largest4(x) >= a)) {
+              u64 w[4];
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) any = any || (x[i] >= a && x[i] <= b);
-            if (__any_sync(kAll, any)) {
-              u64 w[VEC];
+              for (int i = 0; i < 4; i += 2) weigh.two(x[i], x[i + 1], w[i], w[i + 1]);
 #pragma unroll
-              for (int i = 0; i < VEC; i += 2) weigh.two(x[i], x[i + 1], w[i], w[i + 1]);
-#pragma unroll
-              for (int i = 0; i < VEC; ++i) {
+              for (int i = 0; i < 4; ++i) {
+                if (all_of && x[i] > -INFINITY) sum += w[i];
                 const unsigned bin = linear ? linear_bin(x[i], scale) : (hi - key_of(x[i])) >> step;
                 if (x[i] >= a && x[i] <= b && from.keeps(x[i], v0 + i) && bin < kMassBins) {
                   if (!linear) atomicAdd(&hist[bin], 1u);
@@ -872,6 +1082,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
               }
             }
           });
+          if (all_of) {
+            u64 before;
+            join(warp_sum(sum), before, Z);
+            need = draw_ceil(p_in, Z);
+          }
           if (!find_bin(true, !linear, need - under)) break;   // cannot be: everything below the cut would be needed
           under += sh.above;
           const unsigned count = sh.count;
@@ -889,26 +1104,64 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
             else keep = x == from.thr ? from : Border{x, INT32_MAX};
             break;
           }
-          linear = false;
+          if (linear) {
+            // the bin's entries, if they fit the list: their order tells the border
+            linear = false;
+            settle();
+            if (threadIdx.x == 0) {
+              sh.told.count = 0ull;
+              sh.len = 0;
+            }
+            __syncthreads();
+            const float first_in = value_of(lo), last_in = value_of(hi);
+            each([&](const float* x, int v0) {
+              if (largest4(x) < first_in) return;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (x[i] >= first_in && x[i] <= last_in && from.keeps(x[i], v0 + i)) {
+                  const unsigned at = atomicAdd(own_count, 1u);
+                  if (at < kList) own[at] = static_cast<u64>(~key_of(x[i])) << 32 | static_cast<uint32_t>(v0 + i);
+                }
+              }
+            });
+            meet();
+            const unsigned c = lane < parts ? static_cast<unsigned>(ld_peer_u64(&sh.told.count, lane)) : 0u;
+            const unsigned all_len = __reduce_add_sync(kAll, c);
+            const bool fits = all_len <= kList;
+            if (fits && part == 0) pull(c, all_len, kAll);
+            left();
+            if (fits) {
+              if (part == 0) {
+                __syncthreads();
+                order(kList, false, need - under, -FLT_MAX, false);
+                send();
+              }
+              meet();
+              keep = sh.border;
+              break;
+            }
+          }
         }
       }
       if (least > keep.thr) keep = Border{least, INT32_MAX};
       // the draw: every warp's kept weight, then the warp whose range holds the threshold
-      u64 sum = 0ull, cum;
+      u64 sum = 0ull, low_sum = 0ull, cum;
+      const bool all_stay = keep.thr == -FLT_MAX && keep.cut == INT32_MAX && sums;
       each([&](const float* x, int v0) {
-        bool any = false;
+        if (all_stay) {
+          weigh.add4(x, sum, low_sum);
+          return;
+        }
+        if (__any_sync(kAll, largest4(x) >= keep.thr)) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) any = any || keep.keeps(x[i], v0 + i);
-        if (__any_sync(kAll, any)) {
-#pragma unroll
-          for (int i = 0; i < VEC; i += 2) {
+          for (int i = 0; i < 4; i += 2) {
             u64 a, b;
             weigh.two(x[i], x[i + 1], a, b);
             sum += (keep.keeps(x[i], v0 + i) ? a : 0ull) + (keep.keeps(x[i + 1], v0 + i + 1) ? b : 0ull);
           }
         }
       });
-      sum = warp_sum(sum);
+      sum = warp_sum(all_stay ? (sum << 21) + low_sum : sum);
       join(sum, cum, total);
       if (p.tokens != nullptr) {
         bool whole;
@@ -917,7 +1170,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
 #pragma unroll 1
           for (int r = 0; r < my_rows; ++r) {
             float x[VEC];
-            P::get(mine[r * 32 + lane], x);
+            piece(r, x);
             const int v0 = (first + r * 32 + lane) * VEC - shift;
             u64 w[VEC], own_sum = 0ull;
 #pragma unroll
@@ -960,28 +1213,24 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
     float* out = probs - shift;
     const bool aligned = (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
     each([&](const float* x, int v0) {
-      float y[VEC];
-      bool any = false;
+      float y[4];
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        y[i] = 0.f;
-        any = any || keep.keeps(x[i], v0 + i);
-      }
-      if (__any_sync(kAll, any)) {
+      for (int i = 0; i < 4; ++i) y[i] = 0.f;
+      if (__any_sync(kAll, largest4(x) >= keep.thr)) {
 #pragma unroll
-        for (int i = 0; i < VEC; i += 2) {
+        for (int i = 0; i < 4; i += 2) {
           u64 a, b;
           weigh.two(x[i], x[i + 1], a, b);
           if (keep.keeps(x[i], v0 + i)) y[i] = share(a);
           if (keep.keeps(x[i + 1], v0 + i + 1)) y[i + 1] = share(b);
         }
       }
-      if (aligned && v0 >= 0 && v0 + VEC <= V) {
+      if (aligned && v0 >= 0 && v0 + 4 <= V) {
 #pragma unroll
-        for (int i = 0; i < VEC; i += 4) __stcs(reinterpret_cast<float4*>(probs + v0 + i), make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]));
+        for (int i = 0; i < 4; i += 4) __stcs(reinterpret_cast<float4*>(probs + v0 + i), make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]));
       } else {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i)
+        for (int i = 0; i < 4; ++i)
           if (v0 + i >= 0 && v0 + i < V) probs[v0 + i] = y[i];
       }
     });
@@ -991,7 +1240,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
 
 template <typename TT>
 cudaError_t launch_typed(const DrawArgs& a, cudaStream_t s, bool pdl) {
-  constexpr int kMaxSmem = 200 * 1024;
+  constexpr int kMaxSmem = 10 * kWarps * 32 * 16 + kScratchBytes;
   static bool done[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -1005,15 +1254,17 @@ cudaError_t launch_typed(const DrawArgs& a, cudaStream_t s, bool pdl) {
   const int pieces = (a.V + 2 * VEC - 2) / VEC;          // whatever the row's alignment
   const int all_rows = (pieces + 31) / 32;
   auto rows_of = [&](int parts) { return (all_rows + parts * kWarps - 1) / (parts * kWarps); };
-  // CTAs a row: as many as leave two of them room in an SM's shared memory (ten rows of
-  // 16-byte pieces a warp, 80 KB), and more while they leave SMs idle and have two rows
-  // each. Clusters of 16 find no room beside one another: only for a few rows.
+  // CTAs a row: as many as find room at once, two an SM, while each warp has two rows of
+  // 16-byte pieces; at least as many as keep what is read again within L2 (96 MB for
+  // the rows under way). Clusters of 16 find no room beside one another: only for few rows.
+  const long long slots = 2LL * num_sms_of_current_device();
+  const long long row_bytes = 16LL * pieces;
   int parts = 1;
-  while (parts < kMaxParts && rows_of(parts) > 10) parts *= 2;
-  while (parts < (a.N <= 4 ? kMaxParts : 8) && 2LL * parts * a.N <= 2LL * num_sms_of_current_device() && rows_of(parts) > 2) parts *= 2;
-  const int rows = rows_of(parts);
+  while (parts < 8 && slots / parts * row_bytes > 96LL << 20 && a.N * row_bytes > 96LL << 20) parts *= 2;
+  while (parts < (a.N <= 4 ? kMaxParts : 8) && 2LL * parts * a.N <= slots && rows_of(parts) > 2) parts *= 2;
+  // held in shared memory where two CTAs find room (ten rows a warp: 80 KB)
+  const int rows = rows_of(parts) <= 10 ? rows_of(parts) : 0;
   const size_t smem = static_cast<size_t>(rows) * kWarps * 32 * 16 + kScratchBytes;
-  if (smem > kMaxSmem) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.N) * parts);
   cfg.blockDim = dim3(kThreads);
