@@ -40,11 +40,11 @@ namespace {
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxParts = 16;
 constexpr int kCountBins = 2048, kMassBins = 1024;
-constexpr int kHistInts = 4096;      // 16 KB: counts, or counts and three parts of a weight
+constexpr int kHistInts = 3 * kMassBins;   // of weights: counts, lower and upper words
 constexpr int kList = 2048;          // candidates of a CTA, and of a row: 32 KB
 constexpr int kMostListed = 1280;    // top-k borders that the list is made for
-constexpr int kHoped = 128, kHopedMost = 1280;   // candidates among which top-p's border is looked for, and then
-constexpr int kCounted = 512;        // candidates whose ranks are counted; more are sorted
+constexpr int kHoped = 64, kHopedMost = 1280;   // candidates among which top-p's border is looked for, and then
+constexpr int kCounted = 192;        // candidates whose ranks are counted; more are sorted
 constexpr int kScratchBytes = 2 * kList * 8;   // the lists, or the histograms
 constexpr int kInFlight = 5;         // 16-byte loads a thread, first pass
 constexpr int kAgain = 2;            // and later ones
@@ -199,18 +199,24 @@ __device__ __forceinline__ u64 both(float x) { return pair2(x, x); }
 // Entries below `low` have no weight and are raised to it; where m c is so large that
 // x c would lose r, every entry with a weight lies within a factor of two of m: x - m
 // is then exact and takes x's place (base). Two entries at once, nearly all of it
-// on the multiply-add pipe (integer shifts and selects run at half its rate: a sum of
-// 64-bit shifted integers took 30 instructions an entry, half of them there).
+// on the multiply-add pipe (16 cycles an entry and SM quarter, bound by that pipe and
+// the shuffles; integer shifts, selects and conversions take 2 to 8 cycles each, and a
+// sum of 64-bit shifted integers took 1024 rows of bf16 from 265 to 315 us).
 struct Weigh {
   u64 ch32, ch, cl, neg_base, neg_max, start;
   float low;
   float hi, lo;              // this lane's table entry
   static constexpr float kMagic = 12582912.f;         // 1.5 2^23, bits 0x4B400000
   static constexpr unsigned kTwo = 0x40000000u;       // 2.0
-  __device__ __forceinline__ void set(float m, float T, int lane) {
+  // c in two floats
+  static __device__ __forceinline__ float2 factor(float T) {
     T = fminf(fmaxf(T, 0x1p-100f), 0x1p100f);
     constexpr float kLh = 1.44269502162933349609375f, kLl = 1.92596303350e-8f;   // log2(e)
-    float c = __fdiv_rn(kLh, T), d = __fdiv_rn(__fmaf_rn(-c, T, kLh) + kLl, T);
+    const float c = __fdiv_rn(kLh, T);
+    return make_float2(c, __fdiv_rn(__fmaf_rn(-c, T, kLh) + kLl, T));
+  }
+  __device__ __forceinline__ void set(float m, float2 f, int lane) {
+    float c = f.x, d = f.y;
     // so small a temperature that the float below m has no weight: no smaller one is needed
     const float most = 46.f * 0x1p24f / fabsf(m);   // 46 and more for the float below m
     if (c > most) {
@@ -274,6 +280,21 @@ struct Weigh {
     high += sum(a.h) + sum(b.h) + sum(a.l) + sum(b.l);      // 8 kTwo = 0 in 32 bits
     rest += sum(a.r) + sum(b.r);                            // 4 kTwo = 0
   }
+  // The sum of four weights in fp32, for rows with |m c| below kNear. Each is off by the
+  // rounding of an exponent below 32 (2^-20; what lies beyond weighs V 2^-32 at most) and
+  // by c's low part, (|m c| + 32) 2^-25, both times ln 2, by 2^-22 (the exponential) and
+  // two roundings of the sum: (0.35 |m c| + 29) 2^-24 of itself.
+  static constexpr float kNear = 1024.f;
+  __device__ __forceinline__ float near4(const float* x) const {
+    float e[4];
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      const u64 z = fma2(pair2(x[i], x[i + 1]), ch, neg_max);
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e[i]) : "f"(lo_of(z)));
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e[i + 1]) : "f"(hi_of(z)));
+    }
+    return (e[0] + e[1]) + (e[2] + e[3]);
+  }
   __device__ __forceinline__ float scale() const { return lo_of(ch); }   // log2(e) / T
   __device__ __forceinline__ u64 operator()(float x) const {
     u64 a, b;
@@ -286,8 +307,8 @@ struct Weigh {
 // through the weights of the 1st, the kHoped-th and the kHopedMost-th has it (such rows
 // go to the histograms at once). A guess: either way gives the same result.
 __device__ __forceinline__ bool looks_flat(float m, float upo, float flo, float c, float p, int V) {
-  constexpr float kLogHoped = 7.f, kLogMost = 3.321928f;     // log2 of kHoped, of kHopedMost / kHoped
-  static_assert(kHoped == 128 && kHopedMost == 1280, "their logarithms");
+  constexpr float kLogHoped = 6.f, kLogMost = 4.321928f;     // log2 of kHoped, of kHopedMost / kHoped
+  static_assert(kHoped == 64 && kHopedMost == 1280, "their logarithms");
   const float y1 = fminf((m - upo) * c, 60.f), y2 = fminf((upo - flo) * c, 60.f);
   // the sum of r^-s from r = 1 to 2^l, as an integral
   auto area = [](float s, float l) {
@@ -310,12 +331,11 @@ struct __align__(8) Border {
 
 // What a CTA tells its peers: its largest entry (its key and the complement of its
 // index) and two starts of keys that so many of its threads' maxima reach; then the
-// weight of its entries, of those from the lower and from the upper start on, and how
-// many it lists.
+// weight of its entries and of those that it lists, and their number.
 struct Told {
   u64 top;
   u64 floors;
-  u64 sum, listed, upper, count;
+  u64 sum, listed, count;
 };
 
 struct Shared {
@@ -327,6 +347,7 @@ struct Shared {
   float warp_f[kWarps];
   unsigned bin, count;
   int tie, at, len;
+  unsigned certain, sure;          // whether the border is, in the first CTA, and told to all
   Border border;                   // what the first CTA found
   u64 total;
   float2 min_log;                  // T ln(min_p), in two floats
@@ -427,6 +448,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
   const float min_p = p.min_p != nullptr ? p.min_p[n] : 0.f;
   const bool has_min = min_p > 0.f, has_k = k_in > 0 && k_in < V, has_p = p_in < 1.f;
   const bool greedy = T_in == 0.f || k_in == 1;
+  const float2 c_log2e = Weigh::factor(greedy ? 1.f : T_in);
   // entries that are listed, at least: k, or as many as top-p's border is hoped among
   const int want = greedy ? 0 : has_k ? (k_in <= kMostListed ? k_in : 0) : has_p ? kHopedMost : 0;
   if (has_min && threadIdx.x == 0) {
@@ -477,12 +499,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
     pending = false;
   };
   auto left = [&]() {
+    if (parts == 1) return;
     cluster_arrive();
     pending = true;
   };
   auto meet = [&]() {
     settle();
-    cluster_sync();
+    if (parts == 1) __syncthreads(); else cluster_sync();
   };
 
   // ---------------------------------------------------------------- maximum
@@ -560,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
   float* probs = p.probs != nullptr ? p.probs + static_cast<size_t>(n) * V : nullptr;
   Border keep{-FLT_MAX, INT32_MAX};
   Weigh weigh;
-  weigh.set(m, greedy ? 1.f : T_in, lane);
+  weigh.set(m, c_log2e, lane);
   u64 total = 0ull;
   // min-p: the least float that is not below m + T ln(min_p)
   float least = -FLT_MAX;
@@ -605,12 +628,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
     all = warp_sum(lane < kWarps ? sh.scan[lane] : 0ull);
   };
 
-  // The first CTA's joint list of the entries whose inverted keys are not above
-  // last_key, from all CTAs' lists; c: this lane's CTA's entries.
-  auto pull = [&](unsigned c, unsigned all_len, uint32_t last_key) {
-    // entry i of the joint list lies in the list of the CTA that the counts tell
-    const unsigned incl = static_cast<unsigned>(warp_scan(c, lane));
-    for (unsigned i0 = warp * 32; i0 < all_len; i0 += kThreads) {
+  // The first CTA's joint list of all CTAs' lists; c: entries of this lane's CTA.
+  auto pull = [&](unsigned c) {
+    const unsigned incl = static_cast<unsigned>(warp_scan(c, lane)), len = __shfl_sync(kAll, incl, 31);
+    for (unsigned i0 = warp * 32; i0 < len; i0 += kThreads) {
       const unsigned i = i0 + lane;
       unsigned of = 0u, before = 0u;
       for (int r = 0; r < parts; ++r) {
@@ -620,15 +641,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
           before = e;
         }
       }
-      const u64 e = i < all_len ? ld_peer_u64(own + (i - before), of) : ~0ull;
-      if (i < all_len && static_cast<uint32_t>(e >> 32) <= last_key) list[atomicAdd(&sh.len, 1)] = e;
+      if (i < len) list[i] = ld_peer_u64(own + (i - before), of);
     }
+    if (threadIdx.x == 0) sh.len = len;
   };
   // The border among the joint list's entries: of the first `most` in order those with
   // less than `need` before them (of_most: need is top-p's part of their weight) and not
   // below `lowest`, the first one always: sh.border, their weight sh.total, and the token
-  // drawn from them. The first CTA alone.
-  auto order = [&](int most, bool of_most, u64 need, float lowest, bool draw) {
+  // drawn from them, if no entry has between `need` and `need_most` before it (sh.certain).
+  // The first CTA alone.
+  auto order = [&](int most, bool of_most, u64 need, u64 need_most, float lowest, bool draw) {
     const int len = sh.len;
     u64 all;
     int stay = 0;
@@ -659,9 +681,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
       const bool first_of = mine_is && s0 == 0;
       if (of_most) {
         block_sum(first_of && rank < most ? w : 0ull, all);
-        need = draw_ceil(p_in, all);
+        need = need_most = draw_ceil(p_in, all);
       }
       const bool kept = first_of && rank < most && (rank == 0 || (before < need && x >= lowest));
+      const bool open = first_of && rank > 0 && rank < most && before >= need && before < need_most && x >= lowest;
+      const bool sure = __syncthreads_count(open) == 0;
+      if (threadIdx.x == 0) sh.certain = sure;
       block_sum(kept ? w : 0ull, total);
       stay = __syncthreads_count(kept);
       if (first_of) own[i] = kept ? w : 0ull;
@@ -671,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
       }
       if (threadIdx.x == 0) sh.at = INT32_MAX;
       __syncthreads();
-      if (draw) {
+      if (draw && sure) {
         bool whole;
         const u64 thr = draw_threshold(p.u[n], total, whole);
         const uint32_t index = static_cast<uint32_t>(key);
@@ -719,14 +744,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
         mass += w[i];
       }
       u64 incl = block_scan(mass, all);
-      if (of_most) need = draw_ceil(p_in, all);
+      if (of_most) need = need_most = draw_ceil(p_in, all);
       // the sorted entries that stay: the first ones
       u64 before = incl - mass;
+      bool open = false;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         stay += at0 + i < kept && (at0 + i == 0 || (before < need && x[i] >= lowest));
+        open = open || (at0 + i < kept && before >= need && before < need_most && x[i] >= lowest);
         before += w[i];
       }
+      const bool sure = __syncthreads_count(open) == 0;
+      if (threadIdx.x == 0) sh.certain = sure;
       block_sum(static_cast<u64>(stay), all);
       stay = static_cast<int>(all);
       // their weight, and the entry at the border
@@ -746,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
       for (int i = 0; i < PER; ++i) places[i] = static_cast<uint32_t>(list[at0 + i]) << 11 | (at0 + i);
       __syncthreads();
       total = sh.total;
-      if (draw) {
+      if (draw && sure) {
         bool whole;
         const u64 thr = draw_threshold(p.u[n], total, whole);
         unsigned* order = reinterpret_cast<unsigned*>(own);   // 2048 words
@@ -799,73 +828,123 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
     total = weigh(m);
   } else {
     bool found = false;                // the border, through the list
-    u64 Z = 0ull;                      // the weight of all, where top-p has no top-k before it
+    u64 Z = 1ull << kOne;              // the weight that top-p takes a part of, or less
     // where no float lies below m (the lowest number), what has no weight cannot be raised to one
     const bool sums = weigh.low > -INFINITY, listed = want > 0 && sums && !(has_p && !has_k && looks_flat(m, upo, flo, weigh.scale(), p_in, V));
     if (listed) {
       // -------------------------------------------------------------- few candidates
-      // Entries from flo on go to the CTA's list, all CTAs' lists to the first one, which
-      // orders them and knows everything but the weight of the rest. Where the entries
-      // from upo on hold top-p's border, these are enough.
+      // Entries from a start on go to the CTA's list, all CTAs' lists to the first one, which
+      // orders them and knows everything but the weight of the rest. top-p tries the upper
+      // start first: a row's list of kHoped is short to make and to order (all in one list
+      // of kHopedMost: 1024 rows bf16 of a power law of exponent 2.1 207 instead of 182 us).
       const bool all_weigh = !has_k;
-      auto append = [&](const float* x, int v0) {
-        if (largest4(x) >= flo) {
+      const float mc = fabsf(m) * weigh.scale();
+      const bool near_by = mc < Weigh::kNear;
+      u64 need = ~0ull, need_most = ~0ull, near = 0ull;
+      unsigned listed_here = 0u;
+#pragma unroll 1
+      for (bool upper = all_weigh; ; upper = false) {
+        const float from = upper ? upo : flo;
+        auto append = [&](const float* x, int v0) {
+          if (largest4(x) >= from) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (x[i] >= flo) {
-              const unsigned at = atomicAdd(own_count, 1u);
-              if (at < kList) own[at] = static_cast<u64>(~key_of(x[i])) << 32 | static_cast<uint32_t>(v0 + i);
+            for (int i = 0; i < 4; ++i) {
+              if (x[i] >= from) {
+                const unsigned at = atomicAdd(own_count, 1u);
+                if (at < kList) own[at] = static_cast<u64>(~key_of(x[i])) << 32 | static_cast<uint32_t>(v0 + i);
+              }
             }
           }
+        };
+        if (upper) {
+          // The weight of all decides how much of it has to lie before the border. The sum
+          // in fp32 and a bound of its error tell the border unless it falls between two
+          // entries that so little parts; then all is weighed exactly.
+          float sum = 0.f;
+          u64 all, high = 0ull, rest = 0ull;
+          if (near_by) {
+            each([&](const float* x, int v0) {
+              sum += weigh.near4(x);
+              append(x, v0);
+            });
+          } else {
+            each([&](const float* x, int v0) {
+              weigh.add4(x, high, rest);
+              append(x, v0);
+            });
+          }
+          block_sum(near_by ? __float2ull_rn(sum * 0x1p43f) : (high << 21) + rest, all);
+          if (threadIdx.x == 0) sh.told.sum = all;
+        } else {
+          each(append);
         }
-      };
-      if (all_weigh) {
-        u64 sum = 0ull, low_sum = 0ull, all;
-        each([&](const float* x, int v0) {
-          weigh.add4(x, sum, low_sum);
-          append(x, v0);
-        });
-        block_sum((sum << 21) + low_sum, all);
-        if (threadIdx.x == 0) sh.told.sum = all;
-        const int len = min(static_cast<int>(*own_count), kList);
-        u64 above = 0ull, top_sum = 0ull;
-        for (int i0 = warp * 32; i0 < len; i0 += kThreads) {
-          const bool in = i0 + lane < len;
-          const float x = in ? value_of(~static_cast<uint32_t>(own[i0 + lane] >> 32)) : m;
-          const u64 w = weigh(x);
-          above += in ? w : 0ull;
-          top_sum += in && x >= upo ? w : 0ull;
+        __syncthreads();
+        if (all_weigh) {
+          const int len = min(static_cast<int>(*own_count), kList);
+          u64 above = 0ull, all;
+#pragma unroll 1
+          for (int i0 = warp * 32; i0 < len; i0 += kThreads) {
+            const bool in = i0 + lane < len;
+            const u64 w = weigh(in ? value_of(~static_cast<uint32_t>(own[i0 + lane] >> 32)) : m);
+            above += in ? w : 0ull;
+          }
+          block_sum(above, all);
+          if (threadIdx.x == 0) sh.told.listed = all;
         }
-        block_sum(above, all);
-        if (threadIdx.x == 0) sh.told.listed = all;
-        block_sum(top_sum, all);
-        if (threadIdx.x == 0) sh.told.upper = all;
-      } else {
-        each(append);
+        meet();
+        u64 has = 0ull;
+        listed_here = 0u;
+        if (lane < parts) {   // asked for together
+          listed_here = static_cast<unsigned>(ld_peer_u64(&sh.told.count, lane));
+          if (all_weigh) {
+            near = ld_peer_u64(&sh.told.sum, lane);
+            has = ld_peer_u64(&sh.told.listed, lane);
+          }
+        }
+        const unsigned len = __reduce_add_sync(kAll, listed_here);
+        found = len <= kList && (!has_k || len >= static_cast<unsigned>(k_in));
+        if (all_weigh) {
+          near = warp_sum(lane < parts ? near : 0ull);
+          // rounded once a group of four, and what the integers cut off
+          const float adds = static_cast<float>((all_rows / warps + 1) * (VEC / 4));
+          const u64 slack = __float2ull_ru(__ull2float_ru(near) * ((0.36f * mc + adds + 32.f) * 0x1p-24f)) + 2ull * V;
+          Z = near_by ? near - min(slack, near) : near;          // at least
+          need = draw_ceil(p_in, Z);
+          need_most = near_by ? draw_ceil(p_in, near + slack) : need;
+          const bool enough = warp_sum(has) >= need_most;
+          if (upper && !enough && len <= kList) {   // once more, for more entries
+            left();
+            settle();
+            if (threadIdx.x == 0) sh.told.count = 0ull;
+            __syncthreads();
+            continue;
+          }
+          found = found && enough;
+        }
+        break;
       }
-      if (threadIdx.x == 0) sh.len = 0;
-      meet();
-      const unsigned c = lane < parts ? static_cast<unsigned>(ld_peer_u64(&sh.told.count, lane)) : 0u;
-      const unsigned all_len = __reduce_add_sync(kAll, c);
-      found = all_len <= kList && (!has_k || all_len >= static_cast<unsigned>(k_in));
-      u64 need = ~0ull;
-      float from = flo;
-      if (all_weigh) {
-        Z = warp_sum(lane < parts ? ld_peer_u64(&sh.told.sum, lane) : 0ull);
-        const u64 has = warp_sum(lane < parts ? ld_peer_u64(&sh.told.listed, lane) : 0ull);
-        const u64 high = warp_sum(lane < parts ? ld_peer_u64(&sh.told.upper, lane) : 0ull);
-        need = draw_ceil(p_in, Z);
-        found = found && has >= need;
-        if (high >= need) from = upo;
-      }
-      if (found && part == 0) {
-        pull(c, all_len, ~key_of(from));
-      }
+      if (found && part == 0) pull(listed_here);
       left();
       if (found && part == 0) {
         __syncthreads();
-        order(has_k ? k_in : kList, has_k && has_p, need, least, p.tokens != nullptr);
-        if (probs != nullptr) send();
+        order(has_k ? k_in : kList, has_k && has_p, need, need_most, least, p.tokens != nullptr);
+        if (all_weigh && threadIdx.x < parts) st_peer_u32(&sh.sure, threadIdx.x, sh.certain);   // the ordering warp itself
+      }
+      if (found && all_weigh) {
+        meet();   // nobody leaves before the border is sure
+        if (sh.sure == 0u) {
+          u64 sum = 0ull, low_sum = 0ull, before;
+          each([&](const float* x, int) { weigh.add4(x, sum, low_sum); });
+          join(warp_sum((sum << 21) + low_sum), before, Z);
+          if (part == 0) {
+            need = draw_ceil(p_in, Z);
+            order(kList, false, need, need, least, p.tokens != nullptr);
+          }
+        }
+      }
+      if (found && part == 0 && probs != nullptr) {
+        __syncthreads();
+        send();
       }
       if (found && probs != nullptr) {
         meet();
@@ -940,21 +1019,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
               v[0] += c[k].x; v[1] += c[k].y; v[2] += c[k].z; v[3] += c[k].w;
             }
           } else {
-            u64 c[4], a0[4], a1[4], a2[4];
+            u64 c[4], a0[4], a1[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const bool in = r0 + k < parts;
               c[k] = in && counted ? ld_peer_u64(hist + b0, r0 + k) : 0ull;
               a0[k] = in ? ld_peer_u64(hist + kMassBins + b0, r0 + k) : 0ull;
               a1[k] = in ? ld_peer_u64(hist + 2 * kMassBins + b0, r0 + k) : 0ull;
-              a2[k] = in ? ld_peer_u64(hist + 3 * kMassBins + b0, r0 + k) : 0ull;
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               cnt[0] += static_cast<unsigned>(c[k]);
               cnt[1] += static_cast<unsigned>(c[k] >> 32);
-              v[0] += (a0[k] & kAll) + ((a1[k] & kAll) << 14) + ((a2[k] & kAll) << 29);
-              v[1] += (a0[k] >> 32) + ((a1[k] >> 32) << 14) + ((a2[k] >> 32) << 29);
+              v[0] += (a0[k] & kAll) + (a1[k] << 32);
+              v[1] += (a0[k] >> 32) + (a1[k] & 0xffffffff00000000ull);
             }
           }
         }
@@ -1034,7 +1112,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
       // top-p: levels of weights
       if (has_p) {
         const Border from = keep;
-        const bool unknown = !has_k && !listed;   // Z is: weighed with the first level
         if (has_k) {
           u64 sum = 0ull, before;
           each([&](const float* x, int v0) {
@@ -1049,9 +1126,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
           });
           join(warp_sum(sum), before, Z);
         }
-        u64 need = unknown ? 0ull : draw_ceil(p_in, Z);
-        // entries below this one weigh less than 1 - p of all together (or of the largest)
-        const float y0 = log2f(static_cast<float>(V) / ((1.f - fmaxf(p_in, 0.f)) * (unknown ? 0x1p43f : __ull2float_rn(Z)))) + kOne + 0.25f;
+        u64 need = draw_ceil(p_in, Z);        // without top-k known after the first level
+        // entries below this one weigh less than 1 - p of all together
+        const float y0 = log2f(static_cast<float>(V) / ((1.f - fmaxf(p_in, 0.f)) * __ull2float_rn(Z))) + kOne + 0.25f;
         const float cut = fmaxf(fmaxf(__fsub_rd(m, y0 / weigh.scale() * 1.0001f), -FLT_MAX), from.thr);
         uint32_t lo = key_of(cut), hi = key_of(m);
         const float scale = linear_scale(cut, kMassBins);
@@ -1062,7 +1139,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
           int step = max(0, 32 - __clz(hi - lo) - 10);
           if (step <= P::kFinal) step = P::kFinal;
           clear(kHistInts);
-          const bool all_of = linear && unknown;
+          const bool all_of = linear && !has_k;
           u64 sum = 0ull;
           each([&](const float* x, int v0) {
             if (__any_sync(kAll, all_of || largest4(x) >= a)) {
@@ -1075,9 +1152,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
                 const unsigned bin = linear ? linear_bin(x[i], scale) : (hi - key_of(x[i])) >> step;
                 if (x[i] >= a && x[i] <= b && from.keeps(x[i], v0 + i) && bin < kMassBins) {
                   if (!linear) atomicAdd(&hist[bin], 1u);
-                  atomicAdd(&hist[kMassBins + bin], static_cast<unsigned>(w[i]) & 0x3FFFu);
-                  atomicAdd(&hist[2 * kMassBins + bin], static_cast<unsigned>(w[i] >> 14) & 0x7FFFu);
-                  atomicAdd(&hist[3 * kMassBins + bin], static_cast<unsigned>(w[i] >> 29));
+                  // 64 bits in two words: the lower one's old value tells the carry (3 cycles an
+                  // SM each, where a 64-bit addition in shared memory takes 20 and more)
+                  const unsigned low = static_cast<unsigned>(w[i]), old = atomicAdd(&hist[kMassBins + bin], low);
+                  atomicAdd(&hist[2 * kMassBins + bin], static_cast<unsigned>(w[i] >> 32) + (old + low < old));
                 }
               }
             }
@@ -1108,10 +1186,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
             // the bin's entries, if they fit the list: their order tells the border
             linear = false;
             settle();
-            if (threadIdx.x == 0) {
-              sh.told.count = 0ull;
-              sh.len = 0;
-            }
+            if (threadIdx.x == 0) sh.told.count = 0ull;
             __syncthreads();
             const float first_in = value_of(lo), last_in = value_of(hi);
             each([&](const float* x, int v0) {
@@ -1128,12 +1203,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
             const unsigned c = lane < parts ? static_cast<unsigned>(ld_peer_u64(&sh.told.count, lane)) : 0u;
             const unsigned all_len = __reduce_add_sync(kAll, c);
             const bool fits = all_len <= kList;
-            if (fits && part == 0) pull(c, all_len, kAll);
+            if (fits && part == 0) pull(c);
             left();
             if (fits) {
               if (part == 0) {
                 __syncthreads();
-                order(kList, false, need - under, -FLT_MAX, false);
+                order(kList, false, need - under, need - under, -FLT_MAX, false);
+                __syncthreads();
                 send();
               }
               meet();
@@ -1166,13 +1242,33 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
       if (p.tokens != nullptr) {
         bool whole;
         const u64 thr = draw_threshold(p.u[n], total, whole);
-        if (cum <= thr && thr - cum < sum) {   // one warp of the cluster
-#pragma unroll 1
-          for (int r = 0; r < my_rows; ++r) {
+        // The warp whose range holds the threshold, in one CTA; that range's rows divided
+        // over all its warps, then the one of these (a warp alone, its 74 rows one after
+        // another: 1024 rows of 151936 bf16 entries 265 instead of 223 us).
+        const bool here = cum <= thr && thr - cum < sum;
+        if (threadIdx.x == 0) sh.at = -1;
+        __syncthreads();
+        if (here && lane == 0) {
+          sh.at = warp;
+          sh.above = cum;
+        }
+        __syncthreads();
+        const int of = sh.at;
+        if (of >= 0) {
+          const int of_id = part * kWarps + of, of_row0 = static_cast<int>(static_cast<unsigned>(all_rows) * of_id / warps);
+          const int of_rows = static_cast<int>(static_cast<unsigned>(all_rows) * (of_id + 1) / warps) - of_row0;
+          const int r0 = of_rows * warp / kWarps, r1 = of_rows * (warp + 1) / kWarps;
+          u64 w[VEC];
+          auto weigh_row = [&](int r, int& v0) -> u64 {   // this lane's piece: its weights, their sum
+            const int at = (of_row0 + r) * 32 + lane;
+            uint4 q = make_uint4(0u, 0u, 0u, 0u);
+            if (held) q = s_data[(of * rows + r) * 32 + lane];
+            else if (at < pieces) q = clean(__ldg(base + at), at, true);
+            else q = clean(q, at, true);
             float x[VEC];
-            piece(r, x);
-            const int v0 = (first + r * 32 + lane) * VEC - shift;
-            u64 w[VEC], own_sum = 0ull;
+            P::get(q, x);
+            v0 = at * VEC - shift;
+            u64 own_sum = 0ull;
 #pragma unroll
             for (int i = 0; i < VEC; i += 2) weigh.two(x[i], x[i + 1], w[i], w[i + 1]);
 #pragma unroll
@@ -1180,21 +1276,36 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
               if (!keep.keeps(x[i], v0 + i)) w[i] = 0ull;
               own_sum += w[i];
             }
-            const u64 incl = warp_scan(own_sum, lane);
-            const unsigned hit = __ballot_sync(kAll, cum + incl > thr);
-            if (hit != 0u) {
-              u64 c = cum + incl - own_sum;
-              int k = 0;
+            return own_sum;
+          };
+          u64 part_sum = 0ull;
+          int v0;
+#pragma unroll 1
+          for (int r = r0; r < r1; ++r) part_sum += weigh_row(r, v0);
+          part_sum = warp_sum(part_sum);
+          if (lane == 0) sh.warp[0][warp] = part_sum;
+          __syncthreads();
+          u64 c0 = sh.above + warp_sum(lane < warp ? sh.warp[0][lane % kWarps] : 0ull);
+          if (c0 <= thr && thr - c0 < part_sum) {
+#pragma unroll 1
+            for (int r = r0; r < r1; ++r) {
+              const u64 own_sum = weigh_row(r, v0);
+              const u64 incl = warp_scan(own_sum, lane);
+              const unsigned hit = __ballot_sync(kAll, c0 + incl > thr);
+              if (hit != 0u) {
+                u64 c = c0 + incl - own_sum;
+                int k = 0;
 #pragma unroll
-              for (int i = 0; i < VEC; ++i) {
-                c += w[i];
-                k += c <= thr;
+                for (int i = 0; i < VEC; ++i) {
+                  c += w[i];
+                  k += c <= thr;
+                }
+                const int token = __shfl_sync(kAll, v0 + k, __ffs(static_cast<int>(hit)) - 1);
+                if (lane == 0) p.tokens[n] = token;
+                break;
               }
-              const int token = __shfl_sync(kAll, v0 + k, __ffs(static_cast<int>(hit)) - 1);
-              if (lane == 0) p.tokens[n] = token;
-              break;
+              c0 += __shfl_sync(kAll, incl, 31);
             }
-            cum += __shfl_sync(kAll, incl, 31);
           }
         }
       }

@@ -199,6 +199,29 @@ def test_a_large_vocabulary(dfl):
         check(dfl, logits(3, V, dtype, 41), uniforms(3, 41), T=[1.0, 0.8, 1.5], k=[0, 100, 0], p=[1.0, 0.9, 0.8])
 
 
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+def test_equal_and_flat_rows_of_one_block_each(dfl, dtype):
+    """Large batches: a block a row, whose lists and bins overflow: 151936 equal entries, few values, even weights."""
+    N, V = 310, 151936
+    x = torch.zeros((N, V), dtype=dtype, device="cuda")
+    x[1::3] = logits(1, V, F32, 71, "normal")[0].round().to(dtype)
+    x[2::3] = logits(1, V, dtype, 72, "normal")[0] * 0.01
+    x[5, 70000:] = -float("inf")
+    r = np.random.default_rng(71)
+    s = dict(T=[1.0] * N, k=r.choice([0, 0, 1300, 90000, 151935], N).tolist(), p=r.choice([0.3, 0.77, 0.9999, 1.0], N).tolist())
+    u = uniforms(N, 73)
+    tok, pr, st = run(dfl, x, u, **s)
+    alone, _, _ = run(dfl, x, u, **s, probs=False)
+    assert st == 0 and tok == alone
+    f32 = lambda v: float(np.float32(v))  # noqa: E731
+    for n in list(range(0, 24)) + [304, 305, 309]:
+        want = tt.shape(x[n].double().cpu().numpy(), 1.0, s["k"][n], f32(s["p"][n]))
+        assert ((pr[n] > 0) == (want > 0)).all(), n
+        assert (np.abs(pr[n] - want) <= 2.0 ** -22 * 1.01 * want + 2.0 ** -43).all()
+        y = tt.draw(want, f32(u[n]))
+        assert tok[n] == y or abs(np.cumsum(want)[min(tok[n], y)] - f32(u[n])) <= 2.0 ** -27, (n, tok[n], y)
+
+
 def test_many_rows(dfl):
     N, V = 3000, 1500
     x = logits(N, V, BF, 43)
