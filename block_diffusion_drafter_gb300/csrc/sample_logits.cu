@@ -16,18 +16,26 @@
 // along the prefix), 4e-7 for 151936 entries; fp32 weights would give 1e-3 from the
 // exponent's rounding alone.
 //
-// A row belongs to a cluster of CTAs, each of which keeps a contiguous part of it
-// in shared memory, each warp a contiguous part of that: logits are read from HBM
-// once. What a row asks for decides how much follows, always the same for a cluster:
+// A row belongs to a cluster of one to 16 CTAs, each warp takes a contiguous part. The
+// first pass reads it from HBM; what follows reads it again from shared memory, where
+// that holds it (few rows), or from L2. What a row asks for decides how much follows,
+// always the same for all CTAs of a cluster:
 //   the largest entry (temperature 0, top-k 1): one exchange of the CTAs' maxima;
 //   top-k up to kMostListed, and top-p: a lower bound of the border from the maxima of
-//     the threads' entries, which leaves some k, or some hundreds, of candidates. The
-//     first CTA sorts these and finds border and token by itself;
+//     the threads' entries, which leaves some k, or some tens or hundreds, of candidates.
+//     The first CTA orders these and finds border and token by itself. What top-p takes a
+//     part of, the weight of all, is summed in fp32 with a bound of the error;
 //   neither: the weights' sums a warp, and the warp that holds the threshold;
 //   where the candidates do not fit the list or do not hold the border (flat rows, many
-//     equal entries, a large k): histograms over the bits of the values, counts for
-//     top-k, weights for top-p, added over the cluster through distributed shared
-//     memory, the border's bin taken apart further until it holds one entry or value.
+//     equal entries, a large k): histograms over the values, counts for top-k, weights for
+//     top-p, added over the cluster through distributed shared memory, the border's bin
+//     put in order, or taken apart further until it holds one entry or one value.
+// us for rows of 151936 entries, bytes at a copy's rate first: 1 row bf16, top-k 20 and
+// top-p 0.95, 0.05 / 12.9 (latency: four exchanges of 1.5 us between CTAs and the order of
+// 40 candidates); 64 rows f32 5.8 / 20.9; 272 rows f32 24.7 / 63.9; 1024 rows bf16 46.6 / 126,
+// the largest entry alone 64; top-p 0.95 alone, temperature 0.7, 293, one row in twenty
+// flat and weighed twice; neither 223 (the weights: 16 cycles an entry and SM quarter where
+// nothing else runs).
 #include <cuda_bf16.h>
 #include <float.h>
 
@@ -43,11 +51,16 @@ constexpr int kCountBins = 2048, kMassBins = 1024;
 constexpr int kHistInts = 3 * kMassBins;   // of weights: counts, lower and upper words
 constexpr int kList = 2048;          // candidates of a CTA, and of a row: 32 KB
 constexpr int kMostListed = 1280;    // top-k borders that the list is made for
-constexpr int kHoped = 64, kHopedMost = 1280;   // candidates among which top-p's border is looked for, and then
-constexpr int kCounted = 192;        // candidates whose ranks are counted; more are sorted
+// Candidates among which top-p's border is looked for, and then. (1280 instead of 640: 16
+// / 64 rows bf16 at temperature 0.7 46 / 60 instead of 35 / 52 us, 1024 rows 315 instead of
+// 293; 272 rows f32, where one row's border decides, 143 instead of 161.)
+constexpr int kHoped = 64, kHopedMost = 640;
+// Candidates whose ranks are counted, all with all; more are sorted. (Up to 512: 300 rows
+// with top-k 400 89 instead of 58 us.)
+constexpr int kCounted = 192;
 constexpr int kScratchBytes = 2 * kList * 8;   // the lists, or the histograms
 constexpr int kInFlight = 5;         // 16-byte loads a thread, first pass
-constexpr int kAgain = 2;            // and later ones
+constexpr int kAgain = 2;            // and later ones (4: 1024 rows weighed whole 281 instead of 265 us, registers)
 constexpr int kOne = 43;             // the largest weight is 2^43
 typedef unsigned long long u64;
 constexpr unsigned kAll = 0xffffffffu;
@@ -307,8 +320,8 @@ struct Weigh {
 // through the weights of the 1st, the kHoped-th and the kHopedMost-th has it (such rows
 // go to the histograms at once). A guess: either way gives the same result.
 __device__ __forceinline__ bool looks_flat(float m, float upo, float flo, float c, float p, int V) {
-  constexpr float kLogHoped = 6.f, kLogMost = 4.321928f;     // log2 of kHoped, of kHopedMost / kHoped
-  static_assert(kHoped == 64 && kHopedMost == 1280, "their logarithms");
+  constexpr float kLogHoped = 6.f, kLogMost = 3.321928f;     // log2 of kHoped, of kHopedMost / kHoped
+  static_assert(kHoped == 64 && kHopedMost == 640, "their logarithms");
   const float y1 = fminf((m - upo) * c, 60.f), y2 = fminf((upo - flo) * c, 60.f);
   // the sum of r^-s from r = 1 to 2^l, as an integral
   auto area = [](float s, float l) {
@@ -723,8 +736,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
                 v[b] = x;
               }
             }
-            __syncthreads();
+            // up to a distance of 32 a warp stays within its 64 entries
+            if (j > 32 || (j == 1 && k > 32)) __syncthreads(); else __syncwarp();
           }
+        __syncthreads();
       };
       for (int i = len + threadIdx.x; i < kList; i += kThreads) list[i] = ~0ull;
       sort(list, len);
@@ -1368,6 +1383,9 @@ cudaError_t launch_typed(const DrawArgs& a, cudaStream_t s, bool pdl) {
   // CTAs a row: as many as find room at once, two an SM, while each warp has two rows of
   // 16-byte pieces; at least as many as keep what is read again within L2 (96 MB for
   // the rows under way). Clusters of 16 find no room beside one another: only for few rows.
+  // (Twice as many, in two rounds: 64 rows bf16 with top-k 20 27.6 instead of 17.6 us, 272
+  // rows f32 75 instead of 64; rows of all kinds, where the flat ones decide, 54.7 / 54.9
+  // and 155 / 200.)
   const long long slots = 2LL * num_sms_of_current_device();
   const long long row_bytes = 16LL * pieces;
   int parts = 1;
