@@ -51,7 +51,7 @@ dflash_status dflash_tree_masks(const int32_t* parents, const int32_t* cu_rows, 
   if (parents == nullptr || cu_rows == nullptr || mask == nullptr || dev_status == nullptr ||
       (positions != nullptr && ctx_len == nullptr) || !trace_ok(trace))
     return DFLASH_ERR_INVALID_ARG;
-  if (T > INT32_MAX - 1024) return DFLASH_ERR_TOO_LARGE;
+  if (T > INT32_MAX - 1024 || mask_words > INT32_MAX / 32) return DFLASH_ERR_TOO_LARGE;
   const dflash_status st = check_arch();
   if (st != DFLASH_OK) return st;
   const MaskArgs a{parents, cu_rows, ctx_len, B, T, mask_words, mask, positions, dev_status};
@@ -71,11 +71,15 @@ dflash_status dflash_sample(const void* logits, dflash_dtype logits_dtype, long 
   if (N < 0 || V < 1 || ld < V) return DFLASH_ERR_INVALID_ARG;
   if (N == 0) return DFLASH_OK;
   if (logits == nullptr || dev_status == nullptr || (tokens == nullptr) != (u == nullptr) ||
-      (tokens == nullptr && probs == nullptr) || logits == probs || !trace_ok(trace))
+      (tokens == nullptr && probs == nullptr) || !trace_ok(trace))
     return DFLASH_ERR_INVALID_ARG;
   const int es = logits_dtype == DFLASH_BF16 ? 2 : 4;
   if (!aligned(logits, es) || !aligned(probs, 4)) return DFLASH_ERR_ALIGN;
   if (N > (1 << 20) || V > kDrawMaxVocab) return DFLASH_ERR_TOO_LARGE;
+  if (probs != nullptr) {   // rows of logits are read again after others' distributions are written
+    const uintptr_t x = reinterpret_cast<uintptr_t>(logits), y = reinterpret_cast<uintptr_t>(probs);
+    if (y < x + (static_cast<uintptr_t>(N - 1) * ld + V) * es && x < y + static_cast<uintptr_t>(N) * V * 4) return DFLASH_ERR_INVALID_ARG;
+  }
   const dflash_status st = check_arch();
   if (st != DFLASH_OK) return st;
   const DrawArgs a{logits, ld, es == 2, N, V, temperature, top_k, top_p, min_p, u, tokens, probs, dev_status};

@@ -631,7 +631,8 @@ dflash_status dflash_verify_probs(const dflash_config* cfg, const void* target_p
  *   written. positions: device [T], or NULL (ctx_len may then be NULL).
  * A parent that is not below its node counts as none, and a node from
  *   32 * mask_words on has no bit of its own; both set DFLASH_ERR_INVALID_ARG in
- *   dev_status. T == 0 or B == 0 launches nothing. */
+ *   dev_status. mask_words < 2^26, else DFLASH_ERR_TOO_LARGE. T == 0 or B == 0
+ *   launches nothing. */
 dflash_status dflash_tree_masks(const int32_t* parents, const int32_t* cu_rows, const int32_t* ctx_len, int B,
                                 int T, int mask_words, uint32_t* mask, int32_t* positions, int32_t* dev_status,
                                 dflash_trace* trace, dflash_stream_t stream);
@@ -641,8 +642,9 @@ dflash_status dflash_tree_masks(const int32_t* parents, const int32_t* cu_rows, 
  * bit j of mask[t] is set (j below the sequence's rows; bits behind them and
  * keys behind 32 * mask_words are not seen). Any mask is allowed, not only
  * those of trees; a row that sees no key gives zeros. mask: device
- * [T, mask_words], mask_words >= 1. Other arguments, workspace and errors as
- * there. */
+ * [T, mask_words], 1 <= mask_words < 2^26. Other arguments, workspace and errors
+ * as there; key and value rows below ctx_len[b] + n_b must be finite here too,
+ * also those that no row's mask names (they are multiplied by a zero weight). */
 dflash_status dflash_attention_tree_paged(const dflash_heads* heads, const void* q, long long ld_q,
                                           const int32_t* cu_rows, const int32_t* ctx_len, int B, int T,
                                           int max_rows, int max_ctx_hint, int layer,
@@ -665,7 +667,8 @@ dflash_status dflash_attention_tree_paged(const dflash_heads* heads, const void*
  *   (the lowest index on ties). top_k < 1, top_p >= 1 (or NaN) and min_p <= 0
  *   (or NaN) are off; min_p above 1 counts as 1; u is taken in [0, 1).
  * tokens: device int32 [N] with u, or both NULL; probs: device fp32 [N, V] or
- *   NULL (dflash_verify_probs takes it for target_probs); one of the two.
+ *   NULL (dflash_verify_probs takes it for target_probs); one of the two. The
+ *   memory of probs must not overlap that of logits (DFLASH_ERR_INVALID_ARG).
  * -inf and NaN logits have no weight; +inf counts as the largest finite number.
  *   A row of nothing else, and a temperature that is negative or NaN, set
  *   DFLASH_ERR_INVALID_ARG in dev_status and give token 0 and a row of zeros.

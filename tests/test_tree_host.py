@@ -173,6 +173,25 @@ def test_the_binding_refuses_what_the_library_cannot_see(lib, heads):
 
 
 # ------------------------------------------------------------------ the oracle's definitions
+def test_wide_masks_and_overlapping_rows_are_refused(lib, heads):
+    """Masks whose bits pass 31 bits, and distributions written over logits that are still read."""
+    word = lib.load().dflash_tree_masks(FAKE, FAKE, FAKE, 1, 1, 1 << 26, FAKE, FAKE, FAKE, None, None)
+    tree = lib.load().dflash_attention_tree_paged(ref(heads), FAKE, 1024, FAKE, FAKE, 1, 1, 1, 9, 0, ref(pages_of(lib)), FAKE, 1 << 26,
+                                                  0.0, 2 * FAKE, 1024, FAKE, FAKE, 1 << 40, None, None)
+    assert word == tree == lib.ERR_TOO_LARGE
+
+    def sample(probs, dt=lib.F32, ld=100):
+        return lib.load().dflash_sample(FAKE, dt, ld, 3, 100, None, None, None, None, FAKE, FAKE, probs, FAKE, None, None)
+
+    for probs in (FAKE, FAKE + 4, FAKE + 1196, FAKE - 1196):
+        assert sample(probs) == lib.ERR_INVALID_ARG, probs - FAKE
+    assert sample(FAKE + 596, lib.BF16) == sample(FAKE + 2000, ld=250) == lib.ERR_INVALID_ARG
+    # side by side: nothing to refuse (no GPU of the right kind here, or these addresses would be read)
+    if not torch.cuda.is_available():
+        for call in (sample(FAKE + 1200), sample(FAKE - 1200), sample(FAKE + 600, lib.BF16)):
+            assert call not in (lib.ERR_INVALID_ARG, lib.ERR_ALIGN, lib.OK)
+
+
 def test_shaped_distributions_by_plain_counting():
     r = np.random.default_rng(0)
     for _ in range(200):
