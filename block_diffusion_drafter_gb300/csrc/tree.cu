@@ -83,7 +83,9 @@ __global__ void __launch_bounds__(kMaskThreads) tree_masks_kernel(const MaskArgs
 // is one shared-memory read a node. Then each warp moves the branch's rows in one
 // (layer, head, keys or values) after another. Rows only move down: path[j] >= j,
 // and a row's source lies above every row written before, so kBatch rounds of rows
-// are read, then written, with nothing kept aside.
+// are read, then written, with nothing kept aside. Bound by latency for one sequence
+// (36 layers, 8 heads of 128: 2.1 us); 32 of them move 19 MB in 8.6 us, a third of a
+// copy's rate: each block first goes through offsets, tokens, path and pages.
 constexpr int kTreeThreads = 256, kTreeWarps = kTreeThreads / 32;
 constexpr int kMaxPath = DFLASH_MAX_TREE;
 constexpr int kBatch = 8;
