@@ -169,6 +169,23 @@ def test_temperatures_and_uniforms_at_their_ends(dfl):
         assert st == dfl.ERR_INVALID_ARG and tok[3] == 0 and not pr[3].any() and pr[2].any()
 
 
+@pytest.mark.parametrize("V", [28, 1000, 5000])
+@pytest.mark.parametrize("T", [0.69, 0.71, 1.38, 1.42, 2.84, 5.0, 5.52, 5.68, 11.04, 11.36])
+def test_equal_entries_far_from_zero(dfl, T, V):
+    """Equal entries have equal weights whatever an exponent rounds to, so that exactly p V of them are p of the weight; at
+    these temperatures log2(e) / T lies far from the float next to it, at these values that counts most."""
+    vals = [s * f * T / 1.4427 for f in (30, 100, 250, 500, 900, 1000) for s in (1, -1)]
+    p = [0.25, 0.5, 0.75]
+    x = torch.tensor(vals, device="cuda").repeat_interleave(3)[:, None].expand(-1, V).contiguous()
+    N = x.shape[0]
+    tok, pr, st = run(dfl, x, [0.999] * N, T=[T] * N, p=p * len(vals))
+    assert st == 0
+    for n in range(N):
+        k = int(V * p[n % 3])
+        assert (pr[n, :k] > 0).all() and not pr[n, k:].any(), (n, vals[n // 3], p[n % 3], (pr[n] > 0).sum(), k)
+        assert tok[n] == int(k * float(np.float32(0.999)))
+
+
 def test_settings_that_are_off(dfl):
     V, N = 2000, 6
     x, u = logits(N, V, F32, 29), uniforms(N, 29)
