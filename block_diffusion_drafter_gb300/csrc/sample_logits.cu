@@ -200,8 +200,9 @@ __device__ __forceinline__ u64 both(float x) { return pair2(x, x); }
 // (so that no weight is below its value), and r below is raised by 2^-8.
 // c = log2(e) / T in two floats; z = x c - M with M that rounded maximum; 32 z's
 // floor i comes from one multiply-add rounded down onto 1.5 2^23 (without c's low
-// part, which 2^-8 covers, so that r stays positive); r = z - i / 32 + 2^-8 < 0.036
-// is one exact sum rounded once, and the low part added: off by 2^-29 at most.
+// part: 1.23 2^-24 of x c, 0.0024 at most, which 2^-8 covers, so that r stays
+// positive); r = z - i / 32 + 2^-8 < 0.038 is one exact sum rounded once, and the low
+// part added: off by 2^-29 at most.
 // 2^z = 2^(i >> 5) 2^((i & 31) / 32) 2^r: the second factor from a table whose entries
 // the lanes hold (a shuffle looks it up: no bank conflicts, where shared memory has
 // three lanes a bank), as a float and a relative rest; the third 1 + q by the
@@ -209,9 +210,10 @@ __device__ __forceinline__ u64 both(float x) { return pair2(x, x); }
 // power of two (exact), l = h (q + rest), rounded. As an integer: adding 2 to h and l
 // under rounding towards zero leaves their multiples of 2^-22 in the sums' bits; what
 // is cut off of both, added, likewise gives the multiple of 2^-43.
-// Entries below `low` have no weight and are raised to it; where m c is so large that
-// x c would lose r, every entry with a weight lies within a factor of two of m: x - m
-// is then exact and takes x's place (base). Two entries at once, nearly all of it
+// Entries below `low` have no weight and are raised to it; where |m c| is 32768 or more,
+// every entry with a weight lies within a factor of two of m: x - m is then exact and
+// takes x's place (base). (Below that |x c| < 32768 + 47, so that multiples of 2^-8 like
+// M - i / 32 are floats; from 65536 on they are not.) Two entries at once, nearly all of it
 // on the multiply-add pipe (16 cycles an entry and SM quarter, bound by that pipe and
 // the shuffles; integer shifts, selects and conversions take 2 to 8 cycles each, and a
 // sum of 64-bit shifted integers took 1024 rows of bf16 from 265 to 315 us).
@@ -237,7 +239,7 @@ struct Weigh {
       d = 0.f;
     }
     low = __fsub_rd(m, 46.f / c);
-    const float base = fabsf(m) * c < 65536.f ? 0.f : m;
+    const float base = fabsf(m) * c < 32768.f ? 0.f : m;
     const float top = floorf((m - base) * c * 32.f) * 0.03125f;
     ch32 = both(32.f * c);
     ch = both(c);

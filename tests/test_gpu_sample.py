@@ -297,3 +297,30 @@ def test_empty_and_traced(dfl):
     rec = dfl.TraceRecorder(2)
     run(dfl, logits(3, 500, BF, 61), uniforms(3, 61), trace=rec.struct)
     assert [(k, b) for k, b, _, _ in rec.records()] == [(dfl.K_VERIFY, 3.0 * 500 * 6)]
+
+
+def spread(at, side, T, V, wide, seed):
+    """Rows [len(at), V] whose maxima m have |m| log2(e) / T = at, on one side of zero; the others lie below them by
+    T `wide` times an exponential value."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    m = torch.tensor(at, dtype=torch.float64, device="cuda")[:, None] * (side * float(np.float32(T)) / 1.4426950408889634)
+    below = torch.empty((len(at), V), dtype=torch.float64, device="cuda").exponential_(generator=g) * (wide * T)
+    below.scatter_(1, torch.randint(V, (len(at), 1), generator=g, device="cuda"), 0.0)
+    return (m - below).float()
+
+
+@pytest.mark.parametrize("wide", [1.6, 0.6], ids=["peaked", "flat"])
+@pytest.mark.parametrize("T", [1e-3, 0.7, 1.0, 1e4])
+def test_maxima_in_every_range_of_the_weights(dfl, T, wide):
+    """Weights reduce x log2(e) / T, or (x - m) log2(e) / T from 32768 on; up to 1024 their sum may be fp32. fp32 rows on
+    each side of these and of 65536 (where a multiple of 2^-8 stops being a float), at maxima of either sign."""
+    at = [900, 1020, 1030, 5000, 16384, 30000, 32700, 32760, 32767, 32769, 32800, 40000, 65400, 65480, 65500, 65520, 65530, 65540, 65560,
+          65600, 1e5, 1e6]
+    N = len(at)
+    for side in (1, -1):
+        x = spread(at, side, T, 3001, wide, 83)
+        u = uniforms(N, 84)
+        for s in (dict(), dict(p=[0.9] * N), dict(p=[0.6] * N, m=[1e-3] * N), dict(k=[40] * N, p=[0.95] * N), dict(k=[2000] * N, p=[0.7] * N)):
+            check(dfl, x, u, T=[T] * N, **s)
+    x = spread(at[8:18], -1, T, 60013, wide, 85)
+    check(dfl, x, uniforms(10, 86), T=[T] * 10, p=[0.9] * 10)
