@@ -324,3 +324,20 @@ def test_maxima_in_every_range_of_the_weights(dfl, T, wide):
             check(dfl, x, u, T=[T] * N, **s)
     x = spread(at[8:18], -1, T, 60013, wide, 85)
     check(dfl, x, uniforms(10, 86), T=[T] * 10, p=[0.9] * 10)
+
+
+@pytest.mark.parametrize("V", [28, 1000, 5000])
+@pytest.mark.parametrize("T", [0.72108847, 1.4421769, 2.8843539, 5.7687078, 11.537416, 2.79, 5.71])
+def test_equal_entries_at_temperatures_whose_factor_lies_farthest_off(dfl, T, V):
+    """As above where log2(e) / T lies up to 1.22 half steps above the float that the fp32 sum multiplies by: its own
+    rounding, and that of log2(e)."""
+    vals = [s * f * T / 1.442696 for f in (300, 700, 980, 1010, 1020, 1023) for s in (1, -1)]
+    p = [0.25, 0.5, 0.75]
+    x = torch.tensor(vals, device="cuda").repeat_interleave(3)[:, None].expand(-1, V).contiguous()
+    N = x.shape[0]
+    tok, pr, st = run(dfl, x, [0.999] * N, T=[T] * N, p=p * len(vals))
+    assert st == 0
+    for n in range(N):
+        k = int(V * p[n % 3])
+        assert (pr[n, :k] > 0).all() and not pr[n, k:].any(), (n, vals[n // 3], p[n % 3], (pr[n] > 0).sum(), k)
+        assert tok[n] == int(k * float(np.float32(0.999)))
