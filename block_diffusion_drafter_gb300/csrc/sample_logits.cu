@@ -223,9 +223,13 @@ struct Weigh {
   float hi, lo;              // this lane's table entry
   static constexpr float kMagic = 12582912.f;         // 1.5 2^23, bits 0x4B400000
   static constexpr unsigned kTwo = 0x40000000u;       // 2.0
-  // c in two floats
+  // Temperatures outside 2^-100 .. 2^100 count as these (c's low part would lose bits); an
+  // infinite one is its own.
+  static __device__ __forceinline__ float inside(float T) { return isinf(T) ? T : fminf(fmaxf(T, 0x1p-100f), 0x1p100f); }
+  // c in two floats, T inside. T infinite: 0, so that all weights are equal (then `low` is
+  // -inf and -inf times c NaN: entries of -inf have to be left out by the caller).
   static __device__ __forceinline__ float2 factor(float T) {
-    T = fminf(fmaxf(T, 0x1p-100f), 0x1p100f);
+    if (isinf(T)) return make_float2(0.f, 0.f);
     constexpr float kLh = 1.44269502162933349609375f, kLl = 1.92596303350e-8f;   // log2(e)
     const float c = __fdiv_rn(kLh, T);
     return make_float2(c, __fdiv_rn(__fmaf_rn(-c, T, kLh) + kLl, T));
@@ -466,11 +470,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
   const float min_p = p.min_p != nullptr ? p.min_p[n] : 0.f;
   const bool has_min = min_p > 0.f, has_k = k_in > 0 && k_in < V, has_p = p_in < 1.f;
   const bool greedy = T_in == 0.f || k_in == 1;
-  const float2 c_log2e = Weigh::factor(greedy ? 1.f : T_in);
+  const float T = Weigh::inside(greedy ? 1.f : T_in);
+  const float2 c_log2e = Weigh::factor(T);
   // entries that are listed, at least: k, or as many as top-p's border is hoped among
   const int want = greedy ? 0 : has_k ? (k_in <= kMostListed ? k_in : 0) : has_p ? kHopedMost : 0;
   if (has_min && threadIdx.x == 0) {
-    const double d = static_cast<double>(T_in) * log(static_cast<double>(fminf(min_p, 1.f)));
+    const double d = static_cast<double>(T) * log(static_cast<double>(fminf(min_p, 1.f)));
     const float a = static_cast<float>(d);
     sh.min_log = make_float2(a, static_cast<float>(d - static_cast<double>(a)));
   }
@@ -603,12 +608,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
   Weigh weigh;
   weigh.set(m, c_log2e, lane);
   u64 total = 0ull;
-  // min-p: the least float that is not below m + T ln(min_p)
+  // min-p: the least float that is not below m + T ln(min_p). That is finite or, where T
+  // is infinite (all weights are 1) or the sum passes the lowest number, keeps all.
   float least = -FLT_MAX;
-  if (has_min) {
+  if (has_min && !isinf(T)) {
     const float a = sh.min_log.x, t = __fadd_rn(m, a), b = __fsub_rn(t, m);   // t + e = m + a
     const float e = __fadd_rn(__fsub_rn(m, __fsub_rn(t, b)), __fsub_rn(a, b));
-    least = fminf(__fadd_ru(t, __fadd_rn(e, sh.min_log.y)), m);
+    if (t >= -FLT_MAX) least = fminf(__fadd_ru(t, __fadd_rn(e, sh.min_log.y)), m);
   }
 
   // A sum over the cluster of one value a warp: what lies before this warp, and all.
@@ -849,7 +855,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawAr
   } else {
     bool found = false;                // the border, through the list
     u64 Z = 1ull << kOne;              // the weight that top-p takes a part of, or less
-    // where no float lies below m (the lowest number), what has no weight cannot be raised to one
+    // where no float below m is without a weight (the lowest number, an infinite
+    // temperature), what has no weight cannot be raised to one
     const bool sums = weigh.low > -INFINITY, listed = want > 0 && sums && !(has_p && !has_k && looks_flat(m, upo, flo, weigh.scale(), p_in, V));
     if (listed) {
       // -------------------------------------------------------------- few candidates

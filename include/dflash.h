@@ -664,7 +664,8 @@ dflash_status dflash_attention_tree_paged(const dflash_heads* heads, const void*
  *   tokens[n] = the first v with w_0 + .. + w_v > u[n] * (sum), over those that stay
  * temperature, top_p, min_p, u: device fp32 [N], top_k: device int32 [N]; each
  *   but u may be NULL: 1, off, off, off. temperature 0 takes the largest entry
- *   (the lowest index on ties). top_k < 1, top_p >= 1 (or NaN) and min_p <= 0
+ *   (the lowest index on ties), an infinite one gives all the same weight, others
+ *   count as within 2^-100 .. 2^100. top_k < 1, top_p >= 1 (or NaN) and min_p <= 0
  *   (or NaN) are off; min_p above 1 counts as 1; u is taken in [0, 1).
  * tokens: device int32 [N] with u, or both NULL; probs: device fp32 [N, V] or
  *   NULL (dflash_verify_probs takes it for target_probs); one of the two. The

@@ -341,3 +341,53 @@ def test_equal_entries_at_temperatures_whose_factor_lies_farthest_off(dfl, T, V)
         k = int(V * p[n % 3])
         assert (pr[n, :k] > 0).all() and not pr[n, k:].any(), (n, vals[n // 3], p[n % 3], (pr[n] > 0).sum(), k)
         assert tok[n] == int(k * float(np.float32(0.999)))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("T", [1e30, 1e38, 2e38, 3e38, float("inf")])
+def test_min_p_at_very_high_temperatures(dfl, T, dtype):
+    """Nearly even weights, which no min-p below 1 parts: T ln(min_p) passes fp32's range."""
+    V, ms = 3001, [1e-45, 1e-6, 0.05, 0.999]
+    x = logits(2 * len(ms), V, dtype, 97, "normal")
+    x[1, ::3] = -float("inf")
+    N = x.shape[0]
+    u = [float(np.float32(v)) for v in np.linspace(0.013, 0.987, N)]
+    check(dfl, x, u, T=[T] * N, m=ms * 2)
+    check(dfl, x, u, T=[T] * N, m=ms * 2, k=[7, 40, 1700, 2000, 0, 3000, 1, 300])
+    # min-p of 1: entries as large as the largest one, and all finite ones where the temperature is infinite
+    x[:, 11] = x[:, 2000] = x.amax(1)
+    tok, pr, st = run(dfl, x, u, T=[T] * N, m=[1.0] * N)
+    f = x.double().cpu().numpy()
+    on = f > -np.inf if T == float("inf") else f == f.max(1, keepdims=True)
+    assert st == 0 and ((pr > 0) == on).all()
+    assert (np.abs(pr - on / on.sum(1, keepdims=True)) <= 2.0 ** -22 * 1.01 * on).all()   # even weights
+    for n in range(N):
+        assert on[n, tok[n]] and on[n, :tok[n] + 1].sum() == np.floor(on[n].sum() * u[n]) + 1
+
+
+def test_an_infinite_temperature_is_even_whatever_the_entries(dfl):
+    V, big = 2003, torch.finfo(F32).max
+    x = logits(6, V, F32, 101, "normal") * 1e37
+    x[0, ::2] = -big
+    x[0, 1::2] = big
+    x[1, :] = -big
+    x[2, 5] = float("inf")
+    x[3, ::7] = float("nan")
+    x[4, 9:] = -float("inf")
+    for s in (dict(), dict(k=[30] * 6), dict(k=[1500] * 6, p=[0.71] * 6), dict(p=[0.3] * 6, m=[0.5] * 6)):
+        check(dfl, x, [0.0, 0.1, 0.37, 0.613, 0.9, 0.999], T=[float("inf")] * 6, **s)
+
+
+def test_temperatures_beyond_the_range_count_as_its_ends(dfl):
+    V = 1009
+    for T, end in ((1e38, 2.0 ** 100), (3e38, 2.0 ** 100), (1e-38, 2.0 ** -100), (1e-45, 2.0 ** -100)):
+        x = logits(4, V, F32, 103, "normal") * (1e30 if T > 1 else 1e-30)
+        u = uniforms(4, 104)
+        for s in (dict(), dict(m=[1e-20, 0.05, 0.9, 1.0]), dict(p=[0.8] * 4)):
+            got, want = run(dfl, x, u, T=[T] * 4, **s), run(dfl, x, u, T=[end] * 4, **s)
+            assert got[0] == want[0] and np.array_equal(got[1], want[1]) and got[2] == want[2] == 0
+            assert (want[1] > 0).sum() > 4 or "m" in s
+    # a border below the lowest number: what lies one step under the largest entry has a weight of exp(-16)
+    x = torch.full((1, V), torch.finfo(F32).min, device="cuda")
+    x[0, 5] = float(np.nextafter(np.float32(torch.finfo(F32).min), np.float32(0)))
+    check(dfl, x, [0.99999], T=[2.0 ** 100], m=[1e-12])
