@@ -221,8 +221,11 @@ dflash_status dflash_attention_tree_paged(const dflash_heads* h, const void* q, 
                                           int layer, const dflash_kv_pages* pages, const uint32_t* mask,
                                           int mask_words, float scale, void* out, long long ld_o, int32_t* dev_status,
                                           void* ws, size_t ws_bytes, dflash_trace* trace, dflash_stream_t stream) {
-  if (mask_words < 1 || (mask == nullptr && T > 0 && B > 0)) return DFLASH_ERR_INVALID_ARG;
-  if (mask_words > INT32_MAX / 32) return DFLASH_ERR_TOO_LARGE;
+  if (mask_words < 0) return DFLASH_ERR_INVALID_ARG;
+  if (T > 0 && B > 0) {   // a batch of none has a mask of no words
+    if (mask_words < 1 || mask == nullptr) return DFLASH_ERR_INVALID_ARG;
+    if (mask_words > INT32_MAX / 32) return DFLASH_ERR_TOO_LARGE;
+  }
   return attention_chunk(h, q, ld_q, cu_rows, ctx_len, B, T, max_rows, max_ctx_hint, layer, pages, 0, scale, mask,
                          mask_words, out, ld_o, dev_status, ws, ws_bytes, trace, stream);
 }

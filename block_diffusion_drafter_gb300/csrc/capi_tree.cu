@@ -46,9 +46,9 @@ extern "C" {
 dflash_status dflash_tree_masks(const int32_t* parents, const int32_t* cu_rows, const int32_t* ctx_len, int B, int T,
                                 int mask_words, uint32_t* mask, int32_t* positions, int32_t* dev_status,
                                 dflash_trace* trace, dflash_stream_t stream) {
-  if (T < 0 || B < 0 || mask_words < 1) return DFLASH_ERR_INVALID_ARG;
-  if (T == 0 || B == 0) return DFLASH_OK;
-  if (parents == nullptr || cu_rows == nullptr || mask == nullptr || dev_status == nullptr ||
+  if (T < 0 || B < 0 || mask_words < 0) return DFLASH_ERR_INVALID_ARG;
+  if (T == 0 || B == 0) return DFLASH_OK;   // a mask of no words, too
+  if (mask_words < 1 || parents == nullptr || cu_rows == nullptr || mask == nullptr || dev_status == nullptr ||
       (positions != nullptr && ctx_len == nullptr) || !trace_ok(trace))
     return DFLASH_ERR_INVALID_ARG;
   if (T > INT32_MAX - 1024 || mask_words > INT32_MAX / 32) return DFLASH_ERR_TOO_LARGE;

@@ -631,8 +631,8 @@ dflash_status dflash_verify_probs(const dflash_config* cfg, const void* target_p
  *   written. positions: device [T], or NULL (ctx_len may then be NULL).
  * A parent that is not below its node counts as none, and a node from
  *   32 * mask_words on has no bit of its own; both set DFLASH_ERR_INVALID_ARG in
- *   dev_status. mask_words < 2^26, else DFLASH_ERR_TOO_LARGE. T == 0 or B == 0
- *   launches nothing. */
+ *   dev_status. 1 <= mask_words < 2^26, above it DFLASH_ERR_TOO_LARGE. T == 0 or
+ *   B == 0 launches nothing, whatever mask_words >= 0. */
 dflash_status dflash_tree_masks(const int32_t* parents, const int32_t* cu_rows, const int32_t* ctx_len, int B,
                                 int T, int mask_words, uint32_t* mask, int32_t* positions, int32_t* dev_status,
                                 dflash_trace* trace, dflash_stream_t stream);
@@ -642,9 +642,10 @@ dflash_status dflash_tree_masks(const int32_t* parents, const int32_t* cu_rows, 
  * bit j of mask[t] is set (j below the sequence's rows; bits behind them and
  * keys behind 32 * mask_words are not seen). Any mask is allowed, not only
  * those of trees; a row that sees no key gives zeros. mask: device
- * [T, mask_words], 1 <= mask_words < 2^26. Other arguments, workspace and errors
- * as there; key and value rows below ctx_len[b] + n_b must be finite here too,
- * also those that no row's mask names (they are multiplied by a zero weight). */
+ * [T, mask_words], 1 <= mask_words < 2^26 (T == 0 or B == 0: any, 0 too). Other
+ * arguments, workspace and errors as there; key and value rows below
+ * ctx_len[b] + n_b must be finite here too, also those that no row's mask names
+ * (they are multiplied by a zero weight). */
 dflash_status dflash_attention_tree_paged(const dflash_heads* heads, const void* q, long long ld_q,
                                           const int32_t* cu_rows, const int32_t* ctx_len, int B, int T,
                                           int max_rows, int max_ctx_hint, int layer,

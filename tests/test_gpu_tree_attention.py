@@ -235,3 +235,14 @@ def test_bad_pages_and_padded_batches(dfl, shape):
     s.qbuf[s.T + 1::2] = float("inf")
     s.run()
     s.check(rows=6)
+
+
+def test_a_step_without_nodes(dfl):
+    heads, none = dfl.make_heads(1, 8, 2, 128), torch.zeros((0, 8, 128), dtype=BF, device="cuda")
+    pool, st = torch.zeros((1, 3, 2, 128, 128), dtype=BF, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    mask = torch.zeros((0, 0), dtype=torch.int32, device="cuda")
+    dfl.dflash_tree_masks(ints([]), ints([0, 0]), ints([5]), mask, ints([]), st)
+    dfl.dflash_attention_tree_paged(heads, none, ints([0, 0]), ints([5]), 0, 5, 0, dfl.KvPages(pool, pool.clone(), ints([[0, 1]])), mask,
+                                    none.clone(), st, dfl.ChunkWorkspace(heads))
+    torch.cuda.synchronize()
+    assert int(st) == 0

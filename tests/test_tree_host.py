@@ -192,6 +192,32 @@ def test_wide_masks_and_overlapping_rows_are_refused(lib, heads):
             assert call not in (lib.ERR_INVALID_ARG, lib.ERR_ALIGN, lib.OK)
 
 
+def test_an_empty_batch_needs_no_mask(lib, heads):
+    """A step without any node: its mask is [0, 0]. Nothing is launched."""
+    call, tree = lib.load().dflash_tree_masks, lib.load().dflash_attention_tree_paged
+    for B, T in ((0, 0), (2, 0), (0, 3)):
+        for words in (0, 1, 1 << 26):
+            assert call(None, None, None, B, T, words, None, None, None, None, None) == lib.OK, (B, T, words)
+            assert tree(ref(heads), None, 0, None, None, B, T, 0, 0, 0, None, None, words, 0.0, None, 0, None, None, 0, None, None) == lib.OK
+        for words in (-1, -2 ** 31):
+            assert call(FAKE, FAKE, FAKE, B, T, words, FAKE, None, FAKE, None, None) == lib.ERR_INVALID_ARG
+    assert call(FAKE, FAKE, FAKE, -1, 0, 0, FAKE, None, FAKE, None, None) == lib.ERR_INVALID_ARG
+    assert tree(ref(heads), None, 0, None, None, 0, 0, 0, 0, 2, None, None, 0, 0.0, None, 0, None, None, 0, None, None) == lib.ERR_INVALID_ARG
+    assert tree(None, None, 0, None, None, 0, 0, 0, 0, 0, None, None, 0, 0.0, None, 0, None, None, 0, None, None) == lib.ERR_INVALID_ARG
+    if torch.cuda.is_available():
+        return          # the binding wants its operands on the device then (tests/test_gpu_tree_attention.py)
+    one = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    lib.dflash_tree_masks(one(0), one(3), one(2), one(0, 0), one(0), one(1))
+    lib.dflash_tree_masks(one(0), one(1), None, one(0, 0), None, one(1))
+    pool, q = torch.zeros((2, 4, 2, 128, 128), dtype=torch.bfloat16), torch.zeros((0, 8, 128), dtype=torch.bfloat16)
+
+    class NoScratch:
+        ptr, nbytes = None, 0
+
+    lib.dflash_attention_tree_paged(heads, q, one(3), one(2), 0, 0, 0, lib.KvPages(pool, pool.clone(), one(2, 2)), one(0, 0), q.clone(),
+                                    one(1), NoScratch())
+
+
 def test_shaped_distributions_by_plain_counting():
     r = np.random.default_rng(0)
     for _ in range(200):
