@@ -155,7 +155,8 @@ dflash_status dflash_pages_reserve(const dflash_kv_pages* pages, int32_t* refs, 
   if (B < 0) return DFLASH_ERR_INVALID_ARG;
   if (B == 0) return DFLASH_OK;
   if (want_len == nullptr || dev_status == nullptr || !trace_ok(trace)) return DFLASH_ERR_INVALID_ARG;
-  if (B > kMaxReserve) return DFLASH_ERR_TOO_LARGE;
+  // missing entries are summed in 32 bits
+  if (B > kMaxReserve || static_cast<long long>(B) * pages->pages_per_seq > INT32_MAX) return DFLASH_ERR_TOO_LARGE;
   if ((st = check_arch()) != DFLASH_OK) return st;
   PagesArgs a = book_args(pages, refs, dev_status);
   a.len = want_len;

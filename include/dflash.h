@@ -726,7 +726,8 @@ dflash_status dflash_verify_tree(const dflash_heads* heads, const int32_t* token
  *   back into a page that it shares must not be written on there.
  * reserve: entries of sequence b that are -1 and belong to a position below
  *   want_len[b] get a free page each. Positions beyond the table and pages that
- *   are not there set DFLASH_ERR_CAPACITY; such entries stay -1. B <= 4096.
+ *   are not there set DFLASH_ERR_CAPACITY; such entries stay -1. B <= 4096, and
+ *   B * pages_per_seq < 2^31, else DFLASH_ERR_TOO_LARGE.
  * fork: for every pair i, sequence dst[i] becomes a copy of sequence src[i]:
  *   dst's pages are released, src's full pages are shared, the page that holds
  *   the rest of its ctx_len[src] positions is copied (those rows, every layer)

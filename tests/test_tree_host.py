@@ -218,6 +218,19 @@ def test_an_empty_batch_needs_no_mask(lib, heads):
                                     one(1), NoScratch())
 
 
+
+def test_reserve_refuses_tables_whose_entries_it_cannot_count(lib):
+    """Missing entries are summed over the batch in 32 bits."""
+    def reserve(B, per):
+        return lib.load().dflash_pages_reserve(ref(pages_of(lib, pages_per_seq=per)), FAKE, FAKE, B, FAKE, None, None)
+
+    assert reserve(4096, 1 << 19) == reserve(2049, 1 << 20) == reserve(4096, (1 << 24) - 1) == lib.ERR_TOO_LARGE
+    assert reserve(0, (1 << 24) - 1) == lib.OK
+    if not torch.cuda.is_available():   # nothing to refuse but the machine
+        for call in (reserve(4096, (1 << 19) - 1), reserve(2047, 1 << 20), reserve(128, (1 << 24) - 1)):
+            assert call not in (lib.ERR_INVALID_ARG, lib.ERR_TOO_LARGE, lib.OK)
+
+
 def test_shaped_distributions_by_plain_counting():
     r = np.random.default_rng(0)
     for _ in range(200):
