@@ -391,3 +391,47 @@ def test_temperatures_beyond_the_range_count_as_its_ends(dfl):
     x = torch.full((1, V), torch.finfo(F32).min, device="cuda")
     x[0, 5] = float(np.nextafter(np.float32(torch.finfo(F32).min), np.float32(0)))
     check(dfl, x, [0.99999], T=[2.0 ** 100], m=[1e-12])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("N,V", [(310, 151936), (10, 200003), (3, 1 << 19), (10, 1 << 19)])
+def test_nan_and_infinite_entries_of_rows_that_are_read_again(dfl, N, V, dtype):
+    """Rows too long for shared memory: every pass reads the entries as they came, NaN and infinities among them."""
+    r = np.random.default_rng(N + V)
+    x = logits(N, V, dtype, 107)
+    for n in range(N):
+        row, kind = x[n], n % 8
+        if kind in (2, 5):
+            row *= 0.01                                  # flat
+        if kind in (4, 7):
+            row.zero_()                                  # equal
+        if kind in (0, 4, 5):
+            row[int(r.integers(0, 7))::7] = float("nan")
+        if kind in (1, 7):
+            row[int(r.integers(0, V // 2)):int(r.integers(V // 2, V))] = float("nan")
+        if kind in (1, 2, 5):
+            row[3::5] = -float("inf")
+        if kind == 3:
+            row[int(r.integers(0, V))] = float("inf")
+        if kind == 6:
+            row[torch.tensor(r.integers(0, V, 50), device="cuda")] = float("inf")
+        if kind == 0 and n % 16 == 8:
+            row.fill_(float("nan"))
+    s = dict(T=r.choice([0.0, 0.7, 1.0, 1.0, 1.3], N).tolist(), k=[int(v) for v in r.choice([0, 0, 0, 20, 1300, 90000], N)],
+             p=r.choice([0.3, 0.77, 0.9999, 1.0], N).tolist(), m=r.choice([0.0, 0.0, 0.05], N).tolist())
+    u = uniforms(N, 109)
+    tok, pr, st = run(dfl, x, u, **s)
+    alone, _, _ = run(dfl, x, u, **s, probs=False)
+    assert tok == alone
+    f32, big = lambda v: float(np.float32(v)), float(torch.finfo(dtype).max)  # noqa: E731
+    for n in sorted(set(list(range(min(N, 26))) + [N - 1, N - 2, N - 3])):
+        f = x[n].double().cpu().numpy()
+        want = tt.shape(np.where(f == np.inf, big, f), f32(s["T"][n]), s["k"][n], f32(s["p"][n]), f32(s["m"][n]))
+        if want is None:
+            assert tok[n] == 0 and not pr[n].any()
+            continue
+        assert ((pr[n] > 0) <= (want > 0)).all() and ((pr[n] == 0) <= (want < 2.0 ** -42)).all(), n
+        assert (np.abs(pr[n] - want) <= 2.0 ** -22 * 1.01 * want + 2.0 ** -43).all(), n
+        y = tt.draw(want, f32(u[n]))
+        assert tok[n] == y or abs(np.cumsum(want)[min(tok[n], y)] - f32(u[n])) <= 2.0 ** -27, (n, tok[n], y)
+    assert st == (dfl.ERR_INVALID_ARG if N > 8 else 0)

@@ -74,6 +74,29 @@ def test_what_is_no_tree_is_reported(dfl):
         assert pos.tolist() == (7 + m.sum(1) - 1).tolist()
 
 
+@pytest.mark.parametrize("ns", [[(7 * i) % 5 for i in range(700)], [1] * 513, [2500, 3, 5000, 0, 40], [3] * 520 + [2300, 1, 9]],
+                         ids=["700", "513", "2500 and 5000 nodes", "a large one behind 520"])
+def test_masks_of_many_sequences_and_of_large_ones(dfl, ns):
+    """Offsets and parents that a block does not keep in shared memory."""
+    r = np.random.default_rng(sum(ns))
+    trees = [tree(r, n, 300.0 if n > 1000 else 3.0) if n else [] for n in ns]     # large ones: few generations
+    T, W = sum(ns), (max(ns) + 31) // 32
+    cu, ctx = ints(np.cumsum([0] + ns).tolist()), ints([3 * i for i in range(len(ns))])
+    mask = torch.full((T + 2, W), 77, dtype=torch.int32, device="cuda")
+    pos, st = torch.full((T + 2,), 77, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    dfl.dflash_tree_masks(ints([p for t in trees for p in t]), cu, ctx, mask[:T], pos[:T], st)
+    torch.cuda.synchronize()
+    assert int(st) == 0 and (mask[T:] == 77).all() and (pos[T:] == 77).all()
+    got, at, places = mask.cpu().numpy(), 0, pos.tolist()
+    for b, t in enumerate(trees):
+        if not t:
+            continue
+        m = tt.sees(t)
+        assert np.array_equal(got[at:at + len(t)], tt.bits(m, W)), b
+        assert places[at:at + len(t)] == (3 * b + m.sum(1) - 1).tolist()
+        at += len(t)
+
+
 # ------------------------------------------------------------------ attention
 class TreeScene(Scene):
     def __init__(self, dfl, dtype, hq, hkv, dh, ns, ctxs, kind="tree", words=None, **kw):
