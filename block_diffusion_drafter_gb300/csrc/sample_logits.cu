@@ -50,7 +50,14 @@ constexpr int kMaxParts = 16;
 constexpr int kCountBins = 2048, kMassBins = 1024;
 constexpr int kHistInts = 3 * kMassBins;   // of weights: counts, lower and upper words
 constexpr int kList = 2048;          // candidates of a CTA, and of a row: 32 KB
-constexpr int kMostListed = 1280;    // top-k borders that the list is made for
+// top-k borders that the list is made for; larger ones by histograms. (Temperature 1, list
+// against histograms, us, without / with top-p 0.95. k = 900: 1 row bf16 34.2 / 31.3 against
+// 33.2 / 56.5, 64 rows f32 59 / 57 and 61 / 102, 272 f32 140 / 134 and 186 / 323, 1024 bf16
+// 273 / 260 and 555 / 1366. k = 1270: 39.6 / 32.1 and 33.4 / 56.5, 68 / 60 and 63 / 108,
+// 159 / 140 and 195 / 346, 315 / 328 and 581 / 1427. k = 1500, where the list begins to
+// overflow: 40 / 43 and 34 / 57, 72 / 120 and 61 / 111, 187 / 230 and 201 / 359, 399 / 455
+// and 593 / 1432.)
+constexpr int kMostListed = 1280;
 // Candidates among which top-p's border is looked for, and then. (1280 instead of 640: 16
 // / 64 rows bf16 at temperature 0.7 46 / 60 instead of 35 / 52 us, 1024 rows 315 instead of
 // 293; 272 rows f32, where one row's border decides, 143 instead of 161.)
@@ -375,6 +382,9 @@ struct Shared {
   float2 min_log;                  // T ln(min_p), in two floats
 };
 
+// Two CTAs an SM leave 64 registers a thread, and all ways share them: the stack frame is 40
+// bytes for f32 (112 bytes of spill stores, 140 of loads over the whole kernel), 56 for bf16
+// (310, 424). What keeps more values alive pays here first.
 template <typename TT>
 __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const DrawArgs p, const int parts, const int rows) {
   using P = Pack<TT>;
